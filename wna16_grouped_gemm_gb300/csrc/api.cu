@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "../../include/wna16_moe.h"
+#include "block.h"
 #include "gemm.h"
 
 using namespace wna16;
@@ -492,6 +493,19 @@ int launch_plan(const GemmPlan& P, cudaStream_t s) {
 }
 
 }  // namespace
+
+int wna16::device_limits(int& sms, int& max_smem) {
+    DevInfo d;
+    if (int rc = device_info(d)) return rc;
+    sms = d.sms;
+    max_smem = d.max_smem;
+    return WNA16_OK;
+}
+
+int wna16::encode_tma_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[3],
+                         const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swz) {
+    return encode_3d(map, dtype, base, dims, strides, box, swz);
+}
 
 int wna16::set_error(int code, const char* fmt, ...) {
     va_list ap;
