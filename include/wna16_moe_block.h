@@ -109,9 +109,10 @@ WNA16_API int wna16_moe_route_scored(const void* logits, int64_t ld, const float
  * 32-bit integers for small batches; for larger ones fp32 sums of exact
  * products on the tensor cores, which are the same integers while every
  * partial sum stays below 2^24 (always for K <= 1024), and otherwise off by a
- * relative 2^-23 per 16 k at most.  Workspace (256-byte aligned, its first word
- * is the status word of wna16_moe_read_status): the size below, 0 for small
- * batches (workspace may then be NULL). */
+ * relative 2^-23 per 16 k at most.  Workspace (256-byte aligned): its first
+ * word is the status word of wna16_moe_read_status, the size is below (0 for
+ * small batches).  It may be NULL: the status word is then not readable; an
+ * output whose sums are missing after a device timeout is NaN either way. */
 WNA16_API int wna16_moe_linear_q8(const int8_t* xq, const float* x_scales, const int8_t* wq, const float* w_scales,
                                   const float* bias, const void* addend, int64_t T, int64_t K, int64_t N, int type,
                                   void* out, void* workspace, size_t workspace_bytes, void* stream);

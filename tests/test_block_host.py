@@ -127,7 +127,7 @@ def _linear(lib, *, xq=P[0], xs=P[1], wq=P[2], ws=P[3], bias=None, addend=None, 
     (dict(K=65552), UNS), (dict(T=1 << 24), UNS), (dict(N=1 << 24), UNS), (dict(xq=None), INV), (dict(wq=None), INV),
     (dict(xs=None), INV), (dict(ws=None), INV), (dict(xq=P[0] + 8), INV), (dict(wq=P[2] + 4), INV),
     (dict(xs=P[1] + 2), INV), (dict(bias=P[4] + 1), INV), (dict(addend=P[4] + 1), INV), (dict(out=None), INV),
-    (dict(out=P[5] + 1), INV), (dict(workspace=None), INV), (dict(workspace=P[6] + 16), INV), (dict(nbytes=100), SMALL),
+    (dict(out=P[5] + 1), INV), (dict(workspace=P[6] + 16), INV), (dict(nbytes=100), SMALL),
     (dict(out=P[0] + 4096), INV), (dict(out=P[2]), INV), (dict(addend=P[5] + 2), INV), (dict(workspace=P[2]), INV),
 ])
 def test_linear_refuses(lib, kw, code):
@@ -148,7 +148,7 @@ def test_empty_batches_do_nothing(lib):
 def test_linear_workspace_size(lib):
     size = lib.wna16_moe_linear_q8_workspace_size
     assert size(1, 4096, 4096) == 0                                   # small batches need none
-    assert size(2048, 4096, 4096) >= 2048 * 4096 * 2                  # the tokens in 16 bits
+    assert size(2048, 4096, 4096) >= 4                                # the status word
     assert size(2048, 4088, 4096) == 0 and size(-1, 64, 64) == 0      # refused sizes
 
 

@@ -240,7 +240,7 @@ def linear_q8(xq, x_scales, wq, w_scales, *, bias=None, addend=None, dtype=torch
     xq int8 [T, K], x_scales fp32 [T] or [T, 1], wq int8 [N, K], w_scales fp32
     [N] or [N, 1], bias fp32 [N], addend [T, N] of the output's type (out=addend
     adds in place).  workspace: uint8, at least linear_q8_workspace_size(T, K, N)
-    bytes (allocated when needed and not given)."""
+    bytes, holds the status word for read_status; may be left out."""
     _need(xq, torch.int8, "xq", 2)
     _need(wq, torch.int8, "wq", 2)
     _need(x_scales, torch.float32, "x_scales")
@@ -272,13 +272,13 @@ def linear_q8(xq, x_scales, wq, w_scales, *, bias=None, addend=None, dtype=torch
     out = _out(out, (T, N), dtype, "out", xq, stream)
     s = _stream(xq, stream)
     lib = _load()
-    if workspace is None:
-        need = lib.wna16_moe_linear_q8_workspace_size(T, K, N) if T > 0 and K > 0 and N > 0 else 0
-        if need:
-            workspace = _out(None, (need,), torch.uint8, "workspace", xq, stream)
-    else:
+    if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
         _same_device(xq, workspace, "workspace")
+        need = lib.wna16_moe_linear_q8_workspace_size(T, K, N)
+        if workspace.numel() < need:   # (an empty tensor has no address to refuse)
+            raise binding.Wna16Error(binding.ERR_WORKSPACE_TOO_SMALL,
+                                     f"workspace has {workspace.numel()} bytes, needs {need}")
     _check(lib.wna16_moe_linear_q8(
         xq.data_ptr(), x_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), None if bias is None else bias.data_ptr(),
         None if addend is None else addend.data_ptr(), T, K, N, _TYPES[dtype], out.data_ptr(),

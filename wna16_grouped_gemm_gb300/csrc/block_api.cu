@@ -132,7 +132,8 @@ int wna16_moe_add_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, i
     const Range ins[3] = {{x, extent(T, ldx, K, es), "x"},
                           {residual, residual ? extent(T, ldr, K, es) : 0, "residual"},
                           {weight, static_cast<size_t>(K) * size_of(weight_type), "weight"}};
-    const bool in_place = residual_out && ((residual_out == x && ldx == K) || (residual_out == residual && ldr == K));
+    // in place: the same rows at the same places
+    const bool in_place = (residual_out != x || ldx == K || T == 1) && (residual_out != residual || ldr == K || T == 1);
     if (int rc = check_overlap(outs, ins, in_place)) return rc;
     RowParams p;
     p.x = x;
@@ -315,12 +316,12 @@ int wna16_moe_linear_q8(const int8_t* xq, const float* x_scales, const int8_t* w
         if (int rc = check_pointer(addend, es, "addend")) return rc;
     if (int rc = check_pointer(out, es, "out")) return rc;
     const size_t need = linear_q8_workspace(T, K, N);
-    if (need) {
+    if (need && workspace) {
         if (int rc = check_pointer(workspace, 256, "workspace")) return rc;
         if (workspace_bytes < need)
             return set_error(WNA16_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     }
-    const Range outs[2] = {{out, static_cast<size_t>(T * N) * es, "out"}, {need ? workspace : nullptr, need, "workspace"}};
+    const Range outs[2] = {{out, static_cast<size_t>(T * N) * es, "out"}, {workspace, workspace ? need : 0, "workspace"}};
     const Range ins[6] = {{xq, static_cast<size_t>(T * K), "xq"},
                           {wq, static_cast<size_t>(N * K), "wq"},
                           {x_scales, static_cast<size_t>(T) * 4, "x_scales"},

@@ -13,16 +13,22 @@
 // tile_kernel (many tokens): bound by the tensor cores.  sm_103a has no 8-bit
 // integer kind of tcgen05.mma, but 8-bit integers are exact in fp16, and their
 // products and sums (below 2^24) exact in the fp32 accumulator, so the
-// codes run through kind::f16.  The weights are the M side: a block owns 128
-// output channels and one tile of tokens.
-//   convert kernel            xq -> fp16 in the workspace (rows padded with 0 to a multiple of 64 k)
-//   TMA producer (warp 0)     64-k stages: weight codes (128 x 64 bytes) and the token tile (fp16)
-//   converter warps (4..11)   thread = weight row: 64 codes -> fp16 -> tcgen05.st into a TMEM buffer
-//   MMA issuer (warp 1)       tcgen05.mma, A from TMEM, B from shared memory
-//   epilogue (warps 12..19)   tcgen05.ld, scales, bias, addend, store
-// The weights' fp16 form never passes through shared memory.
+// codes run through kind::f16.  A pair of CTAs (cta_group::2) owns 256 output
+// channels (the M side, 128 per CTA) and one tile of up to 256 tokens (half of
+// them in each CTA's shared memory):
+//   TMA producer (warp 0)      128-k stages: codes of the CTA's weight rows and tokens
+//   W converters (warps 4..11) thread = weight row: 64 codes -> fp16 -> TMEM (operand A)
+//   X converters (12..19)      thread = token: 64 codes -> fp16 -> shared memory (operand B)
+//   MMA issuer (warp 1 of the even CTA)   256 x nt x 64 per pair of operand buffers
+//   epilogue (warps 20..27)    tcgen05.ld, scales, bias, addend, store
+// Only codes cross the memory system, and the weights' fp16 form never passes
+// through shared memory.  When there are few tiles, 2 or 4 pairs form a cluster
+// that shares a tile's K and adds its sums through distributed shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "../../include/wna16_moe_block.h"
 #include "block.h"
@@ -148,46 +154,27 @@ __device__ __forceinline__ uint2 fp16x4_of(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-constexpr int kConvertThreads = 256;
-// x16[t][k] = xq[t][k], k < K; 0 for K <= k < Kp.  16 codes per thread and step; also clears the status word.
-__global__ void __launch_bounds__(kConvertThreads)
-    convert_kernel(const int8_t* __restrict__ xq, int64_t T, int K, int Kp, __half* __restrict__ x16, int* status) {
-    pdl_wait();
-    pdl_trigger();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *status = kStatusOk;
-    const int per_row = Kp / 16;
-    const int64_t total = T * per_row;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kConvertThreads + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * kConvertThreads) {
-        const int64_t t = i / per_row;
-        const int k = static_cast<int>(i - t * per_row) * 16;
-        uint4 c = make_uint4(0, 0, 0, 0);
-        if (k < K) c = __ldg(reinterpret_cast<const uint4*>(xq + t * K + k));
-        const uint2 a = fp16x4_of(c.x), b = fp16x4_of(c.y), d = fp16x4_of(c.z), e = fp16x4_of(c.w);
-        uint4* o = reinterpret_cast<uint4*>(x16 + t * Kp + k);
-        o[0] = make_uint4(a.x, a.y, b.x, b.y);
-        o[1] = make_uint4(d.x, d.y, e.x, e.y);
-    }
-}
-
-constexpr int kM = 128;            // weight rows per tile
-constexpr int kStageK = 64;        // k per stage and per TMEM buffer (32 columns)
-constexpr int kABufs = 8;
+constexpr int kM = 128;            // weight rows per CTA (256 per pair)
+constexpr int kStageK = 128;       // k per stage of codes: one 128-byte swizzle row
+constexpr int kHalfK = 64;         // k per converter set and stage: 32 TMEM columns, one 128-byte swizzle row of fp16
+constexpr int kStages = 3;
+constexpr int kBufs = 4;           // operand buffers, one stage each: 64 TMEM columns, two swizzle atoms of fp16
+constexpr int kMaxSplit = 4;
 constexpr int kProducer = 0, kIssuer = 1, kAlloc = 2;
-constexpr int kFirstConverter = 4, kConverters = 8;
-constexpr int kFirstEpilogue = kFirstConverter + kConverters, kEpilogues = 8;
+constexpr int kFirstW = 4, kFirstX = 12, kFirstEpilogue = 20;   // 8 warps each, in two sets of 4
+constexpr int kSet = 4, kEpilogues = 8;
 constexpr int kTileThreads = 32 * (kFirstEpilogue + kEpilogues);
 constexpr int kCols = 512;
-constexpr int kMaxStages = 8;
+constexpr uint32_t kACol = 256;    // TMEM: accumulator in columns 0..nt-1, operand buffers from here
+constexpr int kBars = 2 * kStages + 2 * kBufs + 3;
+constexpr int kMaxTokens = 256;    // tokens per tile
 
 struct TileParams {
     LinearParams p;
-    int nt = 0;            // tokens per tile
-    int nstage = 0;        // even: a stage's slot belongs to one set of converter warps
+    int nt = 0;            // tokens per tile, half of them in each CTA of the pair
     int kblocks = 0;       // stages over the whole K
     int n_tiles = 0, t_tiles = 0;
-    int ksplit = 1;
-    float* partial = nullptr;   // [ksplit][T][N] (ksplit > 1)
+    int ksplit = 1;        // pairs per cluster: each takes a part of K
     int* status = nullptr;
 };
 
@@ -199,32 +186,38 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const LinearParams& p = tp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nt = tp.nt, nstage = tp.nstage;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t leader = rank & ~1u, side = rank & 1u;
+    const int split = static_cast<int>(rank >> 1);
+    const int nt = tp.nt, xrows = nt / 2, ksplit = tp.ksplit;
     constexpr int w_bytes = kM * kStageK;
-    const int x_bytes = nt * kStageK * 2;
-    uint8_t* sX = smem;
-    uint8_t* sW = smem + nstage * x_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sW + nstage * w_bytes);
-    uint64_t* empty = full + kMaxStages;
-    uint64_t* afull = empty + kMaxStages;
-    uint64_t* aempty = afull + kABufs;
-    uint64_t* accfull = aempty + kABufs;
-    uint64_t* accempty = accfull + 1;
+    const int x_bytes = xrows * kStageK;
+    const int h_bytes = xrows * kStageK * 2;
+    uint8_t* sW = smem;
+    uint8_t* sX = sW + kStages * w_bytes;
+    uint8_t* sH = sX + kStages * x_bytes;      // the tokens' codes as fp16
+    float* sScale = reinterpret_cast<float*>(sH + kBufs * h_bytes);   // the tile's token scales
+    uint64_t* full = reinterpret_cast<uint64_t*>(sScale + kMaxTokens);
+    uint64_t* empty = full + kStages;
+    uint64_t* bfull = empty + kStages;         // the leader's: both CTAs' operands of a buffer are in place
+    uint64_t* bempty = bfull + kBufs;
+    uint64_t* accfull = bempty + kBufs;
+    uint64_t* accempty = accfull + 1;          // the leader's
     uint64_t* drain = accempty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < nstage; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kConverters / 2 + 1);   // its converter set's warps and the MMAs' commit
+            mbar_init(&empty[i], 4 * kSet);            // both sets of both kinds of converters
         }
-        for (int i = 0; i < kABufs; ++i) {
-            mbar_init(&afull[i], kConverters / 2);
-            mbar_init(&aempty[i], 1);
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(&bfull[i], 2 * 4 * kSet);        // the converters of both CTAs
+            mbar_init(&bempty[i], 1);
         }
         mbar_init(accfull, 1);
-        mbar_init(accempty, kEpilogues);
+        mbar_init(accempty, 2 * kEpilogues);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -232,29 +225,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tma_prefetch_desc(&tm_x);
     }
     if (warp == kAlloc) {
-        tmem_alloc(tmem_slot, kCols);
-        tmem_relinquish();
+        tmem_alloc_pair(tmem_slot, kCols);
+        tmem_relinquish_pair();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                                    // the other CTA's barriers exist
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const uint32_t a_col = 512 - kABufs * (kStageK / 2);   // accumulator below, buffers above
     pdl_wait();
     pdl_trigger();
     int* status = tp.status;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = kStatusOk;   // any timeout is seconds away
 
-    const int items = tp.n_tiles * tp.t_tiles * tp.ksplit;
-    // item -> (token tile, K split, weight tile), weight tiles fastest
-    auto decode = [&](int v, int& n0, int& t0, int& kb0, int& kb1) {
-        const int s = v / tp.n_tiles;
-        n0 = (v - s * tp.n_tiles) * kM;
-        const int split = s % tp.ksplit;
-        t0 = (s / tp.ksplit) * nt;
-        kb0 = static_cast<int>(static_cast<int64_t>(tp.kblocks) * split / tp.ksplit);
-        kb1 = static_cast<int>(static_cast<int64_t>(tp.kblocks) * (split + 1) / tp.ksplit);
-        return split;
-    };
+    const int items = tp.n_tiles * tp.t_tiles;
+    const int first = static_cast<int>(blockIdx.x) / (2 * ksplit);
+    const int stride = static_cast<int>(gridDim.x) / (2 * ksplit);
+    const int kb0 = static_cast<int>(static_cast<int64_t>(tp.kblocks) * split / ksplit);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(tp.kblocks) * (split + 1) / ksplit);
+    // item -> (token tile, weight tile), weight tiles fastest
+    auto w_row = [&](int v) { return (v % tp.n_tiles) * (2 * kM) + static_cast<int>(side) * kM; };
+    auto t_row = [&](int v) { return (v / tp.n_tiles) * nt; };
 
     if (warp == kProducer) {
         if (lane == 0) {
@@ -262,26 +253,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const uint32_t tx = static_cast<uint32_t>(w_bytes + x_bytes);
             uint32_t kc = 0;   // stages so far
             bool ok = true;
-            for (int v = blockIdx.x; v < items && ok; v += gridDim.x) {
-                int n0, t0, kb0, kb1;
-                decode(v, n0, t0, kb0, kb1);
+            for (int v = first; v < items && ok; v += stride) {
+                const int n0 = w_row(v), t0 = t_row(v) + static_cast<int>(side) * xrows;
                 for (int kb = kb0; kb < kb1; ++kb, ++kc) {
-                    const int slot = kc % nstage;
-                    const uint32_t ph = (kc / nstage) & 1u;
-                    if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag, status)) {
+                    const int slot = kc % kStages;
+                    if (!mbar_wait(&empty[slot], ((kc / kStages) & 1u) ^ 1u, abort_flag, status)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(&full[slot], tx);
                     tma_load_3d(sW + slot * w_bytes, &tm_w, &full[slot], kb * kStageK, n0, 0, pol);
-                    tma_load_3d(sX + slot * x_bytes, &tm_x, &full[slot], 0, t0, kb, pol);
+                    tma_load_3d(sX + slot * x_bytes, &tm_x, &full[slot], kb * kStageK, t0, 0, pol);
                 }
             }
             // no copy may be in flight when the block ends: wait for the last issue of every slot
-            for (uint32_t c = kc > static_cast<uint32_t>(nstage) ? kc - nstage : 0; c < kc; ++c) {
-                const uint32_t a = smem_u32(&full[c % nstage]);
+            for (uint32_t c = kc > kStages ? kc - kStages : 0; c < kc; ++c) {
+                const uint32_t a = smem_u32(&full[c % kStages]);
                 const uint64_t b = globaltimer_ns();
-                while (!mbar_try_wait(a, (c / nstage) & 1u)) {
+                while (!mbar_try_wait(a, (c / kStages) & 1u)) {
                     if (globaltimer_ns() - b > kWaitLimitNs) {
                         atomicExch(status, kStatusTimeout);
                         break;
@@ -290,204 +279,265 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
     } else if (warp == kIssuer) {
-        auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-            bool r = true;
-            if (lane == 0) r = mbar_wait(bar, parity, abort_flag, status);
-            return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
-        };
-        // f16 A and B, f32 D, both K-major
-        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>(kM >> 4) << 24);
-        uint32_t kc = 0, it = 0;
-        bool ok = true, issued = false;
-        for (int v = blockIdx.x; v < items && ok; v += gridDim.x, ++it) {
-            int n0, t0, kb0, kb1;
-            decode(v, n0, t0, kb0, kb1);
-            if (!warp_wait(accempty, (it & 1u) ^ 1u)) {
-                ok = false;
-                break;
-            }
-            for (int kb = kb0; kb < kb1; ++kb, ++kc) {
-                const int slot = kc % nstage;
-                const int ab = kc % kABufs;
-                if (!warp_wait(&full[slot], (kc / nstage) & 1u) || !warp_wait(&afull[ab], (kc / kABufs) & 1u)) {
+        if (side == 0) {
+            auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+                bool r = true;
+                if (lane == 0) r = mbar_wait(bar, parity, abort_flag, status);
+                return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+            };
+            // f16 A and B, f32 D, both K-major, 256 x nt
+            const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>((2 * kM) >> 4) << 24);
+            const uint16_t mask = static_cast<uint16_t>(3u << rank);
+            uint32_t kc = 0, it = 0;
+            bool ok = true, issued = false;
+            for (int v = first; v < items && ok; v += stride, ++it) {
+                if (!warp_wait(accempty, (it & 1u) ^ 1u)) {
                     ok = false;
                     break;
                 }
-                const uint32_t b_lo = smem_desc_sw128_lo(smem_u32(sX + slot * x_bytes));
-                const uint32_t a0 = tmem + a_col + ab * (kStageK / 2);
-                if (elect_one(status)) {
-                    tc_fence_after();
+                for (int kb = kb0; kb < kb1; ++kb, ++kc) {
+                    const int b = kc % kBufs;
+                    if (!warp_wait(&bfull[b], (kc / kBufs) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t b_lo = smem_desc_sw128_lo(smem_u32(sH + b * h_bytes));
+                    const uint32_t atom = static_cast<uint32_t>(h_bytes) >> 5;   // 64 k of the tokens, >> 4
+                    const uint32_t a0 = tmem + kACol + b * (kStageK / 2);
+                    if (elect_one(status)) {
+                        tc_fence_after();
 #pragma unroll
-                    for (int k16 = 0; k16 < kStageK / 16; ++k16)
-                        tc_mma_ts_lohi(tmem, a0 + k16 * 8, b_lo + k16 * 2, kSmemDescSw128Hi, idesc,
-                                       kb > kb0 || k16 > 0 ? 1u : 0u);
-                    tc_commit(&aempty[ab]);
-                    tc_commit(&empty[slot]);
-                    if (kb + 1 == kb1) tc_commit(accfull);
+                        for (int k16 = 0; k16 < kStageK / 16; ++k16)
+                            tc_mma_ts_pair(tmem, a0 + k16 * 8, b_lo + (k16 >> 2) * atom + (k16 & 3) * 2,
+                                           kSmemDescSw128Hi, idesc, kb > kb0 || k16 > 0 ? 1u : 0u);
+                        tc_commit_pair(&bempty[b], mask);
+                        if (kb + 1 == kb1) tc_commit_pair(accfull, mask);
+                    }
+                    __syncwarp();
+                    issued = true;
+                }
+            }
+            if (issued && (!ok || *abort_flag)) {   // no MMA may still run when TMEM is released
+                if (elect_one(status)) {
+                    tc_commit_pair(drain, static_cast<uint16_t>(1u << rank));
+                    const uint32_t a = smem_u32(drain);
+                    const uint64_t b = globaltimer_ns();
+                    while (!mbar_try_wait(a, 0)) {
+                        if (globaltimer_ns() - b > kWaitLimitNs) break;
+                    }
                 }
                 __syncwarp();
-                issued = true;
             }
         }
-        if (issued && (!ok || *abort_flag)) {   // no MMA may still run when TMEM is released
-            if (elect_one(status)) {
-                tc_commit(drain);
-                const uint32_t a = smem_u32(drain);
-                const uint64_t b = globaltimer_ns();
-                while (!mbar_try_wait(a, 0)) {
-                    if (globaltimer_ns() - b > kWaitLimitNs) break;
-                }
-            }
-            __syncwarp();
-        }
-    } else if (warp >= kFirstConverter && warp < kFirstConverter + kConverters) {
-        // Two sets of four warps (one warp per TMEM lane quarter) take the stages in
-        // turn.  nstage and kABufs are even, so a slot or buffer always
-        // belongs to the same set, which waits for each of its phases in order.
-        const uint32_t set = static_cast<uint32_t>(warp - kFirstConverter) >> 2;
-        const int quarter = warp & 3;
+    } else if (warp >= kFirstW && warp < kFirstEpilogue) {
+        // Converters.  Set s of either kind takes the k half s of every stage.
+        const bool is_x = warp >= kFirstX;
+        const uint32_t set = static_cast<uint32_t>(warp - (is_x ? kFirstX : kFirstW)) / kSet;
+        const int quarter = warp & 3;                     // TMEM lanes 32 * quarter ..
         const int row = quarter * 32 + lane;
-        const uint32_t xr = (static_cast<uint32_t>(row) >> 1) & 3u;   // 64-byte swizzle
-        const uint32_t abase = tmem + a_col + (static_cast<uint32_t>(quarter * 32) << 16);
-        uint32_t kc = 0;
+        const uint32_t xr = static_cast<uint32_t>(row) & 7u;   // 128-byte swizzle
+        const uint32_t abase = tmem + kACol + (static_cast<uint32_t>(quarter * 32) << 16);
+        const bool live = !is_x || row < xrows;
+        const uint8_t* codes = is_x ? sX + row * kStageK : sW + row * kStageK;
+        const int code_bytes = is_x ? x_bytes : w_bytes;
+        const uint32_t bfull0 = map_shared(smem_u32(bfull), leader);
+        uint32_t kc = 0;   // stages so far
         bool ok = true;
-        for (int v = blockIdx.x; v < items && ok; v += gridDim.x) {
-            int n0, t0, kb0, kb1;
-            decode(v, n0, t0, kb0, kb1);
+        for (int v = first; v < items && ok; v += stride) {
             for (int kb = kb0; kb < kb1; ++kb, ++kc) {
-                if ((kc & 1u) != set) continue;
-                const int slot = kc % nstage;
-                const int ab = kc % kABufs;
-                const uint32_t aph = ((kc / kABufs) & 1u) ^ 1u;
-                if (!mbar_wait(&full[slot], (kc / nstage) & 1u, abort_flag, status)) {
+                const int slot = kc % kStages;
+                const int b = kc % kBufs;
+                const uint32_t bph = ((kc / kBufs) & 1u) ^ 1u;
+                if (!mbar_wait(&full[slot], (kc / kStages) & 1u, abort_flag, status)) {
                     ok = false;
                     break;
                 }
-                const bool ready = mbar_test_wait(smem_u32(&aempty[ab]), aph);
-                const uint8_t* src = sW + slot * w_bytes + row * kStageK;
+                const bool ready = mbar_test_wait(smem_u32(&bempty[b]), bph);
                 uint32_t a[32];
+                if (live) {
+                    const uint8_t* src = codes + slot * code_bytes;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(src + ((static_cast<uint32_t>(c) ^ xr) << 4));
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(src + (((4 * set + c) ^ xr) << 4));
+                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint2 h = fp16x4_of(ww[j]);
-                        a[c * 8 + j * 2] = h.x;
-                        a[c * 8 + j * 2 + 1] = h.y;
+                        for (int j = 0; j < 4; ++j) {
+                            const uint2 h = fp16x4_of(ww[j]);
+                            a[c * 8 + j * 2] = h.x;
+                            a[c * 8 + j * 2 + 1] = h.y;
+                        }
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[slot]);   // the codes are in registers
-                if (!ready && !mbar_wait(&aempty[ab], aph, abort_flag, status)) {
+                if (!ready && !mbar_wait(&bempty[b], bph, abort_flag, status)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                tc_st_32x32b_x32(abase + ab * (kStageK / 2), a);
-                tc_wait_st();
-                tc_fence_before();
+                if (is_x) {
+                    if (live) {
+                        uint8_t* dst = sH + b * h_bytes + set * (h_bytes / 2) + row * (kHalfK * 2);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(dst + ((static_cast<uint32_t>(j) ^ xr) << 4)) =
+                                make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+                    }
+                    fence_proxy_async_shared();
+                } else {
+                    tc_fence_after();
+                    tc_st_32x32b_x32(abase + b * (kStageK / 2) + set * (kHalfK / 2), a);
+                    tc_wait_st();
+                    tc_fence_before();
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&afull[ab]);
+                if (lane == 0) mbar_arrive_cluster(bfull0 + b * 8);
             }
         }
-    } else if (warp >= kFirstEpilogue) {
-        // two sets of four warps: the lower and the upper half of the tile's tokens
-        const int half = (warp - kFirstEpilogue) >> 2;
-        const int quarter = warp & 3;
-        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        uint32_t it = 0;
-        for (int v = blockIdx.x; v < items; v += gridDim.x, ++it) {
-            int n0, t0, kb0, kb1;
-            const int split = decode(v, n0, t0, kb0, kb1);
-            if (!mbar_wait_bounded(accfull, it & 1u, abort_flag, status, true)) break;
-            tc_fence_after();
-            const int n = n0 + quarter * 32 + lane;
-            const bool live = n < p.N;
-            const float ws = live && tp.ksplit == 1 ? __ldg(p.ws + n) : 1.0f;
-            const float bias = live && tp.ksplit == 1 && p.bias ? __ldg(p.bias + n) : 0.0f;
-            const int j1 = (half + 1) * (nt / 2);
-            for (int j = half * (nt / 2); j < j1; j += 16) {
-                uint32_t d[16];
-                tc_ld_32x32b_x16(tmem + lane_base + static_cast<uint32_t>(j), d);
-                tc_wait_ld();
+    }
+
+    // Epilogue: thread = weight row; two sets of four warps, the lower and the
+    // upper half of the tile's tokens.
+    const int eset = (warp - kFirstEpilogue) / kSet;
+    const int quarter = warp & 3;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    bool done = true;   // false: a wait gave up; what is missing is written as NaN
+    const int row = quarter * 32 + lane;
+    // 16 sums of this thread's output channel n, tokens t .. t + 15 of which the tile has `count`
+    auto emit = [&](int n, float ws, float bias, int t, int count, const float* scale, const float (&sum)[16]) {
+        if (n >= p.N || count <= 0) return;
+        T* out = static_cast<T*>(p.out) + static_cast<int64_t>(t) * p.N + n;
+        float r[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = t0 + j + i;
-                    if (t < p.T && live && j + i < j1) {
-                        const int64_t o = static_cast<int64_t>(t) * p.N + n;
-                        if (tp.ksplit > 1) {
-                            tp.partial[static_cast<int64_t>(split) * p.T * p.N + o] = __uint_as_float(d[i]);
-                        } else {
-                            float r = __uint_as_float(d[i]) * __ldg(p.xs + t) * ws;
-                            if (p.bias) r += bias;
-                            if (p.addend) r += to_f(static_cast<const T*>(p.addend)[o]);
-                            static_cast<T*>(p.out)[o] = from_f<T>(r);
-                        }
-                    }
-                }
+        for (int i = 0; i < 16; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(scale + i);
+            r[i] = fmaf(sum[i] * x.x, ws, bias);
+            r[i + 1] = fmaf(sum[i + 1] * x.y, ws, bias);
+            r[i + 2] = fmaf(sum[i + 2] * x.z, ws, bias);
+            r[i + 3] = fmaf(sum[i + 3] * x.w, ws, bias);
+        }
+        if (p.addend) {
+            const T* add = static_cast<const T*>(p.addend) + static_cast<int64_t>(t) * p.N + n;
+            T a[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a[i] = add[static_cast<int64_t>(i < count ? i : 0) * p.N];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] += to_f(a[i]);
+        }
+        if (count >= 16) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) out[static_cast<int64_t>(i) * p.N] = from_f<T>(r[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < count) out[static_cast<int64_t>(i) * p.N] = from_f<T>(r[i]);
+        }
+    };
+    auto load_acc = [&](int column, float (&v)[16]) {
+        uint32_t d[16];
+        tc_ld_32x32b_x16(tmem + lane_base + static_cast<uint32_t>(column), d);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = done ? __uint_as_float(d[i]) : NAN;
+    };
+    if (warp >= kFirstEpilogue) {
+        const uint32_t accempty0 = map_shared(smem_u32(accempty), leader);
+        const int thread = threadIdx.x - 32 * kFirstEpilogue;
+        uint32_t it = 0;
+        for (int v = first; v < items; v += stride, ++it) {
+            const int t0 = t_row(v), n = w_row(v) + row;
+            const float ws = n < p.N ? __ldg(p.ws + n) : 0.0f;
+            const float bias = n < p.N && p.bias ? __ldg(p.bias + n) : 0.0f;
+            if (it > 0) named_barrier(1, 32 * kEpilogues);   // the last tile's scales have been read
+            for (int i = thread; i < nt; i += 32 * kEpilogues) sScale[i] = __ldg(p.xs + min(t0 + i, p.T - 1));
+            named_barrier(1, 32 * kEpilogues);
+            done = done && mbar_wait_bounded(accfull, it & 1u, abort_flag, status, true);
+            done = __all_sync(0xffffffffu, done);
+            tc_fence_after();
+            if (ksplit > 1) break;   // one item per cluster: joined below
+            for (int j = eset * xrows; j < (eset + 1) * xrows; j += 16) {
+                float s[16];
+                load_acc(j, s);
+                emit(n, ws, bias, t0 + j, p.T - t0 - j, sScale + j, s);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(accempty);
+            if (lane == 0) mbar_arrive_cluster(accempty0);
+        }
+    }
+    if (ksplit > 1) {
+        // The cluster's pairs hold sums over parts of K: pair s gets the others'
+        // sums of its share of the tile's tokens in shared memory (free now: all
+        // operands have been read) and adds them in the order of the parts.
+        const int share = nt / ksplit;           // a multiple of 16
+        const int v = first;
+        float* sums = reinterpret_cast<float*>(smem);   // [ksplit][share][kM]
+        __syncwarp();
+        cluster_sync();
+        if (warp >= kFirstEpilogue) {
+            for (int d = 0; d < ksplit; ++d) {
+                if (d == split) continue;
+                const uint32_t to = map_shared(smem_u32(sums + (split * share) * kM + row), static_cast<uint32_t>(2 * d) + side);
+                for (int j = eset * 16; j < share; j += 32) {
+                    float x[16];
+                    load_acc(d * share + j, x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) st_shared_cluster_f32(to + (j + i) * kM * 4, x[i]);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+        if (warp >= kFirstEpilogue) {
+            const int n = w_row(v) + row;
+            const float ws = n < p.N ? __ldg(p.ws + n) : 0.0f;
+            const float bias = n < p.N && p.bias ? __ldg(p.bias + n) : 0.0f;
+            for (int j = eset * 16; j < share; j += 32) {
+                float x[16], s[16];
+                load_acc(split * share + j, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+                for (int d = 0; d < ksplit; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[i] += d == split ? x[i] : sums[(d * share + j + i) * kM + row];
+                const int c = split * share + j;   // token of the tile
+                emit(n, ws, bias, t_row(v) + c, p.T - t_row(v) - c, sScale + c, s);
+            }
         }
     }
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
+    cluster_sync();     // the pair's TMEM is not in use, and no CTA leaves while another may reach its barriers
     if (warp == kAlloc) {
         tc_fence_after();
-        tmem_dealloc(tmem, kCols);
+        tmem_dealloc_pair(tmem, kCols);
     }
 }
 
-// sums of the K splits in split order, then the epilogue
-template <typename T>
-__global__ void __launch_bounds__(256) join_kernel(const LinearParams p, const float* __restrict__ partial, int ksplit) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t total = static_cast<int64_t>(p.T) * p.N;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t t = i / p.N;
-        const int n = static_cast<int>(i - t * p.N);
-        float s = 0.0f;
-        for (int k = 0; k < ksplit; ++k) s += partial[k * total + i];
-        s = s * __ldg(p.xs + t) * __ldg(p.ws + n);
-        if (p.bias) s += __ldg(p.bias + n);
-        if (p.addend) s += to_f(static_cast<const T*>(p.addend)[i]);
-        static_cast<T*>(p.out)[i] = from_f<T>(s);
-    }
-}
+// status of calls without a workspace
+__device__ int g_linear_status;
 
 // ------------------------------------------------------------------ plans
 
 constexpr int kSmallTokens = 32;   // up to here: small_kernel
-constexpr int kSms = 152;
+constexpr int kPairs = 76;         // CTA pairs of 152 SMs
 
 struct Plan {
     int nt = 0, ksplit = 1, kblocks = 0, n_tiles = 0, t_tiles = 0;
-    int64_t kp = 0;
-    size_t status = 0, x16 = 0, partial = 0, total = 0;
 };
 
 Plan make_plan(int64_t T, int64_t K, int64_t N) {
     Plan L;
     L.kblocks = static_cast<int>((K + kStageK - 1) / kStageK);
-    L.kp = static_cast<int64_t>(L.kblocks) * kStageK;
-    L.nt = T <= 64 ? 64 : T <= 128 ? 128 : 256;
-    L.n_tiles = static_cast<int>((N + kM - 1) / kM);
-    L.t_tiles = static_cast<int>((T + L.nt - 1) / L.nt);
+    L.n_tiles = static_cast<int>((N + 2 * kM - 1) / (2 * kM));
+    // token tiles of at most 256, all of about the same size
+    L.t_tiles = static_cast<int>((T + 255) / 256);
+    const int64_t each = (T + L.t_tiles - 1) / L.t_tiles;
     const int64_t tiles = static_cast<int64_t>(L.n_tiles) * L.t_tiles;
-    while (L.ksplit < 8 && tiles * L.ksplit * 2 <= kSms && L.kblocks >= 2 * L.ksplit * 4) L.ksplit *= 2;
-    size_t o = 256;
-    auto take = [&](size_t bytes) {
-        const size_t at = o;
-        o = (o + bytes + 255) & ~static_cast<size_t>(255);
-        return at;
-    };
-    L.x16 = take(static_cast<size_t>(T * L.kp) * 2);
-    L.partial = L.ksplit > 1 ? take(static_cast<size_t>(T * N) * 4 * L.ksplit) : 0;
-    L.total = o;
+    // few tiles: the pairs of a cluster share a tile's K, at least 4 stages each
+    while (L.ksplit < kMaxSplit && tiles * L.ksplit * 2 <= kPairs && L.kblocks >= L.ksplit * 2 * 4) L.ksplit *= 2;
+    const int64_t unit = 32 > 16 * L.ksplit ? 32 : 16 * L.ksplit;
+    L.nt = static_cast<int>((each + unit - 1) / unit * unit);
     return L;
 }
 
@@ -499,17 +549,70 @@ cudaError_t launch_small(const LinearParams& p, cudaStream_t s) {
     return launch_pdl(small_kernel<T, 4>, grid, block, 0, s, p);
 }
 
+int cuda_error(cudaError_t e, const char* what) {
+    return e == cudaSuccess ? WNA16_OK : set_error(WNA16_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// The address of g_linear_status on the current device.
+int status_word(int** p) {
+    constexpr int kDevices = 64;
+    static std::atomic<int*> known[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+    *p = dev < kDevices ? known[dev].load() : nullptr;
+    if (*p) return WNA16_OK;
+    void* a = nullptr;
+    e = cudaGetSymbolAddress(&a, g_linear_status);
+    if (e != cudaSuccess) return cuda_error(e, "cudaGetSymbolAddress");
+    *p = static_cast<int*>(a);
+    if (dev < kDevices) known[dev].store(*p);
+    return WNA16_OK;
+}
+
+// Codes [rows][K] as boxes of `box_rows` rows x 128 k (zeros past the end)
+int code_map(CUtensorMap* map, const int8_t* q, int64_t rows, int64_t K, int box_rows) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows), 1};
+    const uint64_t strides[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(K) * static_cast<uint64_t>(rows)};
+    const uint32_t box[3] = {kStageK, static_cast<uint32_t>(box_rows), 1};
+    return encode_tma_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// CTA pairs of `kern` that the device runs at the same time (one CTA per SM).
+template <typename K>
+int resident_pairs(K kern, int smem, int& pairs) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];   // one array per kernel type: all of them take a whole SM
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+    pairs = dev < kDevices ? known[dev].load() : 0;
+    if (pairs > 0) return WNA16_OK;
+    e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return cuda_error(e, "shared memory of the 8-bit linear");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+    if (e != cudaSuccess || pairs < 1) return cuda_error(e == cudaSuccess ? cudaErrorInvalidConfiguration : e, "cudaOccupancyMaxActiveClusters");
+    if (dev < kDevices) known[dev].store(pairs);
+    return WNA16_OK;
+}
+
 template <typename T>
 int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
-    auto cuda_error = [](cudaError_t e, const char* what) {
-        return e == cudaSuccess ? WNA16_OK : set_error(WNA16_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    };
     if (p.T <= kSmallTokens) return cuda_error(launch_small<T>(p, s), "8-bit linear launch");
     int sms = 0, max_smem = 0;
     if (int rc = device_limits(sms, max_smem)) return rc;
     const Plan L = make_plan(p.T, p.K, p.N);
-    auto* base = static_cast<uint8_t*>(workspace);
-    auto* x16 = reinterpret_cast<__half*>(base + L.x16);
     TileParams tp;
     tp.p = p;
     tp.nt = L.nt;
@@ -517,57 +620,45 @@ int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
     tp.n_tiles = L.n_tiles;
     tp.t_tiles = L.t_tiles;
     tp.ksplit = L.ksplit;
-    tp.partial = reinterpret_cast<float*>(base + L.partial);
-    tp.status = reinterpret_cast<int*>(base);
-    const int stage = kM * kStageK + L.nt * kStageK * 2;
-    const int bars = 8 * (2 * kMaxStages + 2 * kABufs + 3) + 16;
-    int ns = (max_smem - 1024 - bars) / stage;
-    ns = (ns > kMaxStages ? kMaxStages : ns) & ~1;
-    tp.nstage = ns;
-    const int smem = ns * stage + bars + 1024;
+    tp.status = static_cast<int*>(workspace);
+    if (!workspace)
+        if (int rc = status_word(&tp.status)) return rc;
+    const int ring = kStages * (kM + L.nt / 2) * kStageK + kBufs * (L.nt / 2) * kStageK * 2;
+    const int sums = L.ksplit > 1 ? L.nt * kM * 4 : 0;       // the join reuses the rings
+    const int smem = (ring > sums ? ring : sums) + kMaxTokens * 4 + kBars * 8 + 16 + 1024;
+    if (smem > max_smem) return set_error(WNA16_ERR_UNSUPPORTED, "8-bit linear: %d bytes of shared memory", smem);
 
     CUtensorMap tm_w, tm_x;
-    {
-        const uint64_t dims[3] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.N), 1};
-        const uint64_t strides[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.K) * p.N};
-        const uint32_t box[3] = {kStageK, kM, 1};
-        if (int rc = encode_tma_3d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.wq, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
-            return rc;
-    }
-    {
-        const uint64_t dims[3] = {64, static_cast<uint64_t>(p.T), static_cast<uint64_t>(L.kblocks)};
-        const uint64_t strides[2] = {static_cast<uint64_t>(L.kp) * 2, 128};
-        const uint32_t box[3] = {64, static_cast<uint32_t>(L.nt), 1};
-        if (int rc = encode_tma_3d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-            return rc;
-    }
+    if (int rc = code_map(&tm_w, p.wq, p.N, p.K, kM)) return rc;
+    if (int rc = code_map(&tm_x, p.xq, p.T, p.K, L.nt / 2)) return rc;
     auto kern = tile_kernel<T>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return cuda_error(e, "shared memory of the 8-bit linear");
-    const int64_t units = static_cast<int64_t>(p.T) * (L.kp / 16);
-    const int64_t blocks = (units + kConvertThreads - 1) / kConvertThreads;
-    e = launch_pdl(convert_kernel, dim3(static_cast<unsigned>(blocks < 8 * sms ? blocks : 8 * sms)), dim3(kConvertThreads), 0, s,
-                   p.xq, static_cast<int64_t>(p.T), p.K, static_cast<int>(L.kp), x16, tp.status);
-    if (e != cudaSuccess) return cuda_error(e, "8-bit linear conversion launch");
-    const int64_t items = static_cast<int64_t>(L.n_tiles) * L.t_tiles * L.ksplit;
-    e = launch_pdl(kern, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kTileThreads),
-                   static_cast<size_t>(smem), s, tm_w, tm_x, tp);
-    if (e != cudaSuccess) return cuda_error(e, "8-bit linear launch");
-    if (L.ksplit > 1) {
-        const int64_t n = static_cast<int64_t>(p.T) * p.N;
-        const int64_t jb = (n + 255) / 256;
-        e = launch_pdl(join_kernel<T>, dim3(static_cast<unsigned>(jb < 8 * sms ? jb : 8 * sms)), dim3(256), 0, s, p,
-                       static_cast<const float*>(tp.partial), L.ksplit);
-        if (e != cudaSuccess) return cuda_error(e, "8-bit linear join launch");
-    }
-    return WNA16_OK;
+    const int64_t items = static_cast<int64_t>(L.n_tiles) * L.t_tiles;
+    int pairs = 0;
+    if (int rc = resident_pairs(kern, max_smem, pairs)) return rc;
+    // a pair runs item after item; with a shared K every cluster has one item
+    const int64_t clusters = L.ksplit > 1 || items < pairs ? items : pairs;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * L.ksplit));
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(2 * L.ksplit);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_error(cudaLaunchKernelEx(&cfg, kern, tm_w, tm_x, tp), "8-bit linear launch");
 }
 
 }  // namespace
 
-size_t linear_q8_workspace(int64_t T, int64_t K, int64_t N) {
-    return T <= kSmallTokens ? 0 : make_plan(T, K, N).total;
-}
+size_t linear_q8_workspace(int64_t T, int64_t, int64_t) { return T <= kSmallTokens ? 0 : 256; }
 
 int run_linear_q8(const LinearParams& p, void* workspace, cudaStream_t s) {
     if (p.type == kBf16) return run_typed<__nv_bfloat16>(p, workspace, s);
