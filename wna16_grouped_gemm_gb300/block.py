@@ -21,7 +21,7 @@ import dataclasses
 import torch
 
 from . import binding
-from .binding import _check, _need
+from .binding import _check
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _Q_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
@@ -55,53 +55,73 @@ def _load():
     return _lib
 
 
-def _rows(t, name: str, dtype=None):
-    """A 2-D tensor whose rows are contiguous; returns its row distance."""
+# The raw calls behind torch.cuda.current_device() and current_stream(): a tenth
+# of their time, which counts where a decode step makes several small calls.
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _first(t, name: str, stream) -> tuple[int, int]:
+    """(device, stream) of a call, from its first tensor."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if (t.dtype not in _TYPES) if dtype is None else (t.dtype != dtype):
+    dev = t.get_device()
+    if dev != _device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_device()}")
+    return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _rows(t, dev: int, name: str, dtype=None) -> int:
+    """The row distance of a 2-D tensor with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if (t.dtype not in _TYPES) if dtype is None else (t.dtype is not dtype):
         raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    rows, cols = t.shape
+    if cols > 1 and step != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return ld if rows > 1 else max(cols, 1)
 
 
-def _out(t, shape: tuple, dtype, name: str, like, stream):
-    """The output tensor `t`, checked, or a new one (on the stream that writes it)."""
-    if t is None:
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=like.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=like.device)
-    _need(t, dtype, name)
-    if tuple(t.shape) != shape:
+def _ptr(t, dev: int, dtype, shape, name: str) -> int:
+    """The address of a contiguous tensor of this type and shape."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise TypeError(f"{name} must be a tensor on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    _same_device(like, t, name)
-    return t
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _same_device(x, t, name: str):
-    if t.device != x.device:
-        raise ValueError(f"{name} is on {t.device}, not on {x.device}")
+def _new(shape, dtype, dev: int, stream):
+    """An output, allocated on the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _stream(x, stream) -> int:
-    dev = x.device.index
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-
-
-def _q_outputs(x, T: int, K: int, q_dtype, group_size: int, q, scales, stream):
+def _q_outputs(T: int, K: int, q_dtype, group_size: int, q, scales, dev: int, stream):
+    """(q, scales, their addresses, the format)."""
     if q is not None:
         q_dtype = q.dtype
-    if q_dtype not in _Q_TYPES:
+    q_type = _Q_TYPES.get(q_dtype)
+    if q_type is None:
         raise TypeError(f"8-bit rows are torch.int8 or torch.float8_e4m3fn, got {q_dtype}")
-    groups = K // group_size if group_size > 0 else 1
-    return (_out(q, (T, K), q_dtype, "q", x, stream),
-            _out(scales, (T, groups), torch.float32, "scales", x, stream), _Q_TYPES[q_dtype])
+    groups = (T, K // group_size if group_size > 0 else 1)
+    if q is None:
+        q = _new((T, K), q_dtype, dev, stream)
+    if scales is None:
+        scales = _new(groups, torch.float32, dev, stream)
+    return (q, scales, _ptr(q, dev, q_dtype, (T, K), "q"), _ptr(scales, dev, torch.float32, groups, "scales"), q_type)
 
 
 def add_rmsnorm_q8(x, weight, residual=None, *, eps: float = 1e-6, q_dtype=torch.int8, group_size: int = 0,
@@ -115,36 +135,36 @@ def add_rmsnorm_q8(x, weight, residual=None, *, eps: float = 1e-6, q_dtype=torch
     None, None with want_q=False), h in x's type (None without a residual) and
     y in x's type (None unless want_norm or norm_out is given).
     residual_out=residual updates the residual in place."""
-    ldx = _rows(x, "x")
-    T, K = x.shape
-    ldr = 0
+    dev, s = _first(x, "x", stream)
+    ldx = _rows(x, dev, "x")
+    shape = x.shape
+    T, K = shape
+    dtype = x.dtype
+    ldr = r_ptr = ro_ptr = no_ptr = q_ptr = s_ptr = None
     if residual is not None:
-        ldr = _rows(residual, "residual", x.dtype)
-        if residual.shape != x.shape:
-            raise ValueError(f"residual must be {tuple(x.shape)}, got {tuple(residual.shape)}")
-        _same_device(x, residual, "residual")
-        residual_out = _out(residual_out, (T, K), x.dtype, "residual_out", x, stream)
+        ldr = _rows(residual, dev, "residual", dtype)
+        if residual.shape != shape:
+            raise ValueError(f"residual must be {tuple(shape)}, got {tuple(residual.shape)}")
+        r_ptr = residual.data_ptr()
+        if residual_out is None:
+            residual_out = _new(shape, dtype, dev, stream)
+        ro_ptr = _ptr(residual_out, dev, dtype, shape, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"weight must be a tensor of {x.dtype} or float32")
-    _need(weight, weight.dtype, "weight", 1)
-    if weight.shape[0] != K:
-        raise ValueError(f"weight must be [{K}], got {tuple(weight.shape)}")
-    _same_device(x, weight, "weight")
-    if want_norm or norm_out is not None:
-        norm_out = _out(norm_out, (T, K), x.dtype, "norm_out", x, stream)
+    w_dtype = torch.float32 if isinstance(weight, torch.Tensor) and weight.dtype is torch.float32 else dtype
+    w_ptr = _ptr(weight, dev, w_dtype, (K,), "weight")
+    if norm_out is None and want_norm:
+        norm_out = _new(shape, dtype, dev, stream)
+    if norm_out is not None:
+        no_ptr = _ptr(norm_out, dev, dtype, shape, "norm_out")
     q_type = 0
     if want_q:
-        q, scales, q_type = _q_outputs(x, T, K, q_dtype, group_size, q, scales, stream)
+        q, scales, q_ptr, s_ptr, q_type = _q_outputs(T, K, q_dtype, group_size, q, scales, dev, stream)
     elif q is not None or scales is not None:
         raise ValueError("q or scales with want_q=False")
-    s = _stream(x, stream)
-    _check(_load().wna16_moe_add_rmsnorm_q8(
-        x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(),
-        _TYPES[weight.dtype], T, K, _TYPES[x.dtype], eps, q_type, group_size, None if q is None else q.data_ptr(),
-        None if scales is None else scales.data_ptr(), None if residual_out is None else residual_out.data_ptr(),
-        None if norm_out is None else norm_out.data_ptr(), s))
+    _check((_lib or _load()).wna16_moe_add_rmsnorm_q8(
+        x.data_ptr(), ldx, r_ptr, ldr or 0, w_ptr, _TYPES[w_dtype], T, K, _TYPES[dtype], eps, q_type, group_size, q_ptr,
+        s_ptr, ro_ptr, no_ptr, s))
     return q, scales, residual_out, norm_out
 
 
@@ -152,26 +172,26 @@ def swiglu_q8(gu, *, swiglu_limit: float = 7.0, q_dtype=torch.int8, group_size: 
               stream=None):
     """(q, scales) of silu(min(g, L)) * clamp(u, -L, L) in 8 bits; gu [T, 2N]
     holds g in its first N columns and u in the others (bf16, fp16 or fp32)."""
-    ld = _rows(gu, "gu")
+    dev, s = _first(gu, "gu", stream)
+    ld = _rows(gu, dev, "gu")
     T, N2 = gu.shape
     if N2 % 2:
         raise ValueError(f"gu must have an even number of columns, got {N2}")
-    q, scales, q_type = _q_outputs(gu, T, N2 // 2, q_dtype, group_size, q, scales, stream)
-    s = _stream(gu, stream)
-    _check(_load().wna16_moe_swiglu_q8(gu.data_ptr(), ld, T, N2 // 2, _TYPES[gu.dtype], swiglu_limit, q_type,
-                                       group_size, q.data_ptr(), scales.data_ptr(), s))
+    q, scales, q_ptr, s_ptr, q_type = _q_outputs(T, N2 // 2, q_dtype, group_size, q, scales, dev, stream)
+    _check((_lib or _load()).wna16_moe_swiglu_q8(gu.data_ptr(), ld, T, N2 // 2, _TYPES[gu.dtype], swiglu_limit, q_type,
+                                                 group_size, q_ptr, s_ptr, s))
     return q, scales
 
 
 def quantize_q8(x, *, q_dtype=torch.int8, group_size: int = 0, q=None, scales=None, stream=None):
     """(q, scales) of the rows of x [T, K] in 8 bits (weights [N, K]: one scale
-    per output channel, scales.view(N) for linear_q8)."""
-    ld = _rows(x, "x")
+    per output channel, which linear_q8 takes)."""
+    dev, s = _first(x, "x", stream)
+    ld = _rows(x, dev, "x")
     T, K = x.shape
-    q, scales, q_type = _q_outputs(x, T, K, q_dtype, group_size, q, scales, stream)
-    s = _stream(x, stream)
-    _check(_load().wna16_moe_quantize_q8(x.data_ptr(), ld, T, K, _TYPES[x.dtype], q_type, group_size, q.data_ptr(),
-                                         scales.data_ptr(), s))
+    q, scales, q_ptr, s_ptr, q_type = _q_outputs(T, K, q_dtype, group_size, q, scales, dev, stream)
+    _check((_lib or _load()).wna16_moe_quantize_q8(x.data_ptr(), ld, T, K, _TYPES[x.dtype], q_type, group_size, q_ptr,
+                                                   s_ptr, s))
     return q, scales
 
 
@@ -179,21 +199,22 @@ def dequantize_q8(q, scales, *, dtype=torch.bfloat16, out=None, stream=None):
     """The values code * scale of 8-bit rows q [T, K], scales [T, groups], in `dtype`."""
     if not isinstance(q, torch.Tensor) or q.dtype not in _Q_TYPES:
         raise TypeError("q must be an int8 or float8_e4m3fn tensor")
-    _need(q, q.dtype, "q", 2)
-    _need(scales, torch.float32, "scales", 2)
-    T, K = q.shape
+    dev, s = _first(q, "q", stream)
+    shape = q.shape
+    if len(shape) != 2 or scales.dim() != 2:
+        raise ValueError(f"q and scales must have 2 dims, got {tuple(shape)} and {tuple(scales.shape)}")
+    T, K = shape
     groups = scales.shape[1]
-    if scales.shape[0] != T or groups < 1 or K % groups:
+    if groups < 1 or K % groups:
         raise ValueError(f"scales must be [{T}, groups] with groups dividing {K}, got {tuple(scales.shape)}")
-    _same_device(q, scales, "scales")
-    if out is not None:
-        dtype = out.dtype
-    if dtype not in _TYPES:
-        raise TypeError(f"values are bfloat16, float16 or float32, got {dtype}")
-    out = _out(out, (T, K), dtype, "out", q, stream)
-    s = _stream(q, stream)
-    _check(_load().wna16_moe_dequantize_q8(q.data_ptr(), scales.data_ptr(), T, K, _Q_TYPES[q.dtype],
-                                           K // groups if groups > 1 else 0, _TYPES[dtype], out.data_ptr(), s))
+    if out is None:
+        out = _new(shape, dtype, dev, stream)
+    type_ = _TYPES.get(out.dtype)
+    if type_ is None:
+        raise TypeError(f"values are bfloat16, float16 or float32, got {out.dtype}")
+    _check((_lib or _load()).wna16_moe_dequantize_q8(
+        _ptr(q, dev, q.dtype, shape, "q"), _ptr(scales, dev, torch.float32, (T, groups), "scales"), T, K,
+        _Q_TYPES[q.dtype], K // groups if groups > 1 else 0, type_, _ptr(out, dev, out.dtype, shape, "out"), s))
     return out
 
 
@@ -206,31 +227,35 @@ def route_scored(logits, topk: int, *, score: str = "sigmoid", bias=None, groups
     only.  With groups > 1 the experts are chosen inside the topk_groups groups
     of largest group_score ("top2": sum of the two best, "max": the best).  The
     weights are the chosen scores, divided by their sum (renormalize), times scale."""
-    ld = _rows(logits, "logits")
+    dev, s = _first(logits, "logits", stream)
+    ld = _rows(logits, dev, "logits")
     T, E = logits.shape
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     if group_score not in _GROUP_SCORES:
         raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
-    if bias is not None:
-        _need(bias, torch.float32, "bias", 1)
-        if bias.shape[0] != E:
-            raise ValueError(f"bias must be [{E}], got {tuple(bias.shape)}")
-        _same_device(logits, bias, "bias")
     if topk < 1:
         raise ValueError(f"topk={topk} must be positive")
-    ids = _out(ids, (T, topk), torch.int32, "ids", logits, stream)
-    weights = _out(weights, (T, topk), torch.float32, "weights", logits, stream)
-    s = _stream(logits, stream)
-    _check(_load().wna16_moe_route_scored(
-        logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T, E, _TYPES[logits.dtype], _SCORES[score],
-        groups, topk_groups, _GROUP_SCORES[group_score], topk, 1 if renormalize else 0, scale, ids.data_ptr(),
-        weights.data_ptr(), s))
+    shape = (T, topk)
+    if ids is None:
+        ids = _new(shape, torch.int32, dev, stream)
+    if weights is None:
+        weights = _new(shape, torch.float32, dev, stream)
+    _check((_lib or _load()).wna16_moe_route_scored(
+        logits.data_ptr(), ld, None if bias is None else _ptr(bias, dev, torch.float32, (E,), "bias"), T, E,
+        _TYPES[logits.dtype], _SCORES[score], groups, topk_groups, _GROUP_SCORES[group_score], topk,
+        1 if renormalize else 0, scale, _ptr(ids, dev, torch.int32, shape, "ids"),
+        _ptr(weights, dev, torch.float32, shape, "weights"), s))
     return ids, weights
 
 
 def linear_q8_workspace_size(T: int, K: int, N: int) -> int:
-    return int(_load().wna16_moe_linear_q8_workspace_size(T, K, N))
+    return int((_lib or _load()).wna16_moe_linear_q8_workspace_size(T, K, N))
+
+
+def _scale_ptr(t, dev: int, n: int, name: str) -> int:
+    """Address of n fp32 scales, [n] or [n, 1]."""
+    return _ptr(t, dev, torch.float32, (n, 1) if isinstance(t, torch.Tensor) and t.dim() == 2 else (n,), name)
 
 
 def linear_q8(xq, x_scales, wq, w_scales, *, bias=None, addend=None, dtype=torch.bfloat16, out=None, workspace=None,
@@ -241,48 +266,32 @@ def linear_q8(xq, x_scales, wq, w_scales, *, bias=None, addend=None, dtype=torch
     [N] or [N, 1], bias fp32 [N], addend [T, N] of the output's type (out=addend
     adds in place).  workspace: uint8, at least linear_q8_workspace_size(T, K, N)
     bytes, holds the status word for read_status; may be left out."""
-    _need(xq, torch.int8, "xq", 2)
-    _need(wq, torch.int8, "wq", 2)
-    _need(x_scales, torch.float32, "x_scales")
-    _need(w_scales, torch.float32, "w_scales")
+    dev, s = _first(xq, "xq", stream)
+    if not isinstance(wq, torch.Tensor) or xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError("xq and wq must be matrices")
     T, K = xq.shape
     N = wq.shape[0]
-    if wq.shape[1] != K:
-        raise ValueError(f"wq must be [N, {K}], got {tuple(wq.shape)}")
-    if x_scales.numel() != T or w_scales.numel() != N:
-        raise ValueError(f"x_scales must hold {T} and w_scales {N} values, got {tuple(x_scales.shape)} and "
-                         f"{tuple(w_scales.shape)}")
-    if out is not None:
-        dtype = out.dtype
-    elif addend is not None:
-        dtype = addend.dtype
-    if dtype not in _TYPES:
+    shape = (T, N)
+    if out is None:
+        out = _new(shape, dtype if addend is None else addend.dtype, dev, stream)
+    dtype = out.dtype
+    type_ = _TYPES.get(dtype)
+    if type_ is None:
         raise TypeError(f"the output is bfloat16, float16 or float32, got {dtype}")
-    if bias is not None:
-        _need(bias, torch.float32, "bias", 1)
-        if bias.shape[0] != N:
-            raise ValueError(f"bias must be [{N}], got {tuple(bias.shape)}")
-    if addend is not None:
-        _need(addend, dtype, "addend", 2)
-        if tuple(addend.shape) != (T, N):
-            raise ValueError(f"addend must be {(T, N)}, got {tuple(addend.shape)}")
-    for t, name in ((wq, "wq"), (x_scales, "x_scales"), (w_scales, "w_scales"), (bias, "bias"), (addend, "addend")):
-        if t is not None:
-            _same_device(xq, t, name)
-    out = _out(out, (T, N), dtype, "out", xq, stream)
-    s = _stream(xq, stream)
-    lib = _load()
+    lib = _lib or _load()
+    ws_ptr, ws_bytes = None, 0
     if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
-        _same_device(xq, workspace, "workspace")
+        ws_bytes = workspace.numel()
+        ws_ptr = _ptr(workspace, dev, torch.uint8, (ws_bytes,), "workspace")
         need = lib.wna16_moe_linear_q8_workspace_size(T, K, N)
-        if workspace.numel() < need:   # (an empty tensor has no address to refuse)
-            raise binding.Wna16Error(binding.ERR_WORKSPACE_TOO_SMALL,
-                                     f"workspace has {workspace.numel()} bytes, needs {need}")
+        if ws_bytes < need:   # (an empty tensor has no address to refuse)
+            raise binding.Wna16Error(binding.ERR_WORKSPACE_TOO_SMALL, f"workspace has {ws_bytes} bytes, needs {need}")
     _check(lib.wna16_moe_linear_q8(
-        xq.data_ptr(), x_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), None if bias is None else bias.data_ptr(),
-        None if addend is None else addend.data_ptr(), T, K, N, _TYPES[dtype], out.data_ptr(),
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), s))
+        _ptr(xq, dev, torch.int8, (T, K), "xq"), _scale_ptr(x_scales, dev, T, "x_scales"),
+        _ptr(wq, dev, torch.int8, (N, K), "wq"), _scale_ptr(w_scales, dev, N, "w_scales"),
+        None if bias is None else _ptr(bias, dev, torch.float32, (N,), "bias"),
+        None if addend is None else _ptr(addend, dev, dtype, shape, "addend"), T, K, N, type_,
+        _ptr(out, dev, dtype, shape, "out"), ws_ptr, ws_bytes, s))
     return out
 
 

@@ -13,16 +13,18 @@
 // tile_kernel (many tokens): bound by the tensor cores.  sm_103a has no 8-bit
 // integer kind of tcgen05.mma, but 8-bit integers are exact in fp16, and their
 // products and sums (below 2^24) exact in the fp32 accumulator, so the
-// codes run through kind::f16.  A pair of CTAs (cta_group::2) owns 256 output
-// channels (the M side, 128 per CTA) and one tile of up to 256 tokens (half of
-// them in each CTA's shared memory):
-//   TMA producer (warp 0)      128-k stages: codes of the CTA's weight rows and tokens
-//   W converters (warps 4..11) thread = weight row: 64 codes -> fp16 -> TMEM (operand A)
-//   X converters (12..19)      thread = token: 64 codes -> fp16 -> shared memory (operand B)
-//   MMA issuer (warp 1 of the even CTA)   256 x nt x 64 per pair of operand buffers
+// codes run through kind::f16.  A pair of CTAs (cta_group::2) owns 256 rows of
+// operand A (the M side, 128 per CTA) and a tile of up to 256 rows of operand B
+// (half of them in each CTA's shared memory).  A is the weights where tokens are
+// few (tiles of B fit them) and the tokens where they are many (a thread then
+// holds neighbouring output channels and stores 32 bytes at a time):
+//   TMA producer (warp 0)      128-k stages: codes of the CTA's rows of A and B
+//   A converters (warps 4..11) thread = row: 64 codes -> fp16 -> TMEM
+//   B converters (12..19)      thread = row: 64 codes -> fp16 -> shared memory
+//   MMA issuer (warp 1 of the even CTA)   256 x nt x 128 per pair of operand buffers
 //   epilogue (warps 20..27)    tcgen05.ld, scales, bias, addend, store
-// Only codes cross the memory system, and the weights' fp16 form never passes
-// through shared memory.  When there are few tiles, 2 or 4 pairs form a cluster
+// Only codes cross the memory system, and A's fp16 form never passes through
+// shared memory.  When there are few tiles, 2 or 4 pairs form a cluster
 // that shares a tile's K and adds its sums through distributed shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -144,7 +146,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps) small_kernel(const LinearPar
 
 // ------------------------------------------------------------------ many tokens
 
-// 4 codes -> 4 fp16 (exact): the code plus 128 as the low bits of 1024 .. 1279, minus 1152
+// 4 codes -> 4 fp16 (exact): the code plus 128 as the low bits of 1024 .. 1279, minus 1152.
+// (Masks and a shift in place of the two permutations made the converters a third slower.)
 __device__ __forceinline__ uint2 fp16x4_of(uint32_t w) {
     const uint32_t u = w ^ 0x80808080u;
     const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
@@ -154,33 +157,53 @@ __device__ __forceinline__ uint2 fp16x4_of(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-constexpr int kM = 128;            // weight rows per CTA (256 per pair)
+// Position in a ring of n slots and the parity of its current phase.
+struct Slot {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+constexpr int kM = 128;            // rows of A per CTA (256 per pair)
 constexpr int kStageK = 128;       // k per stage of codes: one 128-byte swizzle row
 constexpr int kHalfK = 64;         // k per converter set and stage: 32 TMEM columns, one 128-byte swizzle row of fp16
 constexpr int kStages = 3;
 constexpr int kBufs = 4;           // operand buffers, one stage each: 64 TMEM columns, two swizzle atoms of fp16
 constexpr int kMaxSplit = 4;
 constexpr int kProducer = 0, kIssuer = 1, kAlloc = 2;
-constexpr int kFirstW = 4, kFirstX = 12, kFirstEpilogue = 20;   // 8 warps each, in two sets of 4
+constexpr int kFirstA = 4, kFirstB = 12, kFirstEpilogue = 20;   // 8 warps each, in two sets of 4
 constexpr int kSet = 4, kEpilogues = 8;
 constexpr int kTileThreads = 32 * (kFirstEpilogue + kEpilogues);
 constexpr int kCols = 512;
 constexpr uint32_t kACol = 256;    // TMEM: accumulator in columns 0..nt-1, operand buffers from here
 constexpr int kBars = 2 * kStages + 2 * kBufs + 3;
-constexpr int kMaxTokens = 256;    // tokens per tile
+constexpr int kMaxCols = 256;      // rows of B per tile (columns of the result)
 
 struct TileParams {
     LinearParams p;
-    int nt = 0;            // tokens per tile, half of them in each CTA of the pair
+    int nt = 0;            // rows of B per tile, half of them in each CTA of the pair
     int kblocks = 0;       // stages over the whole K
-    int n_tiles = 0, t_tiles = 0;
+    int m_tiles = 0, c_tiles = 0;   // tiles of 256 rows of A, of nt rows of B
+    int addend16 = 0;      // the addend is 16-byte aligned
     int ksplit = 1;        // pairs per cluster: each takes a part of K
     int* status = nullptr;
 };
 
-template <typename T>
+// Operand A: the weights, B: the tokens; with TM the other way round.
+template <typename T, bool TM>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+    tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const TileParams tp) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -189,15 +212,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t rank = cluster_ctarank();
     const uint32_t leader = rank & ~1u, side = rank & 1u;
     const int split = static_cast<int>(rank >> 1);
-    const int nt = tp.nt, xrows = nt / 2, ksplit = tp.ksplit;
-    constexpr int w_bytes = kM * kStageK;
-    const int x_bytes = xrows * kStageK;
-    const int h_bytes = xrows * kStageK * 2;
-    uint8_t* sW = smem;
-    uint8_t* sX = sW + kStages * w_bytes;
-    uint8_t* sH = sX + kStages * x_bytes;      // the tokens' codes as fp16
-    float* sScale = reinterpret_cast<float*>(sH + kBufs * h_bytes);   // the tile's token scales
-    uint64_t* full = reinterpret_cast<uint64_t*>(sScale + kMaxTokens);
+    const int nt = tp.nt, brows = nt / 2, ksplit = tp.ksplit;
+    constexpr int a_bytes = kM * kStageK;
+    const int b_bytes = brows * kStageK;
+    const int h_bytes = brows * kStageK * 2;
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + kStages * a_bytes;
+    uint8_t* sH = sB + kStages * b_bytes;      // B's codes as fp16
+    float* sScale = reinterpret_cast<float*>(sH + kBufs * h_bytes);   // the scales of B's rows
+    uint64_t* full = reinterpret_cast<uint64_t*>(sScale + kMaxCols);
     uint64_t* empty = full + kStages;
     uint64_t* bfull = empty + kStages;         // the leader's: both CTAs' operands of a buffer are in place
     uint64_t* bempty = bfull + kBufs;
@@ -206,6 +229,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint64_t* drain = accempty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* acc_ok = abort_flag + 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -221,8 +245,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
-        tma_prefetch_desc(&tm_w);
-        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_b);
     }
     if (warp == kAlloc) {
         tmem_alloc_pair(tmem_slot, kCols);
@@ -238,32 +262,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int* status = tp.status;
     if (blockIdx.x == 0 && threadIdx.x == 0) *status = kStatusOk;   // any timeout is seconds away
 
-    const int items = tp.n_tiles * tp.t_tiles;
+    const int items = tp.m_tiles * tp.c_tiles;
     const int first = static_cast<int>(blockIdx.x) / (2 * ksplit);
     const int stride = static_cast<int>(gridDim.x) / (2 * ksplit);
     const int kb0 = static_cast<int>(static_cast<int64_t>(tp.kblocks) * split / ksplit);
     const int kb1 = static_cast<int>(static_cast<int64_t>(tp.kblocks) * (split + 1) / ksplit);
-    // item -> (token tile, weight tile), weight tiles fastest
-    auto w_row = [&](int v) { return (v % tp.n_tiles) * (2 * kM) + static_cast<int>(side) * kM; };
-    auto t_row = [&](int v) { return (v / tp.n_tiles) * nt; };
+    // item -> (tile of B, tile of A), tiles of A fastest: first rows of this CTA's A and of the pair's B
+    auto a_row = [&](int v) { return (v % tp.m_tiles) * (2 * kM) + static_cast<int>(side) * kM; };
+    auto b_row = [&](int v) { return (v / tp.m_tiles) * nt; };
 
     if (warp == kProducer) {
         if (lane == 0) {
             const uint64_t pol = policy_evict_normal();
-            const uint32_t tx = static_cast<uint32_t>(w_bytes + x_bytes);
+            const uint32_t tx = static_cast<uint32_t>(a_bytes + b_bytes);
+            Slot st;
             uint32_t kc = 0;   // stages so far
             bool ok = true;
             for (int v = first; v < items && ok; v += stride) {
-                const int n0 = w_row(v), t0 = t_row(v) + static_cast<int>(side) * xrows;
-                for (int kb = kb0; kb < kb1; ++kb, ++kc) {
-                    const int slot = kc % kStages;
-                    if (!mbar_wait(&empty[slot], ((kc / kStages) & 1u) ^ 1u, abort_flag, status)) {
+                const int a0 = a_row(v), b0 = b_row(v) + static_cast<int>(side) * brows;
+                for (int kb = kb0; kb < kb1; ++kb, ++kc, st.next(kStages)) {
+                    const int slot = st.i;
+                    if (!mbar_wait(&empty[slot], st.phase ^ 1u, abort_flag, status)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(&full[slot], tx);
-                    tma_load_3d(sW + slot * w_bytes, &tm_w, &full[slot], kb * kStageK, n0, 0, pol);
-                    tma_load_3d(sX + slot * x_bytes, &tm_x, &full[slot], kb * kStageK, t0, 0, pol);
+                    tma_load_3d(sA + slot * a_bytes, &tm_a, &full[slot], kb * kStageK, a0, 0, pol);
+                    tma_load_3d(sB + slot * b_bytes, &tm_b, &full[slot], kb * kStageK, b0, 0, pol);
                 }
             }
             // no copy may be in flight when the block ends: wait for the last issue of every slot
@@ -288,16 +313,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // f16 A and B, f32 D, both K-major, 256 x nt
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>((2 * kM) >> 4) << 24);
             const uint16_t mask = static_cast<uint16_t>(3u << rank);
-            uint32_t kc = 0, it = 0;
+            Slot bs;
+            uint32_t it = 0;
             bool ok = true, issued = false;
             for (int v = first; v < items && ok; v += stride, ++it) {
                 if (!warp_wait(accempty, (it & 1u) ^ 1u)) {
                     ok = false;
                     break;
                 }
-                for (int kb = kb0; kb < kb1; ++kb, ++kc) {
-                    const int b = kc % kBufs;
-                    if (!warp_wait(&bfull[b], (kc / kBufs) & 1u)) {
+                for (int kb = kb0; kb < kb1; ++kb, bs.next(kBufs)) {
+                    const int b = bs.i;
+                    if (!warp_wait(&bfull[b], bs.phase)) {
                         ok = false;
                         break;
                     }
@@ -329,37 +355,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp >= kFirstW && warp < kFirstEpilogue) {
+    } else if (warp >= kFirstA && warp < kFirstEpilogue) {
         // Converters.  Set s of either kind takes the k half s of every stage.
-        const bool is_x = warp >= kFirstX;
-        const uint32_t set = static_cast<uint32_t>(warp - (is_x ? kFirstX : kFirstW)) / kSet;
-        const int quarter = warp & 3;                     // TMEM lanes 32 * quarter ..
-        const int row = quarter * 32 + lane;
+        const bool is_b = warp >= kFirstB;
+        const uint32_t set = static_cast<uint32_t>(warp - (is_b ? kFirstB : kFirstA)) / kSet;
+        const int row = (warp & 3) * 32 + lane;                 // row of A (= TMEM lane) or of this CTA's half of B
         const uint32_t xr = static_cast<uint32_t>(row) & 7u;   // 128-byte swizzle
-        const uint32_t abase = tmem + kACol + (static_cast<uint32_t>(quarter * 32) << 16);
-        const bool live = !is_x || row < xrows;
-        const uint8_t* codes = is_x ? sX + row * kStageK : sW + row * kStageK;
-        const int code_bytes = is_x ? x_bytes : w_bytes;
         const uint32_t bfull0 = map_shared(smem_u32(bfull), leader);
-        uint32_t kc = 0;   // stages so far
-        bool ok = true;
-        for (int v = first; v < items && ok; v += stride) {
-            for (int kb = kb0; kb < kb1; ++kb, ++kc) {
-                const int slot = kc % kStages;
-                const int b = kc % kBufs;
-                const uint32_t bph = ((kc / kBufs) & 1u) ^ 1u;
-                if (!mbar_wait(&full[slot], (kc / kStages) & 1u, abort_flag, status)) {
-                    ok = false;
-                    break;
-                }
-                const bool ready = mbar_test_wait(smem_u32(&bempty[b]), bph);
-                uint32_t a[32];
-                if (live) {
-                    const uint8_t* src = codes + slot * code_bytes;
+        // put(buffer, fp16 pairs): 64 converted codes of the row into operand buffer `buffer`
+        auto convert = [&](const uint8_t* codes, int code_bytes, auto&& put) {
+            Slot st, bs;
+            for (int v = first; v < items; v += stride) {
+                for (int kb = kb0; kb < kb1; ++kb, st.next(kStages), bs.next(kBufs)) {
+                    const uint32_t bph = bs.phase ^ 1u;
+                    if (!mbar_wait(&full[st.i], st.phase, abort_flag, status)) return;
+                    const bool ready = mbar_test_wait(smem_u32(&bempty[bs.i]), bph);
+                    const uint8_t* src = codes + st.i * code_bytes;
+                    uint4 raw[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + (((4 * set + c) ^ xr) << 4));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[st.i]);   // the codes are in registers: the slot refills meanwhile
+                    uint32_t a[32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(src + (((4 * set + c) ^ xr) << 4));
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                        const uint32_t ww[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint2 h = fp16x4_of(ww[j]);
@@ -367,69 +387,95 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             a[c * 8 + j * 2 + 1] = h.y;
                         }
                     }
+                    if (!ready && !mbar_wait(&bempty[bs.i], bph, abort_flag, status)) return;
+                    put(bs.i, a);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(bfull0 + bs.i * 8);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[slot]);   // the codes are in registers
-                if (!ready && !mbar_wait(&bempty[b], bph, abort_flag, status)) {
-                    ok = false;
-                    break;
-                }
-                if (is_x) {
-                    if (live) {
-                        uint8_t* dst = sH + b * h_bytes + set * (h_bytes / 2) + row * (kHalfK * 2);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4*>(dst + ((static_cast<uint32_t>(j) ^ xr) << 4)) =
-                                make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
-                    }
-                    fence_proxy_async_shared();
-                } else {
-                    tc_fence_after();
-                    tc_st_32x32b_x32(abase + b * (kStageK / 2) + set * (kHalfK / 2), a);
-                    tc_wait_st();
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(bfull0 + b * 8);
             }
+        };
+        if (is_b) {
+            const bool live = row < brows;   // a tile of fewer than 256 rows leaves threads without one
+            uint8_t* dst0 = sH + set * (h_bytes / 2) + row * (kHalfK * 2);
+            convert(sB + (live ? row : 0) * kStageK, b_bytes, [&](int b, const uint32_t (&a)[32]) {
+                if (live) {
+                    uint8_t* dst = dst0 + b * h_bytes;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4*>(dst + ((static_cast<uint32_t>(j) ^ xr) << 4)) =
+                            make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+                }
+                fence_proxy_async_shared();
+            });
+        } else {
+            const uint32_t a0 = tmem + kACol + set * (kHalfK / 2) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            convert(sA + row * kStageK, a_bytes, [&](int b, const uint32_t (&a)[32]) {
+                tc_fence_after();
+                tc_st_32x32b_x32(a0 + b * (kStageK / 2), a);
+                tc_wait_st();
+                tc_fence_before();
+            });
         }
     }
 
-    // Epilogue: thread = weight row; two sets of four warps, the lower and the
-    // upper half of the tile's tokens.
+    // Epilogue: thread = row of A; two sets of four warps, the lower and the
+    // upper half of the tile's columns (rows of B).
     const int eset = (warp - kFirstEpilogue) / kSet;
     const int quarter = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const int a_len = TM ? p.T : p.N, b_len = TM ? p.N : p.T;
+    const float* a_scale = TM ? p.xs : p.ws;
+    const float* b_scale = TM ? p.ws : p.xs;
     bool done = true;   // false: a wait gave up; what is missing is written as NaN
     const int row = quarter * 32 + lane;
-    // 16 sums of this thread's output channel n, tokens t .. t + 15 of which the tile has `count`
-    auto emit = [&](int n, float ws, float bias, int t, int count, const float* scale, const float (&sum)[16]) {
-        if (n >= p.N || count <= 0) return;
-        T* out = static_cast<T*>(p.out) + static_cast<int64_t>(t) * p.N + n;
+    // 16 sums of this thread's row a of A, with the rows b .. b + 15 of B of which `count` exist
+    auto emit = [&](int a, float as, float a_bias, int b, int count, const float* scale, const float (&sum)[16]) {
+        if (a >= a_len || count <= 0) return;
         float r[16];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
             const float4 x = *reinterpret_cast<const float4*>(scale + i);
-            r[i] = fmaf(sum[i] * x.x, ws, bias);
-            r[i + 1] = fmaf(sum[i + 1] * x.y, ws, bias);
-            r[i + 2] = fmaf(sum[i + 2] * x.z, ws, bias);
-            r[i + 3] = fmaf(sum[i + 3] * x.w, ws, bias);
+            // (sum * token scale) * channel scale, in either orientation
+            r[i] = TM ? sum[i] * as * x.x : sum[i] * x.x * as;
+            r[i + 1] = TM ? sum[i + 1] * as * x.y : sum[i + 1] * x.y * as;
+            r[i + 2] = TM ? sum[i + 2] * as * x.z : sum[i + 2] * x.z * as;
+            r[i + 3] = TM ? sum[i + 3] * as * x.w : sum[i + 3] * x.w * as;
         }
+        if (p.bias) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] += TM ? __ldg(p.bias + b + (i < count ? i : 0)) : a_bias;
+        }
+        const int64_t at = TM ? static_cast<int64_t>(a) * p.N + b : static_cast<int64_t>(b) * p.N + a;
+        const int64_t step = TM ? 1 : p.N;
+        T* out = static_cast<T*>(p.out) + at;
         if (p.addend) {
-            const T* add = static_cast<const T*>(p.addend) + static_cast<int64_t>(t) * p.N + n;
-            T a[16];
+            const T* add = static_cast<const T*>(p.addend) + at;
+            alignas(32) T v[16];
+            if (TM && tp.addend16) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) a[i] = add[static_cast<int64_t>(i < count ? i : 0) * p.N];
+                for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+                    reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(add)[i];
+            } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] += to_f(a[i]);
+                for (int i = 0; i < 16; ++i) v[i] = add[(i < count ? i : 0) * step];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] += to_f(v[i]);
         }
-        if (count >= 16) {
+        if constexpr (TM) {   // 16 neighbouring outputs (all exist, on a 32-byte boundary: N is a multiple of 16)
+            alignas(32) T v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) out[static_cast<int64_t>(i) * p.N] = from_f<T>(r[i]);
+            for (int i = 0; i < 16; ++i) v[i] = from_f<T>(r[i]);
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+                st_global_32(reinterpret_cast<uint8_t*>(out) + 32 * i, reinterpret_cast<const uint32_t*>(v) + 8 * i);
+        } else if (count >= 16) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) out[i * step] = from_f<T>(r[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (i < count) out[static_cast<int64_t>(i) * p.N] = from_f<T>(r[i]);
+                if (i < count) out[i * step] = from_f<T>(r[i]);
         }
     };
     auto load_acc = [&](int column, float (&v)[16]) {
@@ -444,20 +490,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int thread = threadIdx.x - 32 * kFirstEpilogue;
         uint32_t it = 0;
         for (int v = first; v < items; v += stride, ++it) {
-            const int t0 = t_row(v), n = w_row(v) + row;
-            const float ws = n < p.N ? __ldg(p.ws + n) : 0.0f;
-            const float bias = n < p.N && p.bias ? __ldg(p.bias + n) : 0.0f;
+            const int b0 = b_row(v), a = a_row(v) + row;
+            const float as = a < a_len ? __ldg(a_scale + a) : 0.0f;
+            const float bias = !TM && a < a_len && p.bias ? __ldg(p.bias + a) : 0.0f;
             if (it > 0) named_barrier(1, 32 * kEpilogues);   // the last tile's scales have been read
-            for (int i = thread; i < nt; i += 32 * kEpilogues) sScale[i] = __ldg(p.xs + min(t0 + i, p.T - 1));
+            for (int i = thread; i < nt; i += 32 * kEpilogues) sScale[i] = __ldg(b_scale + min(b0 + i, b_len - 1));
+            // one warp polls; the others wait in a barrier, which costs the converters no issue slots
+            if (warp == kFirstEpilogue) {
+                done = done && mbar_wait_bounded(accfull, it & 1u, abort_flag, status, true);
+                done = __all_sync(0xffffffffu, done);
+                if (lane == 0) *acc_ok = done;
+            }
             named_barrier(1, 32 * kEpilogues);
-            done = done && mbar_wait_bounded(accfull, it & 1u, abort_flag, status, true);
-            done = __all_sync(0xffffffffu, done);
+            done = *acc_ok != 0;
             tc_fence_after();
             if (ksplit > 1) break;   // one item per cluster: joined below
-            for (int j = eset * xrows; j < (eset + 1) * xrows; j += 16) {
+            for (int j = eset * brows; j < (eset + 1) * brows; j += 16) {
                 float s[16];
                 load_acc(j, s);
-                emit(n, ws, bias, t0 + j, p.T - t0 - j, sScale + j, s);
+                emit(a, as, bias, b0 + j, b_len - b0 - j, sScale + j, s);
             }
             tc_fence_before();
             __syncwarp();
@@ -466,9 +517,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (ksplit > 1) {
         // The cluster's pairs hold sums over parts of K: pair s gets the others'
-        // sums of its share of the tile's tokens in shared memory (free now: all
+        // sums of its share of the tile's columns in shared memory (free now: all
         // operands have been read) and adds them in the order of the parts.
-        const int share = nt / ksplit;           // a multiple of 16
+        const int share = (nt / 16 + ksplit - 1) / ksplit * 16;   // the last one may be smaller
         const int v = first;
         float* sums = reinterpret_cast<float*>(smem);   // [ksplit][share][kM]
         __syncwarp();
@@ -477,7 +528,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int d = 0; d < ksplit; ++d) {
                 if (d == split) continue;
                 const uint32_t to = map_shared(smem_u32(sums + (split * share) * kM + row), static_cast<uint32_t>(2 * d) + side);
-                for (int j = eset * 16; j < share; j += 32) {
+                const int mine = min(share, nt - d * share);
+                for (int j = eset * 16; j < mine; j += 32) {
                     float x[16];
                     load_acc(d * share + j, x);
 #pragma unroll
@@ -488,10 +540,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         cluster_sync();
         if (warp >= kFirstEpilogue) {
-            const int n = w_row(v) + row;
-            const float ws = n < p.N ? __ldg(p.ws + n) : 0.0f;
-            const float bias = n < p.N && p.bias ? __ldg(p.bias + n) : 0.0f;
-            for (int j = eset * 16; j < share; j += 32) {
+            const int a = a_row(v) + row;
+            const float as = a < a_len ? __ldg(a_scale + a) : 0.0f;
+            const float bias = !TM && a < a_len && p.bias ? __ldg(p.bias + a) : 0.0f;
+            const int mine = min(share, nt - split * share);
+            for (int j = eset * 16; j < mine; j += 32) {
                 float x[16], s[16];
                 load_acc(split * share + j, x);
 #pragma unroll
@@ -499,8 +552,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int d = 0; d < ksplit; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s[i] += d == split ? x[i] : sums[(d * share + j + i) * kM + row];
-                const int c = split * share + j;   // token of the tile
-                emit(n, ws, bias, t_row(v) + c, p.T - t_row(v) - c, sScale + c, s);
+                const int c = split * share + j;   // column of the tile
+                emit(a, as, bias, b_row(v) + c, b_len - b_row(v) - c, sScale + c, s);
             }
         }
     }
@@ -514,31 +567,59 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
 }
 
-// status of calls without a workspace
+// Status word of calls without a workspace.
 __device__ int g_linear_status;
 
 // ------------------------------------------------------------------ plans
 
 constexpr int kSmallTokens = 32;   // up to here: small_kernel
-constexpr int kPairs = 76;         // CTA pairs of 152 SMs
+// Costs in cycles (clock traces): a stage of 128 k is bound by the converters or
+// by the tensor cores' 4 cycles per column; a column's way through the epilogue,
+// with B's rows as the tokens (2-byte stores) or as the output channels (32-byte
+// stores); the join of a shared K.
+constexpr double kStageCycles = 1250, kColumnCycles = 21, kRowColumnCycles = 8, kJoinCycles = 3000, kJoinColumnCycles = 20;
 
 struct Plan {
-    int nt = 0, ksplit = 1, kblocks = 0, n_tiles = 0, t_tiles = 0;
+    bool tokens_m = false;
+    int nt = 0, ksplit = 1, kblocks = 0, m_tiles = 0, c_tiles = 0;
 };
 
-Plan make_plan(int64_t T, int64_t K, int64_t N) {
-    Plan L;
-    L.kblocks = static_cast<int>((K + kStageK - 1) / kStageK);
-    L.n_tiles = static_cast<int>((N + 2 * kM - 1) / (2 * kM));
-    // token tiles of at most 256, all of about the same size
-    L.t_tiles = static_cast<int>((T + 255) / 256);
-    const int64_t each = (T + L.t_tiles - 1) / L.t_tiles;
-    const int64_t tiles = static_cast<int64_t>(L.n_tiles) * L.t_tiles;
-    // few tiles: the pairs of a cluster share a tile's K, at least 4 stages each
-    while (L.ksplit < kMaxSplit && tiles * L.ksplit * 2 <= kPairs && L.kblocks >= L.ksplit * 2 * 4) L.ksplit *= 2;
-    const int64_t unit = 32 > 16 * L.ksplit ? 32 : 16 * L.ksplit;
-    L.nt = static_cast<int>((each + unit - 1) / unit * unit);
-    return L;
+// The plan of least estimated time (cycles).  active[k]: clusters of k + 1 pairs
+// that run at the same time; wide: 32-byte stores are possible (without them
+// tokens on the M side lose: 3000 x 1024 x 1000 41 us against 14).
+Plan make_plan(int64_t T, int64_t K, int64_t N, bool wide, const int (&active)[kMaxSplit]) {
+    Plan best;
+    double least = 0.0;
+    const int kblocks = static_cast<int>((K + kStageK - 1) / kStageK);
+    for (int tm = 0; tm < (wide ? 2 : 1); ++tm) {
+        const int64_t a_len = tm ? T : N, b_len = tm ? N : T;
+        const int64_t m_tiles = (a_len + 2 * kM - 1) / (2 * kM);
+        const int64_t min_tiles = (b_len + kMaxCols - 1) / kMaxCols;
+        // tiles of B of about the same size, as few as fit and some more
+        for (int64_t c_tiles = min_tiles; c_tiles <= 4 * min_tiles && c_tiles < min_tiles + 8; ++c_tiles) {
+            const int64_t nt = ((b_len + c_tiles - 1) / c_tiles + 31) / 32 * 32;
+            if (nt > kMaxCols || nt * (c_tiles - 1) >= b_len) continue;
+            const int64_t tiles = m_tiles * c_tiles;
+            const double stage = nt * 4 > kStageCycles ? nt * 4 : kStageCycles;
+            const double column = tm ? kRowColumnCycles : kColumnCycles;
+            for (int ks = 1; ks <= kMaxSplit && ks <= kblocks; ++ks) {
+                const int64_t waves = (tiles + active[ks - 1] - 1) / active[ks - 1];
+                if (ks > 1 && waves > 1) break;   // (only ever faster for a single wave)
+                const int64_t per = (kblocks + ks - 1) / ks;
+                const double cost = waves * (per * stage + nt * column) + (ks > 1 ? kJoinCycles + nt * kJoinColumnCycles : 0);
+                if (best.nt == 0 || cost < least) {
+                    least = cost;
+                    best.tokens_m = tm != 0;
+                    best.nt = static_cast<int>(nt);
+                    best.ksplit = ks;
+                    best.kblocks = kblocks;
+                    best.m_tiles = static_cast<int>(m_tiles);
+                    best.c_tiles = static_cast<int>(c_tiles);
+                }
+            }
+        }
+    }
+    return best;
 }
 
 template <typename T>
@@ -578,65 +659,65 @@ int code_map(CUtensorMap* map, const int8_t* q, int64_t rows, int64_t K, int box
     return encode_tma_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// CTA pairs of `kern` that the device runs at the same time (one CTA per SM).
+// Clusters of 1 .. kMaxSplit pairs of `kern` (one CTA per SM) that the device runs at the same time.
 template <typename K>
-int resident_pairs(K kern, int smem, int& pairs) {
+int active_clusters(K kern, int smem, int (&active)[kMaxSplit]) {
     constexpr int kDevices = 64;
-    static std::atomic<int> known[kDevices];   // one array per kernel type: all of them take a whole SM
+    static std::atomic<int> known[kDevices][kMaxSplit];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
-    pairs = dev < kDevices ? known[dev].load() : 0;
-    if (pairs > 0) return WNA16_OK;
+    bool all = dev < kDevices;
+    for (int i = 0; all && i < kMaxSplit; ++i) all = (active[i] = known[dev][i].load()) > 0;
+    if (all) return WNA16_OK;
     e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return cuda_error(e, "shared memory of the 8-bit linear");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
-    if (e != cudaSuccess || pairs < 1) return cuda_error(e == cudaSuccess ? cudaErrorInvalidConfiguration : e, "cudaOccupancyMaxActiveClusters");
-    if (dev < kDevices) known[dev].store(pairs);
+    for (int i = 0; i < kMaxSplit; ++i) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(2 * (i + 1));
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * (i + 1)));
+        cfg.blockDim = dim3(kTileThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&active[i], kern, &cfg);
+        if (e != cudaSuccess || active[i] < 1)
+            return cuda_error(e == cudaSuccess ? cudaErrorInvalidConfiguration : e, "cudaOccupancyMaxActiveClusters");
+        if (dev < kDevices) known[dev][i].store(active[i]);
+    }
     return WNA16_OK;
 }
 
-template <typename T>
-int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
-    if (p.T <= kSmallTokens) return cuda_error(launch_small<T>(p, s), "8-bit linear launch");
-    int sms = 0, max_smem = 0;
-    if (int rc = device_limits(sms, max_smem)) return rc;
-    const Plan L = make_plan(p.T, p.K, p.N);
+template <typename T, bool TM>
+int launch_tiles(const LinearParams& p, const Plan& L, int max_smem, int pairs, void* workspace, cudaStream_t s) {
     TileParams tp;
     tp.p = p;
     tp.nt = L.nt;
     tp.kblocks = L.kblocks;
-    tp.n_tiles = L.n_tiles;
-    tp.t_tiles = L.t_tiles;
+    tp.m_tiles = L.m_tiles;
+    tp.c_tiles = L.c_tiles;
     tp.ksplit = L.ksplit;
+    tp.addend16 = reinterpret_cast<uintptr_t>(p.addend) % 16 == 0;
     tp.status = static_cast<int*>(workspace);
     if (!workspace)
         if (int rc = status_word(&tp.status)) return rc;
     const int ring = kStages * (kM + L.nt / 2) * kStageK + kBufs * (L.nt / 2) * kStageK * 2;
-    const int sums = L.ksplit > 1 ? L.nt * kM * 4 : 0;       // the join reuses the rings
-    const int smem = (ring > sums ? ring : sums) + kMaxTokens * 4 + kBars * 8 + 16 + 1024;
+    const int sums = L.ksplit > 1 ? L.ksplit * ((L.nt / 16 + L.ksplit - 1) / L.ksplit * 16) * kM * 4 : 0;
+    if (sums > ring) return set_error(WNA16_ERR_UNSUPPORTED, "8-bit linear: the join does not fit");   // (the rings hold it)
+    const int smem = ring + kMaxCols * 4 + kBars * 8 + 16 + 1024;
     if (smem > max_smem) return set_error(WNA16_ERR_UNSUPPORTED, "8-bit linear: %d bytes of shared memory", smem);
 
-    CUtensorMap tm_w, tm_x;
-    if (int rc = code_map(&tm_w, p.wq, p.N, p.K, kM)) return rc;
-    if (int rc = code_map(&tm_x, p.xq, p.T, p.K, L.nt / 2)) return rc;
-    auto kern = tile_kernel<T>;
+    CUtensorMap tm_a, tm_b;
+    if (int rc = code_map(&tm_a, TM ? p.xq : p.wq, TM ? p.T : p.N, p.K, kM)) return rc;
+    if (int rc = code_map(&tm_b, TM ? p.wq : p.xq, TM ? p.N : p.T, p.K, L.nt / 2)) return rc;
+    auto kern = tile_kernel<T, TM>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return cuda_error(e, "shared memory of the 8-bit linear");
-    const int64_t items = static_cast<int64_t>(L.n_tiles) * L.t_tiles;
-    int pairs = 0;
-    if (int rc = resident_pairs(kern, max_smem, pairs)) return rc;
+    const int64_t items = static_cast<int64_t>(L.m_tiles) * L.c_tiles;
     // a pair runs item after item; with a shared K every cluster has one item
     const int64_t clusters = L.ksplit > 1 || items < pairs ? items : pairs;
     cudaLaunchConfig_t cfg = {};
@@ -653,7 +734,20 @@ int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cuda_error(cudaLaunchKernelEx(&cfg, kern, tm_w, tm_x, tp), "8-bit linear launch");
+    return cuda_error(cudaLaunchKernelEx(&cfg, kern, tm_a, tm_b, tp), "8-bit linear launch");
+}
+
+template <typename T>
+int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
+    if (p.T <= kSmallTokens) return cuda_error(launch_small<T>(p, s), "8-bit linear launch");
+    int sms = 0, max_smem = 0;
+    if (int rc = device_limits(sms, max_smem)) return rc;
+    int active[kMaxSplit];
+    if (int rc = active_clusters(tile_kernel<T, false>, max_smem, active)) return rc;
+    const bool wide = p.N % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+    const Plan L = make_plan(p.T, p.K, p.N, wide, active);
+    return L.tokens_m ? launch_tiles<T, true>(p, L, max_smem, active[0], workspace, s)
+                      : launch_tiles<T, false>(p, L, max_smem, active[0], workspace, s);
 }
 
 }  // namespace
