@@ -46,13 +46,15 @@ struct ScoredRouteParams {
     int T = 0, E = 0;
     int softmax = 0;
     int groups = 1, topk_groups = 1, group_max = 0, topk = 1;
+    int group_size = 0, groups_log = 0;   // set by the launch: experts per group, log2 of groups rounded up
     int renormalize = 1;
     float scale = 1.0f;
     int32_t* ids = nullptr;
     float* weights = nullptr;
     int vec = 0;                      // four logits per load are possible
+    int bias_vec = 0;                 // four biases per load are possible
 };
-cudaError_t launch_route_scored(int type, const ScoredRouteParams& p, cudaStream_t stream);
+cudaError_t launch_route_scored(int type, ScoredRouteParams p, cudaStream_t stream);
 
 // 8-bit integer product (linear_q8.cu).
 struct LinearParams {

@@ -282,6 +282,7 @@ int wna16_moe_route_scored(const void* logits, int64_t ld, const float* bias, in
     p.ids = topk_ids;
     p.weights = topk_weights;
     p.vec = E / groups % 4 == 0 && aligned(logits, 4 * es) && ld % 4 == 0;
+    p.bias_vec = E / groups % 4 == 0 && aligned(bias, 16);
     return launched(launch_route_scored(type, p, static_cast<cudaStream_t>(stream)), "router kernel launch");
 }
 

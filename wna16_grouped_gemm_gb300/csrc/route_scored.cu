@@ -5,19 +5,23 @@
 //
 // One warp per token.  The lanes are dealt to the groups (32 / groups lanes
 // each, groups rounded up to a power of two), and every lane keeps its experts'
-// logits and choice values in registers, so that a group's two best values are
-// a few shuffles and the top-k is one warp maximum per choice.
+// choice values in registers, so that a group's two best values are a few
+// shuffles.  The top-k: the (k + 1)-th greatest of the lanes' maxima is a
+// lower bound of the (k + 1)-th best value, the few values above it are dealt
+// to the lanes, and each counts those above it.  (One warp maximum per choice,
+// the way for the rare token with more than 64 values above the bound, takes
+// about four times the instructions.)
 //
 // The chosen experts are those of exact scores.  Scores are computed in 32
 // bits with a known error; where two neighbours in the order (of groups or of
-// experts) are closer than that error and not equal by their inputs, the warp
-// makes the token's choice again with 64-bit scores.  Without a bias the order
-// of the experts is the order of the logits themselves, which is exact.
+// experts) are closer than that error and not equal by their inputs, the values
+// in question, and only those, are computed again in 64 bits and ordered by
+// them.  Without a bias the order of the experts is the order of the logits
+// themselves, which is exact.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <cmath>
-#include <type_traits>
 
 #include "block.h"
 #include "ptx.cuh"
@@ -27,7 +31,8 @@ namespace wna16 {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kWarps = 8;   // tokens per block
+constexpr float kLowest = -3.402823466e38f;   // stands for -INFINITY among values that may be chosen
+constexpr int kWarps = 4;   // tokens per block
 
 // Order-preserving map of a float (no NaN) to unsigned, above 0.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -38,7 +43,31 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ __forceinline__ float sigmoid_of(float z) { return 1.0f / (1.0f + expf(-z)); }
+// 64 bits: the order of doubles as unsigned integers
+__device__ __forceinline__ uint64_t order_key64(double v) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double key_value64(uint64_t k) {
+    return __longlong_as_double(static_cast<long long>(k ^ ((k >> 63) ? 1ull << 63 : ~0ull)));
+}
+__device__ __forceinline__ uint64_t warp_max64(uint64_t k) {
+    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(k >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -55,323 +84,546 @@ struct Lanes {
     int sub;         // lane within the group
     int size;        // experts per group
     bool live;
-    __device__ __forceinline__ Lanes(int E, int groups) {
-        int g2 = 1;
-        while (g2 < groups) g2 <<= 1;
-        per_group = 32 / g2;
+    int held;        // experts of this lane: i < held (positions grow with i)
+    __device__ __forceinline__ explicit Lanes(const ScoredRouteParams& p) {
+        per_group = 32 >> p.groups_log;
         const int lane = threadIdx.x & 31;
-        group = lane / per_group;
+        group = lane >> (5 - p.groups_log);
         sub = lane & (per_group - 1);
-        size = E / groups;
-        live = group < groups;
+        size = p.group_size;
+        live = group < p.groups;
+        const int block = 4 << (5 - p.groups_log);   // positions per four slots of the group's lanes
+        const int rest = (size & (block - 1)) - 4 * sub;
+        held = live ? (size >> (7 - p.groups_log)) * 4 + min(max(rest, 0), 4) : 0;
     }
     __device__ __forceinline__ int pos(int i) const { return (i >> 2) * 4 * per_group + sub * 4 + (i & 3); }
-    __device__ __forceinline__ bool has(int i) const { return live && pos(i) < size; }
+    __device__ __forceinline__ bool has(int i) const { return i < held; }
     __device__ __forceinline__ int expert(int i) const { return group * size + pos(i); }
 };
 
-// The softmax's shift and the sum of its exponentials over all experts.
-// With no logit above -inf all scores are 0.
+// One token's logits and how its scores are made of them.  (Passed by value to the
+// rare paths, which are not inlined: what they took by address would live in
+// local memory on the common path too.)
+struct Token {
+    const ScoredRouteParams& p;
+    int type;
+    const void* row;
+    bool infinite = false;   // softmax with logits of +inf: they share the whole weight, the others' scores are 0
+    float m = 0.0f;          // softmax: the largest logit (-inf: all scores are 0)
+    float total = 1.0f;      // softmax: sum of exp(z - m)
+
+    __device__ __forceinline__ float clean(float z) const {
+        if (!(z == z)) return -INFINITY;   // NaN: never preferred
+        if (infinite) return z == INFINITY ? 0.0f : -INFINITY;
+        return z;
+    }
+    __device__ __forceinline__ float logit(int e) const {
+        if (type == kFp32) return clean(static_cast<const float*>(row)[e]);
+        if (type == kFp16) return clean(__half2float(static_cast<const __half*>(row)[e]));
+        return clean(__bfloat162float(static_cast<const __nv_bfloat16*>(row)[e]));
+    }
+    // For the weights.
+    __device__ __forceinline__ float score(float z) const {
+        if (!p.softmax) return 1.0f / (1.0f + expf(-z));
+        if (!(m > -INFINITY)) return 0.0f;
+        return (z == m ? 1.0f : expf(z - m)) / total;
+    }
+    // 64-bit choice value; total64: the softmax's sum (any positive number without a bias: the order is the same)
+    __device__ __forceinline__ double choice64(int e, double total64) const {
+        const float z = logit(e);
+        double s;
+        if (!p.softmax)
+            s = 1.0 / (1.0 + exp(-static_cast<double>(z)));
+        else if (!(m > -INFINITY))
+            s = 0.0;
+        else
+            s = (z == m ? 1.0 : exp(static_cast<double>(z) - static_cast<double>(m))) / total64;
+        return p.bias ? s + static_cast<double>(p.bias[e]) : s;
+    }
+    __device__ __forceinline__ double total64() const {
+        if (!p.softmax || !p.bias) return 1.0;
+        double sum = 0.0;
+#pragma unroll 1
+        for (int e = threadIdx.x & 31; e < p.E; e += 32) {
+            const float z = logit(e);
+            if (m > -INFINITY) sum += z == m ? 1.0 : exp(static_cast<double>(z) - static_cast<double>(m));
+        }
+        return m > -INFINITY ? warp_sum(sum) : 1.0;
+    }
+};
+
+// A warp's values under consideration: key << 32 | ~expert, so that the greater
+// is the better one and, of equal keys, the lower expert's.  0: none.
+constexpr int kMost = 64;   // values considered at a time, at most two per lane
+struct alignas(16) Candidates {   // (v is read 16 bytes at a time, in every warp's copy)
+    uint64_t v[kMost];
+    uint2 found[kMost + 1];   // (value, expert) in no order; the last one takes what is too much
+};
+__device__ __forceinline__ uint64_t pack(uint32_t key, int expert) {
+    return static_cast<uint64_t>(key) << 32 | ~static_cast<uint32_t>(expert);
+}
+__device__ __forceinline__ int expert_of(uint64_t v) { return static_cast<int>(~static_cast<uint32_t>(v)); }
+
+// Collects the experts whose value is at least the lane's `bound` (above -INFINITY);
+// their number, of which the first 64 are in c.v (the rest of it is 0).
 template <int PL>
-__device__ __forceinline__ void softmax_of(const Lanes& L, const float (&z)[PL], float& m, float& total) {
-    m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) m = fmaxf(m, z[i]);
-    m = key_value(__reduce_max_sync(kAll, order_key(m)));
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-        if (L.has(i) && m > -INFINITY) sum += z[i] == m ? 1.0f : expf(z[i] - m);
-    total = warp_sum(sum);
-}
-
-__device__ __forceinline__ float score_of(float z, bool softmax, float m, float total) {
-    if (!softmax) return sigmoid_of(z);
-    if (!(m > -INFINITY)) return 0.0f;
-    return (z == m ? 1.0f : expf(z - m)) / total;
-}
-
-// The token's choice with 64-bit scores: lane j gets choice j's expert and
-// logit.  z: the lane's n logits.  Rarely run, so kept small: its arrays are in
-// local memory and its loops are not unrolled.
-constexpr int kMaxPerLane = 64;
-__device__ __noinline__ void choose64(const ScoredRouteParams& p, const float* z, int n, int& my_id, float& my_z) {
-    const Lanes L(p.E, p.groups);
+__device__ __forceinline__ int collect(const Lanes& L, const float (&value)[PL], float bound, Candidates& c) {
     const int lane = threadIdx.x & 31;
-    double total = 0.0;
-    float m = -INFINITY;
-    if (p.softmax) {
-        for (int i = 0; i < n; ++i) m = fmaxf(m, z[i]);
-        m = key_value(__reduce_max_sync(kAll, order_key(m)));
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) mine += value[i] >= bound ? 1 : 0;
+    int at = mine;   // places of this lane's values: after those of the lanes below
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, at, o);
+        if (lane >= o) at += v;
     }
-    double c[kMaxPerLane];
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        c[i] = -INFINITY;
-        if (!L.has(i)) continue;
-        // sigmoid: 1 / (1 + exp(-z)); softmax: exp(z - m), divided below
-        const double e = p.softmax && z[i] == m ? 1.0 : exp(p.softmax ? static_cast<double>(z[i]) - static_cast<double>(m) : -static_cast<double>(z[i]));
-        c[i] = !p.softmax ? 1.0 / (1.0 + e) : m > -INFINITY ? e : 0.0;
-        total += c[i];
-    }
-    total = p.softmax && m > -INFINITY ? warp_sum(total) : 1.0;
-    double b0 = -INFINITY, b1 = -INFINITY;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        if (!L.has(i)) continue;
-        c[i] = c[i] / total + (p.bias ? static_cast<double>(p.bias[L.expert(i)]) : 0.0);
-        if (c[i] > b0) {
-            b1 = b0;
-            b0 = c[i];
-        } else if (c[i] > b1) {
-            b1 = c[i];
+    const int count = __shfl_sync(kAll, at, 31);
+    at -= mine;
+    __syncwarp();
+    if (mine > 0) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            if (value[i] >= bound) {
+                c.found[min(at, kMost)] = make_uint2(__float_as_uint(value[i]), static_cast<uint32_t>(L.expert(i)));
+                ++at;
+            }
         }
     }
-    uint64_t taken = 0;
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < kMost; h += 32) {
+        if (h > 0 && count <= 32) {
+            c.v[lane + h] = 0ull;
+            break;
+        }
+        const uint2 f = c.found[lane + h];
+        c.v[lane + h] = lane + h < count ? pack(order_key(__uint_as_float(f.x)), static_cast<int>(f.y)) : 0ull;
+    }
+    __syncwarp();
+    return count;
+}
+
+// How many of the first `count` values are greater than v.
+__device__ __forceinline__ int rank_of(uint64_t v, const Candidates& c, int count) {
+    int rank = 0;
+    for (int j = 0; j < count; j += 4) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&c.v[j]), b = *reinterpret_cast<const ulonglong2*>(&c.v[j + 2]);
+        rank += (a.x > v) + (a.y > v) + (b.x > v) + (b.y > v);
+    }
+    return rank;
+}
+
+// All of the token's choice with 64-bit scores: lane j gets choice j's expert.
+// For tokens with more than 64 values in question; kept small (arrays in local
+// memory, loops not unrolled).
+constexpr int kMaxPerLane = 64;
+__device__ __noinline__ int choose64(Token t, int n) {
+    const ScoredRouteParams& p = t.p;
+    const Lanes L(p);
+    const int lane = threadIdx.x & 31;
+    const double total = t.total64();
+    uint64_t key[kMaxPerLane];
+    uint64_t b0 = 0, b1 = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        key[i] = L.has(i) ? order_key64(t.choice64(L.expert(i), total)) : 0ull;
+        if (key[i] > b0) {
+            b1 = b0;
+            b0 = key[i];
+        } else if (key[i] > b1) {
+            b1 = key[i];
+        }
+    }
     if (p.topk_groups < p.groups) {
         for (int o = 1; o < L.per_group; o <<= 1) {
-            const double a0 = __shfl_xor_sync(kAll, b0, o), a1 = __shfl_xor_sync(kAll, b1, o);
+            const uint64_t a0 = __shfl_xor_sync(kAll, b0, o), a1 = __shfl_xor_sync(kAll, b1, o);
             b1 = b0 > a0 ? (b1 > a0 ? b1 : a0) : (a1 > b0 ? a1 : b0);
             b0 = b0 > a0 ? b0 : a0;
         }
-        const double gs = p.group_max || L.size < 2 ? b0 : b0 + b1;
+        const double gs = !L.live ? 0.0 : p.group_max || L.size < 2 ? key_value64(b0) : key_value64(b0) + key_value64(b1);
         int rank = 0;
         for (int g = 0; g < p.groups; ++g) {
             const double o = __shfl_sync(kAll, gs, g * L.per_group);
             rank += o > gs || (o == gs && g < L.group);
         }
-        if (rank >= p.topk_groups) taken = ~0ull;
+        if (rank >= p.topk_groups)
+            for (int i = 0; i < n; ++i) key[i] = 0ull;
     }
-    constexpr int kNone = 0x7fffffff;
+    int my_id = 0;
 #pragma unroll 1
     for (int j = 0; j < p.topk; ++j) {
-        double bv = -INFINITY;
-        int bi = kNone, at = 0;
+        uint64_t best = 0;
+        int at = 0;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            if (L.has(i) && !((taken >> i) & 1) && (bi == kNone || c[i] > bv)) {
-                bv = c[i];
-                bi = L.expert(i);
-                at = i;
-            }
-        }
-        const int mine = bi;
-        for (int o = 16; o > 0; o >>= 1) {
-            const double ov = __shfl_xor_sync(kAll, bv, o);
-            const int oi = __shfl_xor_sync(kAll, bi, o);
-            if (oi != kNone && (bi == kNone || ov > bv || (ov == bv && oi < bi))) {
-                bv = ov;
-                bi = oi;
-            }
-        }
-        const bool own = mine == bi;   // one lane: a candidate is always left (topk <= topk_groups * size)
-        if (own) taken |= 1ull << at;
-        const float zv = __shfl_sync(kAll, z[at], __ffs(__ballot_sync(kAll, own)) - 1);
-        if (lane == j) {
-            my_id = bi;
-            my_z = zv;
-        }
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ float logit_of(T v) {
-    if constexpr (sizeof(T) == 4)
-        return v;
-    else if constexpr (std::is_same<T, __half>::value)
-        return __half2float(v);
-    else
-        return __bfloat162float(v);
-}
-
-template <typename T, int PL>
-__global__ void __launch_bounds__(32 * kWarps) route_scored_kernel(const ScoredRouteParams p) {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (t >= p.T) return;   // whole warps leave together
-    const Lanes L(p.E, p.groups);
-    const T* row = static_cast<const T*>(p.logits) + static_cast<int64_t>(t) * p.ld;
-
-    float z[PL];
-#pragma unroll
-    for (int i = 0; i < PL; i += 4) {
-        if (p.vec && L.has(i)) {
-            alignas(16) T e[4];
-            if constexpr (sizeof(T) == 4)
-                *reinterpret_cast<uint4*>(e) = __ldg(reinterpret_cast<const uint4*>(row + L.expert(i)));
-            else
-                *reinterpret_cast<uint2*>(e) = __ldg(reinterpret_cast<const uint2*>(row + L.expert(i)));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[i + j] = logit_of(e[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[i + j] = !p.vec && L.has(i + j) ? logit_of(row[L.expert(i + j)]) : -INFINITY;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-        if (!(z[i] == z[i])) z[i] = -INFINITY;   // NaN: never preferred
-
-    float m = 0.0f, total = 1.0f;
-    if (p.softmax) {
-        softmax_of<PL>(L, z, m, total);
-        if (m == INFINITY) {   // infinite logits share the whole weight; the others' scores are 0
-#pragma unroll
-            for (int i = 0; i < PL; ++i) z[i] = z[i] == m ? 0.0f : -INFINITY;
-            m = 0.0f;
-        }
-    }
-    const bool pick_groups = p.topk_groups < p.groups;
-    const bool by_logit = p.bias == nullptr;       // the experts' order is the logits' order
-    // choice values; with by_logit needed for the sums of groups only
-    const bool need_c = !by_logit || (pick_groups && !p.group_max);
-    float c[PL];
-    float big = 0.0f;   // largest magnitude among scores and choice values
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-        c[i] = z[i];
-        if (need_c) {
-            c[i] = -INFINITY;
-            if (L.has(i)) {
-                const float s = score_of(z[i], p.softmax, m, total);
-                c[i] = p.bias ? s + __ldg(p.bias + L.expert(i)) : s;
-                big = fmaxf(big, fmaxf(s, fabsf(c[i])));
-            }
-        }
-    }
-    // Two choice values closer than tol may be in either order.  Sigmoid: a
-    // score's error is at most 5 units of 2^-24, a sum's rounding one more, for
-    // each of the two; softmax: besides, the shifted logit's rounding (at most
-    // 0.37 units after the exponential) and the error of the total, a sum of up
-    // to PL + 5 roundings.
-    big = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(big)));
-    const float tol = big * (p.softmax ? static_cast<float>(2 * PL + 32) * 0x1p-24f : 0x1p-20f);
-    bool unsure = false;
-
-    bool out = !L.live;
-    if (pick_groups) {
-        const bool by_c = need_c;
-        float b0 = -INFINITY, b1 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const float v = L.has(i) ? c[i] : -INFINITY;
-            b1 = fmaxf(b1, fminf(b0, v));
-            b0 = fmaxf(b0, v);
-        }
-        for (int o = 1; o < L.per_group; o <<= 1) {
-            const float a0 = __shfl_xor_sync(kAll, b0, o), a1 = __shfl_xor_sync(kAll, b1, o);
-            b1 = fmaxf(fmaxf(b1, a1), fminf(b0, a0));
-            b0 = fmaxf(b0, a0);
-        }
-        const float gs = p.group_max || L.size < 2 ? b0 : b0 + b1;
-        int rank = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const float o = __shfl_sync(kAll, gs, g * L.per_group);
-            rank += o > gs || (o == gs && g < L.group);
-        }
-        if (rank >= p.topk_groups) out = true;
-        if (by_c) {
-            const uint32_t kept = L.live && rank < p.topk_groups ? order_key(gs) : 0xffffffffu;
-            const uint32_t left = L.live && rank >= p.topk_groups ? order_key(gs) : 0u;
-            unsure = key_value(__reduce_min_sync(kAll, kept)) - key_value(__reduce_max_sync(kAll, left)) <= 4.0f * tol;
-        }
-    }
-
-    if (by_logit) {
-#pragma unroll
-        for (int i = 0; i < PL; ++i) c[i] = z[i];
-    }
-    uint32_t key[PL];
-#pragma unroll
-    for (int i = 0; i < PL; ++i) key[i] = !out && L.has(i) ? order_key(c[i]) : 0u;
-
-    int my_id = 0;
-    float my_z = 0.0f;
-    uint32_t last_key = 0, last_id = 0;
-    float last_z = 0.0f;
-    const int candidates = p.topk_groups * L.size;
-    const int rounds = by_logit ? p.topk : min(p.topk + 1, candidates);   // one more, for the last one's margin
-    for (int j = 0; j < rounds; ++j) {
-        uint32_t best = 0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
             if (key[i] > best) {
                 best = key[i];
                 at = i;
             }
         }
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        const uint32_t e = best == top ? static_cast<uint32_t>(L.expert(at)) : 0xffffffffu;
+        const uint64_t top = warp_max64(best);
+        const uint32_t e = best == top && top != 0ull ? static_cast<uint32_t>(L.expert(at)) : kAll;
         const uint32_t id = __reduce_min_sync(kAll, e);
-        float zv = 0.0f;
-        const bool mine = e == id;
+        if (e == id) key[at] = 0ull;
+        if (lane == j) my_id = static_cast<int>(id);
+    }
+    return my_id;
+}
+
+// Whether this lane's group stays, when 32 bits cannot tell: gs is its score,
+// `kept` the decision so far, `lo` the least of the kept groups' scores and `hi` the
+// greatest of the others'.  from: the least value that may be one of the group's two
+// best.  Returns false if there are too many values to look at.
+template <int PL>
+__device__ __noinline__ bool settle_groups(Token t, Lanes L, const float* value, float gs, float lo, float hi,
+                                           float from, float tol, Candidates& cand, bool& kept) {
+    const ScoredRouteParams& p = t.p;
+    const int lane = threadIdx.x & 31;
+    const bool open = L.live && (kept ? gs <= hi + 2.0f * tol : gs >= lo - 2.0f * tol);
+    const int open_kept = __popc(__ballot_sync(kAll, open && kept && L.sub == 0));   // places to give
+    float v[PL];
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            if (i == at) {
-                zv = z[i];
-                if (mine) key[i] = 0u;
+    for (int i = 0; i < PL; ++i) v[i] = value[i];
+    const int count = collect(L, v, open ? from : INFINITY, cand);
+    if (count > 32) return false;
+    const double total = t.total64();
+    const int e = lane < count ? expert_of(cand.v[lane]) : -1;
+    const int my_group = e >= 0 ? e / L.size : -1;
+    const uint64_t k = e >= 0 ? order_key64(t.choice64(e, total)) : 0ull;
+    double sum = 0.0;   // of group `lane`
+    for (int g = 0; g < p.groups; ++g) {
+        const uint64_t v = my_group == g ? k : 0ull;
+        const uint64_t first = warp_max64(v);
+        if (first == 0ull) continue;   // not open
+        double s = key_value64(first);
+        if (!p.group_max && L.size >= 2) {
+            const int owner = __ffs(__ballot_sync(kAll, v == first)) - 1;
+            s += key_value64(warp_max64(lane == owner ? 0ull : v));
+        }
+        if (lane == g) sum = s;
+    }
+    const uint32_t open_mask = __ballot_sync(kAll, open && L.sub == 0);   // by the groups' first lanes
+    const double mine = __shfl_sync(kAll, sum, L.live ? L.group : 0);
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const double o = __shfl_sync(kAll, sum, g);
+        if (open_mask >> (g * L.per_group) & 1u) rank += o > mine || (o == mine && g < L.group);
+    }
+    if (open) kept = rank < open_kept;
+    return true;
+}
+
+// Sorts the `count` collected experts by their 64-bit values.
+__device__ __noinline__ void settle_order(Token t, Candidates& cand, int count) {
+    const int lane = threadIdx.x & 31;
+    const double total = t.total64();
+    int e[2], rank[2] = {0, 0};
+    uint64_t k[2];
+    for (int h = 0; h < 2; ++h) {
+        const bool in = lane + 32 * h < count;
+        e[h] = in ? expert_of(cand.v[lane + 32 * h]) : 0;
+        k[h] = in ? order_key64(t.choice64(e[h], total)) : 0ull;
+        if (count <= 32) break;
+    }
+    for (int j = 0; j < count; ++j) {
+        const uint64_t ok = __shfl_sync(kAll, j < 32 ? k[0] : k[1], j & 31);
+        const int oe = __shfl_sync(kAll, j < 32 ? e[0] : e[1], j & 31);
+        rank[0] += ok > k[0] || (ok == k[0] && oe < e[0]);
+        if (count > 32) rank[1] += ok > k[1] || (ok == k[1] && oe < e[1]);
+    }
+    __syncwarp();
+    if (lane < count) cand.v[rank[0]] = pack(0u, e[0]);
+    if (lane + 32 < count) cand.v[rank[1]] = pack(0u, e[1]);
+    __syncwarp();
+}
+
+template <int PL, bool SOFTMAX>
+__global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_kernel(const __grid_constant__ ScoredRouteParams p, int type) {
+    __shared__ Candidates shared[kWarps];
+    static_assert(sizeof(Candidates) % 16 == 0, "every warp's copy is 16-byte aligned");
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int ti = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (ti >= p.T) return;   // whole warps leave together
+    Candidates& cand = shared[threadIdx.x >> 5];
+    const Lanes L(p);
+    Token t{p, type, static_cast<const uint8_t*>(p.logits) + static_cast<int64_t>(ti) * p.ld * (type == kFp32 ? 4 : 2)};
+
+    // logits, -INFINITY where the lane has no expert
+    float z[PL];
+    if (p.vec) {
+        if (type == kFp32) {
+            const float* row = static_cast<const float*>(t.row) + L.expert(0);
+#pragma unroll
+            for (int i = 0; i < PL; i += 4) {
+                float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                if (L.has(i)) v = __ldg(reinterpret_cast<const float4*>(row + i * L.per_group));
+                z[i] = v.x;
+                z[i + 1] = v.y;
+                z[i + 2] = v.z;
+                z[i + 3] = v.w;
+            }
+        } else {
+            const uint16_t* row = static_cast<const uint16_t*>(t.row) + L.expert(0);
+            const uint32_t none = type == kFp16 ? 0xfc00fc00u : 0xff80ff80u;
+#pragma unroll
+            for (int i = 0; i < PL; i += 4) {
+                uint2 v = make_uint2(none, none);
+                if (L.has(i)) v = __ldg(reinterpret_cast<const uint2*>(row + i * L.per_group));
+                const uint32_t h[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    z[i + j] = type == kFp16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(h[j]))) : __uint_as_float(h[j] << 16);
             }
         }
-        zv = __shfl_sync(kAll, zv, __ffs(__ballot_sync(kAll, mine)) - 1);
-        if (lane == j) {
-            my_id = static_cast<int>(id);
-            my_z = zv;
-        }
-        if (!by_logit) {
-            // Equal inputs give equal scores in any precision, and their order is
-            // the index's (but behind the last choice a third one may be as near).
-            if (j > 0 && key_value(last_key) - key_value(top) <= tol)
-                unsure = unsure || j == p.topk || last_z != zv || __ldg(p.bias + last_id) != __ldg(p.bias + id);
-            last_key = top;
-            last_id = id;
-            last_z = zv;
-        }
-    }
-    if (unsure) {
-        float copy[PL];
 #pragma unroll
-        for (int i = 0; i < PL; ++i) copy[i] = z[i];
-        choose64(p, copy, PL, my_id, my_z);
+        for (int i = 0; i < PL; ++i) z[i] = fmaxf(z[i], -INFINITY);   // NaN: -INFINITY, as Token::clean
+    } else {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) z[i] = L.has(i) ? t.logit(L.expert(i)) : -INFINITY;
     }
 
-    float w = lane < p.topk ? score_of(my_z, p.softmax, m, total) : 0.0f;
+    float bias[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) bias[i] = -INFINITY;   // no expert
+    if (p.bias) {
+        const float* src = p.bias + L.expert(0);
+#pragma unroll
+        for (int i = 0; i < PL; i += 4) {
+            if (p.bias_vec) {
+                if (L.has(i)) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(src + i * L.per_group));
+                    bias[i] = v.x;
+                    bias[i + 1] = v.y;
+                    bias[i + 2] = v.z;
+                    bias[i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (L.has(i + j)) bias[i + j] = __ldg(src + i * L.per_group + j);
+            }
+        }
+    }
+
+    constexpr float kLog2e = 1.44269504f;
+    float top_score = 1.0f;   // no score is greater
+    if constexpr (SOFTMAX) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) m = fmaxf(m, z[i]);
+        t.m = key_value(__reduce_max_sync(kAll, order_key(m)));
+        if (t.m == INFINITY) {
+            t.infinite = true;
+            t.m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) z[i] = t.clean(z[i]);
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) sum += t.m > -INFINITY ? exp2_approx((z[i] - t.m) * kLog2e) : 0.0f;   // (0 without an expert)
+        t.total = warp_sum(sum);
+        top_score = t.m > -INFINITY ? rcp_approx(t.total) : 0.0f;
+    }
+    auto fast_score = [&](float x) {   // with the fast exponential: see unit
+        if constexpr (SOFTMAX)
+            return exp2_approx((t.m > -INFINITY ? x - t.m : -INFINITY) * kLog2e) * top_score;
+        else
+            return rcp_approx(1.0f + exp2_approx(x * -kLog2e));
+    };
+    // What the experts are ordered by: choice values or, without a bias, the logits.
+    // -INFINITY: no expert.
+    const bool by_logit = p.bias == nullptr;
+    float value[PL];
+    if (by_logit) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) value[i] = L.has(i) ? fmaxf(z[i], kLowest) : -INFINITY;
+    } else {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) value[i] = fast_score(z[i]) + bias[i];
+    }
+    // Two choice values that differ by at most unit times the greatest of the scores
+    // and of their own magnitudes may be in either order.  Errors in units of
+    // 2^-24 of that.  Sigmoid: the exponential's relative error is 4 and 1.5 |z| for
+    // its argument's rounding, of which the score sees s (1 - s): 1 + 1.5 * 0.37;
+    // the sum 1, the reciprocal 2, the bias 1; for both values 12.  Softmax: 4 and
+    // at most 2.5 * 0.37 likewise, the reciprocal and product 3, the bias 1, and the
+    // total's, a sum of up to PL + 5 roundings and its terms' 5; for both values.
+    constexpr float unit = SOFTMAX ? static_cast<float>(2 * PL + 48) * 0x1p-24f : 24.0f * 0x1p-24f;
+
+    float best = -INFINITY, second = -INFINITY;   // of the lane
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        second = fmaxf(second, fminf(best, value[i]));
+        best = fmaxf(best, value[i]);
+    }
+    bool out = !L.live;
+    bool all64 = false;
+    if (p.topk_groups < p.groups) {
+        float b0 = best, b1 = second;             // of the group
+        for (int o = 1; o < L.per_group; o <<= 1) {
+            const float a0 = __shfl_xor_sync(kAll, b0, o), a1 = __shfl_xor_sync(kAll, b1, o);
+            b1 = fmaxf(fmaxf(b1, a1), fminf(b0, a0));
+            b0 = fmaxf(b0, a0);
+        }
+        const bool best_only = p.group_max || L.size < 2;
+        const float from = best_only ? b0 : b1;
+        if (by_logit && !best_only) {
+            b0 = fast_score(b0);
+            b1 = fast_score(b1);
+        }
+        const float gs = best_only ? b0 : b0 + b1;
+        int rank = 0;
+#pragma unroll 4
+        for (int g = 0; g < p.groups; ++g) {
+            const float o = __shfl_sync(kAll, gs, g << (5 - p.groups_log));
+            rank += g < L.group ? o >= gs : o > gs;
+        }
+        bool kept = L.live && rank < p.topk_groups;
+        if (!by_logit || !best_only) {   // (the best logits' order is exact)
+            const float lo = key_value(__reduce_min_sync(kAll, kept ? order_key(gs) : 0xffffffffu));
+            const float hi = key_value(__reduce_max_sync(kAll, L.live && !kept ? order_key(gs) : 0u));
+            const float most = L.live ? fmaxf(fabsf(b0), best_only ? 0.0f : fabsf(b1)) : 0.0f;
+            const float tol = unit * fmaxf(top_score, __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most))));
+            if (lo - hi <= 2.0f * tol) {   // a sum's error is twice a value's
+                float copy[PL];
+#pragma unroll
+                for (int i = 0; i < PL; ++i) copy[i] = value[i];
+                bool stays = kept;
+                all64 = !settle_groups<PL>(t, L, copy, gs, lo, hi, by_logit ? from : from - tol, tol, cand, stays);
+                kept = stays;
+            }
+        }
+        out = !kept;
+    }
+
+    int my_id = 0;
+    if (all64) {
+        my_id = choose64(t, PL);
+    } else {
+        // A bound that at least topk + 1 values (or all there are) reach: the lanes'
+        // (topk + 1)-th greatest maximum, or where that takes most of the lanes, the
+        // (topk / 2 + 1)-th greatest second best, each of which has its lane's best above it.
+        const bool seconds = 2 * (p.topk + 1) > p.topk_groups * L.per_group;
+        uint32_t mine = out ? 0u : order_key(seconds ? second : best), top = 0u;
+        for (int j = seconds ? p.topk / 2 : p.topk; j >= 0; --j) {
+            top = __reduce_max_sync(kAll, mine);
+            if (mine == top) mine = 0u;   // (several lanes at once where values are equal)
+        }
+        const float bound = out ? INFINITY : top == 0u ? kLowest : fmaxf(key_value(top), kLowest);
+        int count = collect(L, value, bound, cand);
+        bool unsure = false;
+        if (count <= kMost) {
+            // sort: each value goes to the place of its rank
+            const bool two = count > 32;
+            uint64_t v = cand.v[lane], v2 = two ? cand.v[lane + 32] : 0ull;
+            {
+                const int rank = rank_of(v, cand, count), rank2 = two ? rank_of(v2, cand, count) : 0;
+                __syncwarp();
+                if (lane < count) cand.v[rank] = v;
+                if (lane + 32 < count) cand.v[rank2] = v2;
+                __syncwarp();
+            }
+            v = cand.v[lane];
+            my_id = expert_of(v);
+            if (!by_logit) {
+                const uint64_t next = lane + 1 < count ? cand.v[lane + 1] : 0ull;
+                const float mine = key_value(static_cast<uint32_t>(v >> 32));
+                const float last = __shfl_sync(kAll, mine, p.topk - 1);
+                const float tol = unit * fmaxf(top_score, fmaxf(fabsf(__shfl_sync(kAll, mine, 0)), fabsf(last)));
+                bool close = lane < p.topk && lane + 1 < count && mine - key_value(static_cast<uint32_t>(next >> 32)) <= tol;
+                // Equal inputs give equal scores in any precision, and their order is the
+                // index's (but behind the last choice a third one may be as near).
+                if (close && lane + 1 < p.topk)
+                    close = t.logit(my_id) != t.logit(expert_of(next)) || p.bias[my_id] != p.bias[expert_of(next)];
+                if (__any_sync(kAll, close)) {
+                    // every value that may be among the choices, in 64 bits
+                    count = collect(L, value, out ? INFINITY : fmaxf(last - tol, kLowest), cand);
+                    if (count <= kMost) {
+                        settle_order(t, cand, count);
+                        my_id = expert_of(cand.v[lane]);
+                    } else {
+                        unsure = true;
+                    }
+                }
+            }
+        } else {
+            // many values above the bound: one warp maximum per choice
+            if (out) {
+#pragma unroll
+                for (int i = 0; i < PL; ++i) value[i] = -INFINITY;
+            }
+            float last = INFINITY, tol = 0.0f;
+            int last_id = 0;
+            const int rounds = by_logit ? p.topk : min(p.topk + 1, p.topk_groups * L.size);   // one more, for the last one's margin
+            for (int j = 0; j < rounds; ++j) {
+                float top = -INFINITY;
+                int at = 0;
+#pragma unroll
+                for (int i = 0; i < PL; ++i) {
+                    if (value[i] > top) {
+                        top = value[i];
+                        at = i;
+                    }
+                }
+                const uint32_t key = order_key(top), all = __reduce_max_sync(kAll, key);
+                const uint32_t e = key == all && top > -INFINITY ? static_cast<uint32_t>(L.expert(at)) : kAll;
+                const uint32_t id = __reduce_min_sync(kAll, e);
+#pragma unroll
+                for (int i = 0; i < PL; ++i)
+                    if (i == at && e == id) value[i] = -INFINITY;
+                if (lane == j) my_id = static_cast<int>(id);
+                if (!by_logit) {
+                    const float now = key_value(all);
+                    if (j == 0) tol = top_score;
+                    tol = fmaxf(tol, fabsf(now));
+                    if (last - now <= unit * tol)
+                        unsure = unsure || j == p.topk || t.logit(last_id) != t.logit(static_cast<int>(id)) ||
+                                 p.bias[last_id] != p.bias[id];
+                    last = now;
+                    last_id = static_cast<int>(id);
+                }
+            }
+        }
+        if (unsure) my_id = choose64(t, PL);
+    }
+
+    float w = lane < p.topk ? t.score(t.logit(my_id)) : 0.0f;
     if (p.renormalize) {
         const float sum = warp_sum(w);
-        w = sum > 0.0f ? w / sum : 0.0f;
+        w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
     }
     if (lane < p.topk) {
-        p.ids[static_cast<int64_t>(t) * p.topk + lane] = my_id;
-        p.weights[static_cast<int64_t>(t) * p.topk + lane] = w * p.scale;
+        p.ids[static_cast<int64_t>(ti) * p.topk + lane] = my_id;
+        p.weights[static_cast<int64_t>(ti) * p.topk + lane] = w * p.scale;
     }
 }
 
-template <typename T>
-cudaError_t launch_typed(const ScoredRouteParams& p, cudaStream_t s) {
-    int g2 = 1;
-    while (g2 < p.groups) g2 <<= 1;
-    const int span = 4 * (32 / g2);                      // experts per four register slots of a group's lanes
-    const int pl = (p.E / p.groups + span - 1) / span * 4;
+template <bool SOFTMAX>
+cudaError_t launch_score(int type, const ScoredRouteParams& p, cudaStream_t s) {
+    const int span = 4 << (5 - p.groups_log);            // experts per four register slots of a group's lanes
+    const int pl = (p.group_size + span - 1) / span * 4;
     // few tokens: one warp per block, each on an SM of its own
-    const int warps = p.T >= 2048 ? kWarps : 1;
+    const int warps = p.T >= 1024 ? kWarps : 1;
     const dim3 grid(static_cast<unsigned>((p.T + warps - 1) / warps)), block(32 * warps);
-    if (pl <= 4) return launch_pdl(route_scored_kernel<T, 4>, grid, block, 0, s, p);
-    if (pl <= 8) return launch_pdl(route_scored_kernel<T, 8>, grid, block, 0, s, p);
-    if (pl <= 16) return launch_pdl(route_scored_kernel<T, 16>, grid, block, 0, s, p);
-    if (pl <= 32) return launch_pdl(route_scored_kernel<T, 32>, grid, block, 0, s, p);
-    if (pl <= 64) return launch_pdl(route_scored_kernel<T, 64>, grid, block, 0, s, p);
+    if (pl <= 4) return launch_pdl(route_scored_kernel<4, SOFTMAX>, grid, block, 0, s, p, type);
+    if (pl <= 8) return launch_pdl(route_scored_kernel<8, SOFTMAX>, grid, block, 0, s, p, type);
+    if (pl <= 16) return launch_pdl(route_scored_kernel<16, SOFTMAX>, grid, block, 0, s, p, type);
+    if (pl <= 32) return launch_pdl(route_scored_kernel<32, SOFTMAX>, grid, block, 0, s, p, type);
+    if (pl <= kMaxPerLane) return launch_pdl(route_scored_kernel<64, SOFTMAX>, grid, block, 0, s, p, type);
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_route_scored(int type, const ScoredRouteParams& p, cudaStream_t s) {
+cudaError_t launch_route_scored(int type, ScoredRouteParams p, cudaStream_t s) {
     if (p.T == 0) return cudaSuccess;
-    if (type == kBf16) return launch_typed<__nv_bfloat16>(p, s);
-    if (type == kFp16) return launch_typed<__half>(p, s);
-    return launch_typed<float>(p, s);
+    p.group_size = p.E / p.groups;
+    p.groups_log = 0;
+    while ((1 << p.groups_log) < p.groups) ++p.groups_log;
+    return p.softmax ? launch_score<true>(type, p, s) : launch_score<false>(type, p, s);
 }
 
 }  // namespace wna16
