@@ -27,6 +27,7 @@ struct RowParams {
     float limit = 0.0f;
     int q_type = kInt8;
     int group = 0;                    // 0: one scale per row
+    int group_log = 0;                // log2 of it, set by the launch
     void* q = nullptr;
     float* scales = nullptr;
     void* residual_out = nullptr;
@@ -34,7 +35,7 @@ struct RowParams {
     int vec = 0;                      // 16-byte accesses are possible
 };
 
-cudaError_t launch_rows(RowOp op, int type, const RowParams& p, cudaStream_t stream);
+cudaError_t launch_rows(RowOp op, int type, RowParams p, cudaStream_t stream);
 cudaError_t launch_dequantize_q8(const void* q, const float* scales, int64_t T, int K, int q_type, int group, int type,
                                  void* out, bool vec, cudaStream_t stream);
 

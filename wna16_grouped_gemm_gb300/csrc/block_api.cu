@@ -228,7 +228,7 @@ int wna16_moe_dequantize_q8(const void* q, const float* scales, int64_t T, int64
     const Range outs[1] = {{out, static_cast<size_t>(T * K) * es, "out"}};
     const Range ins[2] = {{q, static_cast<size_t>(T * K), "q"}, {scales, scale_bytes(T, K, group_size), "scales"}};
     if (int rc = check_overlap(outs, ins, false)) return rc;
-    const bool vec = K % 8 == 0 && aligned(q, 8) && aligned(out, 16);
+    const bool vec = K % 16 == 0 && aligned(q, 16) && aligned(out, 16);
     return launched(launch_dequantize_q8(q, scales, T, static_cast<int>(K), q_type, group_size, type, out, vec,
                                          static_cast<cudaStream_t>(stream)),
                     "dequantize kernel launch");
