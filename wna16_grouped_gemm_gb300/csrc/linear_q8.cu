@@ -5,10 +5,13 @@
 //
 // small_kernel (a few tokens): bound by the weights' bytes.  A block owns 16
 // output channels; its 8 warps take the K range in turns of 64, each lane
-// loading 16 consecutive bytes of two weight rows straight into the registers
-// of two mma.sync m16n8k32 (the order of k inside a product is free, so both
-// operands use the order in which the bytes lie).  The integer sums of the
-// warps are added in shared memory.
+// loading 16 consecutive bytes of two weight rows and of a token straight into
+// registers, where they become the fp16 operands of four mma.sync m16n8k16 (the
+// order of k inside a product is free, so both operands use the order in which
+// the bytes lie).  The fp32 sums of at most 1024 products are exact integers;
+// they are added as integers, over the warps in shared memory.  (mma.sync on
+// 8-bit integers, a 40th of the fp16 rate on this chip: 4 x 4096 x 4096 5.0 us,
+// 32 x 4096 x 4096 17.6 us.)
 //
 // tile_kernel (many tokens): bound by the tensor cores.  sm_103a has no 8-bit
 // integer kind of tcgen05.mma, but 8-bit integers are exact in fp16, and their
@@ -60,92 +63,6 @@ __device__ __forceinline__ T from_f(float v) {
         return __float2bfloat16_rn(v);
 }
 
-// ------------------------------------------------------------------ few tokens
-
-constexpr int kSmallWarps = 8;
-constexpr int kSmallRows = 16;
-
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// NT tiles of 8 tokens
-template <typename T, int NT>
-__global__ void __launch_bounds__(32 * kSmallWarps) small_kernel(const LinearParams p) {
-    __shared__ int part[kSmallWarps][kSmallRows][NT * 8 + 1];
-    pdl_wait();
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, q = lane & 3;
-    const int n0 = blockIdx.x * kSmallRows;
-    const int K = p.K;
-    // rows past the end read the last one; their results are not stored
-    const int8_t* w0 = p.wq + static_cast<int64_t>(min(n0 + g, p.N - 1)) * K;
-    const int8_t* w1 = p.wq + static_cast<int64_t>(min(n0 + g + 8, p.N - 1)) * K;
-    const int8_t* x[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) x[j] = p.xq + static_cast<int64_t>(min(j * 8 + g, p.T - 1)) * K;
-
-    int acc[NT][4] = {};
-    constexpr int kUnroll = NT <= 2 ? 4 : 2;
-    constexpr int kStep = 64 * kSmallWarps;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int k0 = warp * 64; k0 < K; k0 += kStep * kUnroll) {   // the same turns for every lane of the warp
-        uint4 a[kUnroll], b[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int k = k0 + u * kStep + q * 16;
-            a[u] = k < K ? ld_stream(w0 + k) : zero;
-            b[u] = k < K ? ld_stream(w1 + k) : zero;
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int k = k0 + u * kStep + q * 16;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint4 c = k < K ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : zero;
-                mma_s8(acc[j], a[u].x, b[u].x, a[u].y, b[u].y, c.x, c.y);
-                mma_s8(acc[j], a[u].z, b[u].z, a[u].w, b[u].w, c.z, c.w);
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        part[warp][g][j * 8 + 2 * q] = acc[j][0];
-        part[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
-        part[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
-        part[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kSmallRows * NT * 8; i += 32 * kSmallWarps) {
-        const int r = i % kSmallRows, t = i / kSmallRows;
-        const int n = n0 + r;
-        if (n >= p.N || t >= p.T) continue;
-        int sum = 0;
-#pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) sum += part[w][r][t];
-        float v = static_cast<float>(sum) * __ldg(p.xs + t) * __ldg(p.ws + n);
-        if (p.bias) v += __ldg(p.bias + n);
-        const int64_t o = static_cast<int64_t>(t) * p.N + n;
-        if (p.addend) v += to_f(static_cast<const T*>(p.addend)[o]);
-        static_cast<T*>(p.out)[o] = from_f<T>(v);
-    }
-}
-
-// ------------------------------------------------------------------ many tokens
-
 // 4 codes -> 4 fp16 (exact): the code plus 128 as the low bits of 1024 .. 1279, minus 1152.
 // (Masks and a shift in place of the two permutations made the converters a third slower.)
 __device__ __forceinline__ uint2 fp16x4_of(uint32_t w) {
@@ -156,6 +73,123 @@ __device__ __forceinline__ uint2 fp16x4_of(uint32_t w) {
     const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), off);
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
+
+// ------------------------------------------------------------------ few tokens
+
+constexpr int kSmallWarps = 8;
+constexpr int kSmallRows = 16;
+constexpr int kExactSteps = 16;   // 64-k steps whose sums stay below 2^24 (1024 * 2^14)
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT tiles of 8 tokens; U steps of 64 k in flight per warp, at least BLOCKS blocks per SM
+template <typename T, int NT, int U, int BLOCKS>
+__global__ void __launch_bounds__(32 * kSmallWarps, BLOCKS) small_kernel(const LinearParams p) {
+    __shared__ int part[kSmallWarps][kSmallRows][NT * 8 + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, q = lane & 3;
+    const int n0 = blockIdx.x * kSmallRows;
+    const int K = p.K;
+    // the block's weights on their way to L2 while the kernel before finishes (nothing of them is used)
+    for (int64_t i = threadIdx.x * 128; i < static_cast<int64_t>(min(kSmallRows, p.N - n0)) * K; i += 32 * kSmallWarps * 128)
+        prefetch_l2(p.wq + static_cast<int64_t>(n0) * K + i);
+    pdl_wait();
+    pdl_trigger();
+    // rows past the end read the last one; their results are not stored
+    const int8_t* w0 = p.wq + static_cast<int64_t>(min(n0 + g, p.N - 1)) * K;
+    const int8_t* w1 = p.wq + static_cast<int64_t>(min(n0 + g + 8, p.N - 1)) * K;
+    const int8_t* x[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x[j] = p.xq + static_cast<int64_t>(min(j * 8 + g, p.T - 1)) * K;
+
+    int sum[NT][4] = {};
+    float acc[NT][4] = {};
+    constexpr int kStep = 64 * kSmallWarps;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    int held = 0;   // steps in acc
+    for (int k0 = warp * 64; k0 < K; k0 += kStep * U) {   // the same turns for every lane of the warp
+        uint4 a[U], b[U], c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * kStep + q * 16;
+            a[u] = k < K ? ld_stream(w0 + k) : zero;
+            b[u] = k < K ? ld_stream(w1 + k) : zero;
+            c[u] = k < K ? __ldg(reinterpret_cast<const uint4*>(x[0] + k)) : zero;
+        }
+        if (held + U > kExactSteps) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sum[j][i] += __float2int_rn(acc[j][i]);
+                    acc[j][i] = 0.0f;
+                }
+            held = 0;
+        }
+        held += U;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * kStep + q * 16;
+            const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+            uint2 fa[4], fb[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                fa[m] = fp16x4_of(aw[m]);
+                fb[m] = fp16x4_of(bw[m]);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint4 xc = j == 0 ? c[u] : k < K ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : zero;
+                const uint32_t xw[4] = {xc.x, xc.y, xc.z, xc.w};
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint2 fx = fp16x4_of(xw[m]);
+                    mma_f16(acc[j], fa[m].x, fb[m].x, fa[m].y, fb[m].y, fx.x, fx.y);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[j][i] += __float2int_rn(acc[j][i]);
+        part[warp][g][j * 8 + 2 * q] = sum[j][0];
+        part[warp][g][j * 8 + 2 * q + 1] = sum[j][1];
+        part[warp][g + 8][j * 8 + 2 * q] = sum[j][2];
+        part[warp][g + 8][j * 8 + 2 * q + 1] = sum[j][3];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kSmallRows * NT * 8; i += 32 * kSmallWarps) {
+        const int r = i % kSmallRows, t = i / kSmallRows;
+        const int n = n0 + r;
+        if (n >= p.N || t >= p.T) continue;
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) total += part[w][r][t];
+        float v = static_cast<float>(total) * __ldg(p.xs + t) * __ldg(p.ws + n);
+        if (p.bias) v += __ldg(p.bias + n);
+        const int64_t o = static_cast<int64_t>(t) * p.N + n;
+        if (p.addend) v += to_f(static_cast<const T*>(p.addend)[o]);
+        static_cast<T*>(p.out)[o] = from_f<T>(v);
+    }
+}
+
+// ------------------------------------------------------------------ many tokens
 
 // Position in a ring of n slots and the parity of its current phase.
 struct Slot {
@@ -622,12 +656,23 @@ Plan make_plan(int64_t T, int64_t K, int64_t N, bool wide, const int (&active)[k
     return best;
 }
 
+// Steps in flight and blocks per SM, measured (us) with the weights streamed from memory:
+//   tokens x 4096 x N      4, 4096   4, 32768   16, 4096   16, 32768   32, 4096
+//   chosen                 4.7       24.0       6.0        32.7        8.2
+//   the other blocks/SM    5.2       27.4       6.6        37.4        8.2
+//   twice the steps        4.9       29.8       6.1        34.9        10.3
+// More blocks hide one another's loads and ends where there are several turns of
+// them; with one turn (at most two blocks per SM) registers for loads count.
 template <typename T>
-cudaError_t launch_small(const LinearParams& p, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>((p.N + kSmallRows - 1) / kSmallRows)), block(32 * kSmallWarps);
-    if (p.T <= 8) return launch_pdl(small_kernel<T, 1>, grid, block, 0, s, p);
-    if (p.T <= 16) return launch_pdl(small_kernel<T, 2>, grid, block, 0, s, p);
-    return launch_pdl(small_kernel<T, 4>, grid, block, 0, s, p);
+cudaError_t launch_small(const LinearParams& p, int sms, cudaStream_t s) {
+    const int blocks = (p.N + kSmallRows - 1) / kSmallRows;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(32 * kSmallWarps);
+    const bool turns = blocks > 2 * sms;
+    if (p.T <= 8)
+        return launch_pdl(turns ? small_kernel<T, 1, 4, 3> : small_kernel<T, 1, 4, 2>, grid, block, 0, s, p);
+    if (p.T <= 16)
+        return launch_pdl(turns ? small_kernel<T, 2, 2, 4> : small_kernel<T, 2, 2, 2>, grid, block, 0, s, p);
+    return launch_pdl(small_kernel<T, 4, 2, 2>, grid, block, 0, s, p);
 }
 
 int cuda_error(cudaError_t e, const char* what) {
@@ -739,9 +784,9 @@ int launch_tiles(const LinearParams& p, const Plan& L, int max_smem, int pairs, 
 
 template <typename T>
 int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
-    if (p.T <= kSmallTokens) return cuda_error(launch_small<T>(p, s), "8-bit linear launch");
     int sms = 0, max_smem = 0;
     if (int rc = device_limits(sms, max_smem)) return rc;
+    if (p.T <= kSmallTokens) return cuda_error(launch_small<T>(p, sms, s), "8-bit linear launch");
     int active[kMaxSplit];
     if (int rc = active_clusters(tile_kernel<T, false>, max_smem, active)) return rc;
     const bool wide = p.N % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
