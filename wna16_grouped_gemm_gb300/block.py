@@ -8,9 +8,9 @@ and the MoE block that runs them together with the routed-expert forward.
     quantize_q8, dequantize_q8   rows to 8 bits and back
     moe_block        norm -> router -> routed experts + shared expert
 
-As in ``binding``: argument checks and marshalling only, every function takes
-CUDA tensors, runs on the current stream (or ``stream``) and needs the built
-library.  Outputs may be passed in (``q=``, ``scales=``, ``out=``, ...), as a
+As in ``binding``: argument checks and marshalling only (in the compiled module
+``_host``), every function takes CUDA tensors, runs on the current stream (or
+``stream``) and needs the built library.  Outputs may be passed in (``q=``, ``scales=``, ``out=``, ...), as a
 program does that keeps its buffers between steps; otherwise they are allocated.
 """
 from __future__ import annotations
@@ -23,17 +23,17 @@ import torch
 from . import binding
 from .binding import _check
 
-_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_Q_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _SCORES = {"sigmoid": 0, "softmax": 1}
 _GROUP_SCORES = {"top2": 0, "max": 1}
 
 _lib = None
+_host = None
 
 
 def declare(lib):
-    """Argument types of the block operators' entry points."""
+    """Declare the block operators' entry points of a loaded library and keep their addresses."""
     P, I64, I, F, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.block = {}
     for name, args in (
             ("add_rmsnorm_q8", [P, I64, P, I64, P, I, I64, I64, I, F, I, I, P, P, P, P, P]),
             ("swiglu_q8", [P, I64, I64, I64, I, F, I, I, P, P, P]),
@@ -43,85 +43,56 @@ def declare(lib):
             ("linear_q8", [P, P, P, P, P, P, I64, I64, I64, I, P, P, SZ, P])):
         f = getattr(lib, "wna16_moe_" + name)
         f.argtypes, f.restype = args, I
+        lib.block[name] = ctypes.cast(f, P).value
     lib.wna16_moe_linear_q8_workspace_size.argtypes = [I64, I64, I64]
     lib.wna16_moe_linear_q8_workspace_size.restype = SZ
     return lib
 
 
 def _load():
-    global _lib
+    """The library, and the module that checks arguments and calls it (raises if either was not built)."""
+    global _lib, _host
+    if _host is None:
+        try:
+            from . import _host as host
+        except ImportError as e:
+            raise RuntimeError("the module _host is missing: build it with wna16_grouped_gemm_gb300.build.build()") from e
+        # the raw calls behind torch.cuda.current_device() and current_stream(): a tenth of their time
+        host.setup((torch.bfloat16, torch.float16, torch.float32, torch.int8, torch.float8_e4m3fn, torch.int32, torch.uint8),
+                   torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _host = host
     if _lib is None:
         _lib = declare(binding.load_library())
     return _lib
 
 
-# The raw calls behind torch.cuda.current_device() and current_stream(): a tenth
-# of their time, which counts where a decode step makes several small calls.
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _first(t, name: str, stream) -> tuple[int, int]:
-    """(device, stream) of a call, from its first tensor."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    dev = t.get_device()
-    if dev != _device():
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_device()}")
-    return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-def _rows(t, dev: int, name: str, dtype=None) -> int:
-    """The row distance of a 2-D tensor with contiguous rows."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if (t.dtype not in _TYPES) if dtype is None else (t.dtype is not dtype):
-        raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
-    ld, step = t.stride()
-    rows, cols = t.shape
-    if cols > 1 and step != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return ld if rows > 1 else max(cols, 1)
-
-
-def _ptr(t, dev: int, dtype, shape, name: str) -> int:
-    """The address of a contiguous tensor of this type and shape."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise TypeError(f"{name} must be a tensor on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _new(shape, dtype, dev: int, stream):
+def _new(shape, dtype, like, stream):
     """An output, allocated on the stream that writes it."""
+    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        raise TypeError("the inputs must be CUDA tensors")
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _q_outputs(T: int, K: int, q_dtype, group_size: int, q, scales, dev: int, stream):
-    """(q, scales, their addresses, the format)."""
-    if q is not None:
-        q_dtype = q.dtype
-    q_type = _Q_TYPES.get(q_dtype)
-    if q_type is None:
-        raise TypeError(f"8-bit rows are torch.int8 or torch.float8_e4m3fn, got {q_dtype}")
-    groups = (T, K // group_size if group_size > 0 else 1)
+def _new_q(x, K: int, q_dtype, group_size: int, q, scales, stream):
+    """What is missing of (q, scales) for 8-bit rows of K values."""
     if q is None:
-        q = _new((T, K), q_dtype, dev, stream)
+        if q_dtype not in (torch.int8, torch.float8_e4m3fn):
+            raise TypeError(f"8-bit rows are torch.int8 or torch.float8_e4m3fn, got {q_dtype}")
+        q = _new((x.shape[0], K), q_dtype, x, stream)
     if scales is None:
-        scales = _new(groups, torch.float32, dev, stream)
-    return (q, scales, _ptr(q, dev, q_dtype, (T, K), "q"), _ptr(scales, dev, torch.float32, groups, "scales"), q_type)
+        scales = _new((x.shape[0], K // group_size if group_size > 0 else 1), torch.float32, x, stream)
+    return q, scales
+
+
+def _matrix(x, name: str):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {tuple(x.shape)}")
+    return x.shape
 
 
 def add_rmsnorm_q8(x, weight, residual=None, *, eps: float = 1e-6, q_dtype=torch.int8, group_size: int = 0,
@@ -135,36 +106,23 @@ def add_rmsnorm_q8(x, weight, residual=None, *, eps: float = 1e-6, q_dtype=torch
     None, None with want_q=False), h in x's type (None without a residual) and
     y in x's type (None unless want_norm or norm_out is given).
     residual_out=residual updates the residual in place."""
-    dev, s = _first(x, "x", stream)
-    ldx = _rows(x, dev, "x")
-    shape = x.shape
-    T, K = shape
-    dtype = x.dtype
-    ldr = r_ptr = ro_ptr = no_ptr = q_ptr = s_ptr = None
-    if residual is not None:
-        ldr = _rows(residual, dev, "residual", dtype)
-        if residual.shape != shape:
-            raise ValueError(f"residual must be {tuple(shape)}, got {tuple(residual.shape)}")
-        r_ptr = residual.data_ptr()
-        if residual_out is None:
-            residual_out = _new(shape, dtype, dev, stream)
-        ro_ptr = _ptr(residual_out, dev, dtype, shape, "residual_out")
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    w_dtype = torch.float32 if isinstance(weight, torch.Tensor) and weight.dtype is torch.float32 else dtype
-    w_ptr = _ptr(weight, dev, w_dtype, (K,), "weight")
-    if norm_out is None and want_norm:
-        norm_out = _new(shape, dtype, dev, stream)
-    if norm_out is not None:
-        no_ptr = _ptr(norm_out, dev, dtype, shape, "norm_out")
-    q_type = 0
+    lib = _lib or _load()
     if want_q:
-        q, scales, q_ptr, s_ptr, q_type = _q_outputs(T, K, q_dtype, group_size, q, scales, dev, stream)
+        if q is None or scales is None:
+            q, scales = _new_q(x, _matrix(x, "x")[1], q_dtype, group_size, q, scales, stream)
     elif q is not None or scales is not None:
         raise ValueError("q or scales with want_q=False")
-    _check((_lib or _load()).wna16_moe_add_rmsnorm_q8(
-        x.data_ptr(), ldx, r_ptr, ldr or 0, w_ptr, _TYPES[w_dtype], T, K, _TYPES[dtype], eps, q_type, group_size, q_ptr,
-        s_ptr, ro_ptr, no_ptr, s))
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+    elif residual_out is None:
+        residual_out = _new(_matrix(x, "x"), x.dtype, x, stream)
+    if norm_out is None and want_norm:
+        norm_out = _new(_matrix(x, "x"), x.dtype, x, stream)
+    rc = _host.add_rmsnorm_q8(lib.block["add_rmsnorm_q8"], x, weight, residual, residual_out, norm_out, q, scales, eps,
+                              group_size, stream)
+    if rc:
+        _check(rc)
     return q, scales, residual_out, norm_out
 
 
@@ -172,49 +130,37 @@ def swiglu_q8(gu, *, swiglu_limit: float = 7.0, q_dtype=torch.int8, group_size: 
               stream=None):
     """(q, scales) of silu(min(g, L)) * clamp(u, -L, L) in 8 bits; gu [T, 2N]
     holds g in its first N columns and u in the others (bf16, fp16 or fp32)."""
-    dev, s = _first(gu, "gu", stream)
-    ld = _rows(gu, dev, "gu")
-    T, N2 = gu.shape
-    if N2 % 2:
-        raise ValueError(f"gu must have an even number of columns, got {N2}")
-    q, scales, q_ptr, s_ptr, q_type = _q_outputs(T, N2 // 2, q_dtype, group_size, q, scales, dev, stream)
-    _check((_lib or _load()).wna16_moe_swiglu_q8(gu.data_ptr(), ld, T, N2 // 2, _TYPES[gu.dtype], swiglu_limit, q_type,
-                                                 group_size, q_ptr, s_ptr, s))
+    lib = _lib or _load()
+    if q is None or scales is None:
+        q, scales = _new_q(gu, _matrix(gu, "gu")[1] // 2, q_dtype, group_size, q, scales, stream)
+    rc = _host.swiglu_q8(lib.block["swiglu_q8"], gu, q, scales, swiglu_limit, group_size, stream)
+    if rc:
+        _check(rc)
     return q, scales
 
 
 def quantize_q8(x, *, q_dtype=torch.int8, group_size: int = 0, q=None, scales=None, stream=None):
     """(q, scales) of the rows of x [T, K] in 8 bits (weights [N, K]: one scale
     per output channel, which linear_q8 takes)."""
-    dev, s = _first(x, "x", stream)
-    ld = _rows(x, dev, "x")
-    T, K = x.shape
-    q, scales, q_ptr, s_ptr, q_type = _q_outputs(T, K, q_dtype, group_size, q, scales, dev, stream)
-    _check((_lib or _load()).wna16_moe_quantize_q8(x.data_ptr(), ld, T, K, _TYPES[x.dtype], q_type, group_size, q_ptr,
-                                                   s_ptr, s))
+    lib = _lib or _load()
+    if q is None or scales is None:
+        q, scales = _new_q(x, _matrix(x, "x")[1], q_dtype, group_size, q, scales, stream)
+    rc = _host.quantize_q8(lib.block["quantize_q8"], x, q, scales, group_size, stream)
+    if rc:
+        _check(rc)
     return q, scales
 
 
 def dequantize_q8(q, scales, *, dtype=torch.bfloat16, out=None, stream=None):
     """The values code * scale of 8-bit rows q [T, K], scales [T, groups], in `dtype`."""
-    if not isinstance(q, torch.Tensor) or q.dtype not in _Q_TYPES:
-        raise TypeError("q must be an int8 or float8_e4m3fn tensor")
-    dev, s = _first(q, "q", stream)
-    shape = q.shape
-    if len(shape) != 2 or scales.dim() != 2:
-        raise ValueError(f"q and scales must have 2 dims, got {tuple(shape)} and {tuple(scales.shape)}")
-    T, K = shape
-    groups = scales.shape[1]
-    if groups < 1 or K % groups:
-        raise ValueError(f"scales must be [{T}, groups] with groups dividing {K}, got {tuple(scales.shape)}")
+    lib = _lib or _load()
     if out is None:
-        out = _new(shape, dtype, dev, stream)
-    type_ = _TYPES.get(out.dtype)
-    if type_ is None:
-        raise TypeError(f"values are bfloat16, float16 or float32, got {out.dtype}")
-    _check((_lib or _load()).wna16_moe_dequantize_q8(
-        _ptr(q, dev, q.dtype, shape, "q"), _ptr(scales, dev, torch.float32, (T, groups), "scales"), T, K,
-        _Q_TYPES[q.dtype], K // groups if groups > 1 else 0, type_, _ptr(out, dev, out.dtype, shape, "out"), s))
+        if not isinstance(q, torch.Tensor) or q.dtype not in (torch.int8, torch.float8_e4m3fn):
+            raise TypeError("q must be an int8 or float8_e4m3fn tensor")
+        out = _new(_matrix(q, "q"), dtype, q, stream)
+    rc = _host.dequantize_q8(lib.block["dequantize_q8"], q, scales, out, stream)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -227,35 +173,27 @@ def route_scored(logits, topk: int, *, score: str = "sigmoid", bias=None, groups
     only.  With groups > 1 the experts are chosen inside the topk_groups groups
     of largest group_score ("top2": sum of the two best, "max": the best).  The
     weights are the chosen scores, divided by their sum (renormalize), times scale."""
-    dev, s = _first(logits, "logits", stream)
-    ld = _rows(logits, dev, "logits")
-    T, E = logits.shape
-    if score not in _SCORES:
+    lib = _lib or _load()
+    s, g = _SCORES.get(score), _GROUP_SCORES.get(group_score)
+    if s is None:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    if group_score not in _GROUP_SCORES:
+    if g is None:
         raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
-    if topk < 1:
-        raise ValueError(f"topk={topk} must be positive")
-    shape = (T, topk)
-    if ids is None:
-        ids = _new(shape, torch.int32, dev, stream)
-    if weights is None:
-        weights = _new(shape, torch.float32, dev, stream)
-    _check((_lib or _load()).wna16_moe_route_scored(
-        logits.data_ptr(), ld, None if bias is None else _ptr(bias, dev, torch.float32, (E,), "bias"), T, E,
-        _TYPES[logits.dtype], _SCORES[score], groups, topk_groups, _GROUP_SCORES[group_score], topk,
-        1 if renormalize else 0, scale, _ptr(ids, dev, torch.int32, shape, "ids"),
-        _ptr(weights, dev, torch.float32, shape, "weights"), s))
+    if ids is None or weights is None:
+        if topk < 1:
+            raise ValueError(f"topk={topk} must be positive")
+        shape = (_matrix(logits, "logits")[0], topk)
+        ids = _new(shape, torch.int32, logits, stream) if ids is None else ids
+        weights = _new(shape, torch.float32, logits, stream) if weights is None else weights
+    rc = _host.route_scored(lib.block["route_scored"], logits, bias, ids, weights, s, groups, topk_groups, g, topk,
+                            1 if renormalize else 0, scale, stream)
+    if rc:
+        _check(rc)
     return ids, weights
 
 
 def linear_q8_workspace_size(T: int, K: int, N: int) -> int:
     return int((_lib or _load()).wna16_moe_linear_q8_workspace_size(T, K, N))
-
-
-def _scale_ptr(t, dev: int, n: int, name: str) -> int:
-    """Address of n fp32 scales, [n] or [n, 1]."""
-    return _ptr(t, dev, torch.float32, (n, 1) if isinstance(t, torch.Tensor) and t.dim() == 2 else (n,), name)
 
 
 def linear_q8(xq, x_scales, wq, w_scales, *, bias=None, addend=None, dtype=torch.bfloat16, out=None, workspace=None,
@@ -266,32 +204,17 @@ def linear_q8(xq, x_scales, wq, w_scales, *, bias=None, addend=None, dtype=torch
     [N] or [N, 1], bias fp32 [N], addend [T, N] of the output's type (out=addend
     adds in place).  workspace: uint8, at least linear_q8_workspace_size(T, K, N)
     bytes, holds the status word for read_status; may be left out."""
-    dev, s = _first(xq, "xq", stream)
-    if not isinstance(wq, torch.Tensor) or xq.dim() != 2 or wq.dim() != 2:
-        raise ValueError("xq and wq must be matrices")
-    T, K = xq.shape
-    N = wq.shape[0]
-    shape = (T, N)
-    if out is None:
-        out = _new(shape, dtype if addend is None else addend.dtype, dev, stream)
-    dtype = out.dtype
-    type_ = _TYPES.get(dtype)
-    if type_ is None:
-        raise TypeError(f"the output is bfloat16, float16 or float32, got {dtype}")
     lib = _lib or _load()
-    ws_ptr, ws_bytes = None, 0
+    if out is None:
+        out = _new((_matrix(xq, "xq")[0], _matrix(wq, "wq")[0]), dtype if addend is None else addend.dtype, xq, stream)
     if workspace is not None:
-        ws_bytes = workspace.numel()
-        ws_ptr = _ptr(workspace, dev, torch.uint8, (ws_bytes,), "workspace")
-        need = lib.wna16_moe_linear_q8_workspace_size(T, K, N)
-        if ws_bytes < need:   # (an empty tensor has no address to refuse)
-            raise binding.Wna16Error(binding.ERR_WORKSPACE_TOO_SMALL, f"workspace has {ws_bytes} bytes, needs {need}")
-    _check(lib.wna16_moe_linear_q8(
-        _ptr(xq, dev, torch.int8, (T, K), "xq"), _scale_ptr(x_scales, dev, T, "x_scales"),
-        _ptr(wq, dev, torch.int8, (N, K), "wq"), _scale_ptr(w_scales, dev, N, "w_scales"),
-        None if bias is None else _ptr(bias, dev, torch.float32, (N,), "bias"),
-        None if addend is None else _ptr(addend, dev, dtype, shape, "addend"), T, K, N, type_,
-        _ptr(out, dev, dtype, shape, "out"), ws_ptr, ws_bytes, s))
+        need = lib.wna16_moe_linear_q8_workspace_size(xq.shape[0], xq.shape[1], wq.shape[0])
+        if workspace.numel() < need:   # (an empty tensor has no address to refuse)
+            raise binding.Wna16Error(binding.ERR_WORKSPACE_TOO_SMALL,
+                                     f"workspace has {workspace.numel()} bytes, needs {need}")
+    rc = _host.linear_q8(lib.block["linear_q8"], xq, x_scales, wq, w_scales, bias, addend, out, workspace, stream)
+    if rc:
+        _check(rc)
     return out
 
 

@@ -2,7 +2,8 @@
 
 Compiles every ``csrc/*.cu`` translation unit in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and links a shared library next to
-this file.  Rebuilds only when a source or header is newer than the library.
+this file, and with the host compiler the CPython module ``_host`` (argument
+checks of the block operators).  Rebuilds only when a source or header is newer.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -22,6 +24,9 @@ LIB_PATH = os.path.join(HERE, "libwna16_moe.so")
 # WNA16_ERR_INDEX in the status word instead of accessing out of bounds
 DEBUG_BUILD_DIR = os.path.join(HERE, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(HERE, "libwna16_moe_debug.so")
+
+HOST_SOURCE = os.path.join(CSRC, "host_binding.c")
+HOST_PATH = os.path.join(HERE, "_host" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -61,9 +66,27 @@ def _compile(src: str, extra, build_dir: str = BUILD_DIR) -> str:
     return obj
 
 
+def build_host(force: bool = False) -> str:
+    """Build the CPython module of the argument checks if needed and return its path."""
+    deps = [HOST_SOURCE, os.path.abspath(__file__), *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and os.path.exists(HOST_PATH) and all(os.path.getmtime(d) <= os.path.getmtime(HOST_PATH) for d in deps):
+        return HOST_PATH
+    tmp = HOST_PATH + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-std=gnu11", "-Wall", "-Wextra", "-shared", "-fPIC", "-I",
+           sysconfig.get_paths()["include"], HOST_SOURCE, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"host compiler failed for {HOST_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    if r.stderr.strip():
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, HOST_PATH)
+    return HOST_PATH
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
-    """Build the library (or, with debug, the bounds-checked library) if
-    needed and return its path."""
+    """Build the library (or, with debug, the bounds-checked library) and the
+    host module if needed and return the library's path."""
+    build_host(force)
     lib = DEBUG_LIB_PATH if debug else LIB_PATH
     build_dir = DEBUG_BUILD_DIR if debug else BUILD_DIR
     if not force and up_to_date(lib):
