@@ -391,25 +391,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
     } else if (warp >= kFirstA && warp < kFirstEpilogue) {
         // Converters.  Set s of either kind takes the k half s of every stage.
+        // Chunk c of a row lies at chunk c ^ (row & 7) of its 128 bytes (the swizzle), so
+        // with the row's part of that in an address, c enters by one exclusive or.
         const bool is_b = warp >= kFirstB;
         const uint32_t set = static_cast<uint32_t>(warp - (is_b ? kFirstB : kFirstA)) / kSet;
-        const int row = (warp & 3) * 32 + lane;                 // row of A (= TMEM lane) or of this CTA's half of B
-        const uint32_t xr = static_cast<uint32_t>(row) & 7u;   // 128-byte swizzle
-        const uint32_t bfull0 = map_shared(smem_u32(bfull), leader);
+        const uint32_t row = static_cast<uint32_t>((warp & 3) * 32 + lane);   // row of A (= TMEM lane) or of this CTA's half of B
+        const uint32_t bfull0 = map_shared(smem_u32(bfull), leader), bempty0 = smem_u32(bempty), full0 = smem_u32(full);
+        const uint32_t to_empty = static_cast<uint32_t>(kStages) * 8;
         // put(buffer, fp16 pairs): 64 converted codes of the row into operand buffer `buffer`
-        auto convert = [&](const uint8_t* codes, int code_bytes, auto&& put) {
-            Slot st, bs;
+        auto convert = [&](uint32_t codes, uint32_t code_bytes, auto&& put) {
+            uint32_t src = codes ^ ((4 * set) << 4), bar = full0, phase = 0;   // this stage's codes and barrier
+            uint32_t buf = 0, buf_phase = 1;
             for (int v = first; v < items; v += stride) {
-                for (int kb = kb0; kb < kb1; ++kb, st.next(kStages), bs.next(kBufs)) {
-                    const uint32_t bph = bs.phase ^ 1u;
-                    if (!mbar_wait(&full[st.i], st.phase, abort_flag, status)) return;
-                    const bool ready = mbar_test_wait(smem_u32(&bempty[bs.i]), bph);
-                    const uint8_t* src = codes + st.i * code_bytes;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait_at(bar, phase, abort_flag, status)) return;
+                    const bool ready = mbar_test_wait(bempty0 + buf * 8, buf_phase);
                     uint4 raw[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + (((4 * set + c) ^ xr) << 4));
+                    for (uint32_t c = 0; c < 4; ++c) raw[c] = ld_shared_16(src ^ (c << 4));
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[st.i]);   // the codes are in registers: the slot refills meanwhile
+                    if (lane == 0) mbar_arrive_at(bar + to_empty);   // the codes are in registers: the slot refills meanwhile
+                    src += code_bytes;
+                    bar += 8;
+                    if (bar == full0 + to_empty) {
+                        bar = full0;
+                        src -= kStages * code_bytes;
+                        phase ^= 1u;
+                    }
                     uint32_t a[32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -421,29 +429,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             a[c * 8 + j * 2 + 1] = h.y;
                         }
                     }
-                    if (!ready && !mbar_wait(&bempty[bs.i], bph, abort_flag, status)) return;
-                    put(bs.i, a);
+                    if (!ready && !mbar_wait_at(bempty0 + buf * 8, buf_phase, abort_flag, status)) return;
+                    put(buf, a);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(bfull0 + bs.i * 8);
+                    if (lane == 0) mbar_arrive_cluster(bfull0 + buf * 8);
+                    buf = (buf + 1) % kBufs;
+                    buf_phase ^= buf == 0 ? 1u : 0u;
                 }
             }
         };
         if (is_b) {
-            const bool live = row < brows;   // a tile of fewer than 256 rows leaves threads without one
-            uint8_t* dst0 = sH + set * (h_bytes / 2) + row * (kHalfK * 2);
-            convert(sB + (live ? row : 0) * kStageK, b_bytes, [&](int b, const uint32_t (&a)[32]) {
+            const bool live = row < static_cast<uint32_t>(brows);   // a tile of fewer than 256 rows leaves threads without one
+            const uint32_t r = live ? row : 0;
+            const uint32_t dst0 = smem_u32(sH) + set * (h_bytes / 2) + r * (kHalfK * 2) + ((r & 7u) << 4);
+            convert((smem_u32(sB) + r * kStageK) ^ ((r & 7u) << 4), b_bytes, [&](uint32_t b, const uint32_t (&a)[32]) {
                 if (live) {
-                    uint8_t* dst = dst0 + b * h_bytes;
+                    const uint32_t dst = dst0 + b * h_bytes;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(dst + ((static_cast<uint32_t>(j) ^ xr) << 4)) =
-                            make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+                    for (uint32_t j = 0; j < 8; ++j) st_shared_16(dst ^ (j << 4), a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
                 }
                 fence_proxy_async_shared();
             });
         } else {
             const uint32_t a0 = tmem + kACol + set * (kHalfK / 2) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            convert(sA + row * kStageK, a_bytes, [&](int b, const uint32_t (&a)[32]) {
+            convert((smem_u32(sA) + row * kStageK) ^ ((row & 7u) << 4), a_bytes, [&](uint32_t b, const uint32_t (&a)[32]) {
                 tc_fence_after();
                 tc_st_32x32b_x32(a0 + b * (kStageK / 2), a);
                 tc_wait_st();
