@@ -91,6 +91,9 @@ NORM_CASES = [
     (9, 1, BF, BF, True, I8, 0), (9, 3, HF, HF, False, E4, 0), (11, 1021, BF, BF, True, I8, 0),
     (6, 4097, FP, FP, True, E4, 0), (3, 24577, BF, FP, True, I8, 0), (17, 32, BF, BF, True, E4, 32),
     (2500, 96, BF, BF, True, I8, 32),
+    # more rows than are worked on at the same time, and the sizes with two and four chunks per thread
+    (3000, 4096, BF, BF, True, I8, 0), (512, 4096, BF, BF, True, I8, 0), (1500, 8192, HF, HF, False, E4, 64),
+    (700, 12288, BF, BF, True, I8, 256),
 ]
 
 
@@ -172,7 +175,8 @@ def test_rows_without_a_scale(moe):
 
 @pytest.mark.parametrize("T,N,dt,L,qt,group", [
     (1, 2048, BF, 7.0, I8, 0), (4, 2048, BF, 7.0, E4, 128), (33, 512, HF, 7.0, I8, 64), (5, 1001, BF, 7.0, I8, 0),
-    (3, 9000, FP, float("inf"), I8, 0), (700, 128, BF, 1.5, E4, 32), (2, 1, BF, 7.0, I8, 0), (2, 32768, BF, 7.0, I8, 0)])
+    (3, 9000, FP, float("inf"), I8, 0), (700, 128, BF, 1.5, E4, 32), (2, 1, BF, 7.0, I8, 0), (2, 32768, BF, 7.0, I8, 0),
+    (3000, 2048, BF, 7.0, I8, 0), (900, 12288, HF, 7.0, E4, 0), (40, 64, BF, float("inf"), E4, 64)])
 def test_swiglu(moe, T, N, dt, L, qt, group):
     gu = randn(T, 2 * N, seed=N, dtype=dt, scale=4.0)
     gu[0, 0] = -200.0
@@ -330,6 +334,30 @@ def test_route_of_nearly_equal_scores(moe, score):
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,Gk", [(1, 1), (8, 3), (4, 2)])
+def test_route_when_all_scores_are_nearly_equal(moe, score, G, Gk):
+    """More values within fp32's error of one another than are collected at a time."""
+    T, E = 60, 256
+    logits = randn(T, E, seed=16)
+    logits[1:] = logits[0]
+    z = logits[0].double()
+    s = 1 / (1 + torch.exp(-z)) if score == "sigmoid" else torch.softmax(z, 0)
+    bias = (s.max() - s).float()                                    # every choice value is s.max() to fp32
+    logits += torch.linspace(0, 1e-6, T, device="cuda")[:, None]
+    for k in (1, 8, 32):
+        check_route(moe, logits, k, score=score, bias=bias, G=G, Gk=Gk)
+
+
+@pytest.mark.parametrize("k", [1, 7, 15, 16, 24, 31, 32])
+def test_route_topk_sizes(moe, k):
+    """The bound below the chosen ones comes from the lanes' best or second best values, by k and the lanes in play."""
+    for E, G, Gk in ((1024, 1, 1), (256, 8, 8), (256, 8, 2), (512, 16, 3), (64, 1, 1), (96, 3, 1)):
+        if k <= Gk * (E // G):
+            check_route(moe, randn(90, E, seed=k + E), k, bias=randn(E, seed=E, scale=0.05), G=G, Gk=Gk)
+            check_route(moe, randn(90, E, seed=k + E + 1, dtype=BF), k, score="softmax", G=G, Gk=Gk, group_score="max")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_route_masked_experts(moe, score):
     inf = float("inf")
     logits = randn(12, 32, seed=7)
@@ -392,6 +420,10 @@ LINEAR_CASES = [
     (33, 4096, 512, FP), (64, 16, 1, FP), (64, 4096, 4096, BF), (65, 1040, 129, FP), (77, 2048, 1000, BF),
     (128, 4096, 128, HF), (129, 80, 257, FP), (200, 4096, 1408, FP), (255, 2064, 300, FP), (256, 4096, 4096, BF),
     (257, 1024, 1023, FP), (512, 8192, 640, FP), (1000, 4096, 2050, BF), (2048, 512, 4096, FP), (3001, 1008, 777, FP),
+    # few tokens, many blocks; sums of more than 1024 products per warp
+    (4, 256, 5003, BF), (13, 512, 6000, FP), (30, 128, 8000, HF), (3, 65536, 40, FP), (20, 16384, 16, FP),
+    # tokens on the M side, with ragged tiles of them
+    (3001, 1008, 784, BF), (2500, 256, 1040, HF), (4100, 128, 512, BF), (5000, 1040, 4096, BF), (1700, 2048, 1408, FP),
 ]
 
 

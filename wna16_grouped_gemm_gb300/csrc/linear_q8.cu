@@ -409,8 +409,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     uint4 raw[4];
 #pragma unroll
                     for (uint32_t c = 0; c < 4; ++c) raw[c] = ld_shared_16(src ^ (c << 4));
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(bar + to_empty);   // the codes are in registers: the slot refills meanwhile
+                    const uint32_t slot_empty = bar + to_empty;
                     src += code_bytes;
                     bar += 8;
                     if (bar == full0 + to_empty) {
@@ -432,7 +431,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (!ready && !mbar_wait_at(bempty0 + buf * 8, buf_phase, abort_flag, status)) return;
                     put(buf, a);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(bfull0 + buf * 8);
+                    // The slot is given back only here, where every word read from it has been used.
+                    // An arrival does not wait for the data of loads issued before it: right after
+                    // them, the loads were served after the refill where the epilogue filled the
+                    // memory pipe (an addend, fp32 results), and the sums were wrong.
+                    if (lane == 0) {
+                        mbar_arrive_at(slot_empty);
+                        mbar_arrive_cluster(bfull0 + buf * 8);
+                    }
                     buf = (buf + 1) % kBufs;
                     buf_phase ^= buf == 0 ? 1u : 0u;
                 }
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto load_acc = [&](int column, float (&v)[16]) {
         uint32_t d[16];
         tc_ld_32x32b_x16(tmem + lane_base + static_cast<uint32_t>(column), d);
-        tc_wait_ld();
+        tc_wait_ld_of(d);
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = done ? __uint_as_float(d[i]) : NAN;
     };

@@ -417,6 +417,16 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// tc_wait_ld for the values of one load: they pass through it, so that nothing is
+// computed from them before the wait (which names no registers itself).
+__device__ __forceinline__ void tc_wait_ld_of(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- clusters and CTA pairs
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
