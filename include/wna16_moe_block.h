@@ -106,12 +106,13 @@ WNA16_API int wna16_moe_route_scored(const void* logits, int64_t ld, const float
  *   bias fp32 [N] or NULL, addend [T, N] of `type` or NULL (may be out),
  *   out [T, N] of `type`; all contiguous
  * K a multiple of 16, at most 65536; xq and wq 16-byte aligned.  The sums are
- * 32-bit integers for small batches; for larger ones fp32 sums of exact
+ * 32-bit integers for up to 32 tokens, and for more where the weights have few
+ * channels; for other calls fp32 sums of exact
  * products on the tensor cores, which are the same integers while every
  * partial sum stays below 2^24 (always for K <= 1024), and otherwise off by a
  * relative 2^-23 per 16 k at most.  Workspace (256-byte aligned): its first
  * word is the status word of wna16_moe_read_status, the size is below (0 for
- * small batches).  It may be NULL: the status word is then not readable; an
+ * up to 32 tokens).  It may be NULL: the status word is then not readable; an
  * output whose sums are missing after a device timeout is NaN either way. */
 WNA16_API int wna16_moe_linear_q8(const int8_t* xq, const float* x_scales, const int8_t* wq, const float* w_scales,
                                   const float* bias, const void* addend, int64_t T, int64_t K, int64_t N, int type,

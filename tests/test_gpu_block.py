@@ -422,6 +422,11 @@ LINEAR_CASES = [
     (257, 1024, 1023, FP), (512, 8192, 640, FP), (1000, 4096, 2050, BF), (2048, 512, 4096, FP), (3001, 1008, 777, FP),
     # few tokens, many blocks; sums of more than 1024 products per warp
     (4, 256, 5003, BF), (13, 512, 6000, FP), (30, 128, 8000, HF), (3, 65536, 40, FP), (20, 16384, 16, FP),
+    # more than 32 tokens with few channels, in groups of 32 and of fewer; the last group with one token
+    (33, 128, 17, FP), (40, 512, 512, HF), (97, 2048, 1000, BF), (600, 1024, 256, FP), (1000, 128, 64, BF),
+    # and with many channels: small tiles of tokens, an odd number of channels
+    (40, 256, 8192, BF), (100, 512, 4096, FP), (70, 2048, 8192, HF), (300, 16, 5003, FP), (129, 80, 6001, FP),
+    (1000, 4096, 1025, FP),
     # tokens on the M side, with ragged tiles of them
     (3001, 1008, 784, BF), (2500, 256, 1040, HF), (4100, 128, 512, BF), (5000, 1040, 4096, BF), (1700, 2048, 1408, FP),
 ]
@@ -433,7 +438,7 @@ def test_linear(moe, T, K, N, dt):
     check_linear(moe, T, K, N, dt, bias=True, addend=True, seed=T + K + 7)
 
 
-@pytest.mark.parametrize("T", [4, 40, 300])
+@pytest.mark.parametrize("T", [4, 40, 300, 3000])
 def test_linear_extreme_codes(moe, T):
     """All codes -128 or 127: sums of K * 2^14 leave the range in which fp32 sums
     are exact; small batches add integers, larger ones stay within 2^-23 per 16 k."""

@@ -1,10 +1,12 @@
 // Product of 8-bit integers with a scale per token and per output channel:
 //   out[t][n] = (sum_k xq[t][k] wq[n][k]) xs[t] ws[n] (+ bias[n]) (+ addend[t][n])
 //
-// Two kernels, by the number of tokens:
+// Two kernels: small_kernel up to 32 tokens and where it is estimated to be faster
+// (few channels: a tile's prologue, ring and join take 4 us), else tile_kernel.
 //
-// small_kernel (a few tokens): bound by the weights' bytes.  A block owns 16
-// output channels; its 8 warps take the K range in turns of 64, each lane
+// small_kernel: bound by the weights' bytes.  A block owns 16
+// output channels and up to 32 tokens (the weights come from L2 for the second and
+// later groups of tokens); its 8 warps take the K range in turns of 64, each lane
 // loading 16 consecutive bytes of two weight rows and of a token straight into
 // registers, where they become the fp16 operands of four mma.sync m16n8k16 (the
 // order of k inside a product is free, so both operands use the order in which
@@ -13,7 +15,7 @@
 // 8-bit integers, a 40th of the fp16 rate on this chip: 4 x 4096 x 4096 5.0 us,
 // 32 x 4096 x 4096 17.6 us.)
 //
-// tile_kernel (many tokens): bound by the tensor cores.  sm_103a has no 8-bit
+// tile_kernel: bound by the tensor cores.  sm_103a has no 8-bit
 // integer kind of tcgen05.mma, but 8-bit integers are exact in fp16, and their
 // products and sums (below 2^24) exact in the fp32 accumulator, so the
 // codes run through kind::f16.  A pair of CTAs (cta_group::2) owns 256 rows of
@@ -32,7 +34,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "../../include/wna16_moe_block.h"
@@ -99,23 +103,24 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 
 // NT tiles of 8 tokens; U steps of 64 k in flight per warp, at least BLOCKS blocks per SM
 template <typename T, int NT, int U, int BLOCKS>
-__global__ void __launch_bounds__(32 * kSmallWarps, BLOCKS) small_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(32 * kSmallWarps, BLOCKS) small_kernel(const LinearParams p, int* status) {
     __shared__ int part[kSmallWarps][kSmallRows][NT * 8 + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
-    const int n0 = blockIdx.x * kSmallRows;
+    const int n0 = blockIdx.x * kSmallRows, t0 = blockIdx.y * NT * 8;
     const int K = p.K;
     // the block's weights on their way to L2 while the kernel before finishes (nothing of them is used)
     for (int64_t i = threadIdx.x * 128; i < static_cast<int64_t>(min(kSmallRows, p.N - n0)) * K; i += 32 * kSmallWarps * 128)
         prefetch_l2(p.wq + static_cast<int64_t>(n0) * K + i);
     pdl_wait();
     pdl_trigger();
+    if (status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = kStatusOk;
     // rows past the end read the last one; their results are not stored
     const int8_t* w0 = p.wq + static_cast<int64_t>(min(n0 + g, p.N - 1)) * K;
     const int8_t* w1 = p.wq + static_cast<int64_t>(min(n0 + g + 8, p.N - 1)) * K;
     const int8_t* x[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) x[j] = p.xq + static_cast<int64_t>(min(j * 8 + g, p.T - 1)) * K;
+    for (int j = 0; j < NT; ++j) x[j] = p.xq + static_cast<int64_t>(min(t0 + j * 8 + g, p.T - 1)) * K;
 
     int sum[NT][4] = {};
     float acc[NT][4] = {};
@@ -175,12 +180,12 @@ __global__ void __launch_bounds__(32 * kSmallWarps, BLOCKS) small_kernel(const L
     }
     __syncthreads();
     for (int i = threadIdx.x; i < kSmallRows * NT * 8; i += 32 * kSmallWarps) {
-        const int r = i % kSmallRows, t = i / kSmallRows;
+        const int r = i % kSmallRows, tt = i / kSmallRows, t = t0 + tt;
         const int n = n0 + r;
         if (n >= p.N || t >= p.T) continue;
         int total = 0;
 #pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) total += part[w][r][t];
+        for (int w = 0; w < kSmallWarps; ++w) total += part[w][r][tt];
         float v = static_cast<float>(total) * __ldg(p.xs + t) * __ldg(p.ws + n);
         if (p.bias) v += __ldg(p.bias + n);
         const int64_t o = static_cast<int64_t>(t) * p.N + n;
@@ -642,7 +647,11 @@ constexpr int kSmallTokens = 32;   // up to here: small_kernel
 // stores); the join of a shared K.
 constexpr double kStageCycles = 1250, kColumnCycles = 21, kRowColumnCycles = 8, kJoinCycles = 3000, kJoinColumnCycles = 20;
 
+// Launch, prologue and exit of a call (tile_kernel, small_kernel), a block of small_kernel, and 1024 k of its 32 tokens.
+constexpr double kTileCycles = 4500, kSmallCycles = 3800, kSmallBlockCycles = 1000, kSmallKCycles = 1500;
+
 struct Plan {
+    double cycles = 0.0;   // estimated time
     bool tokens_m = false;
     int nt = 0, ksplit = 1, kblocks = 0, m_tiles = 0, c_tiles = 0;
 };
@@ -652,7 +661,6 @@ struct Plan {
 // tokens on the M side lose: 3000 x 1024 x 1000 41 us against 14).
 Plan make_plan(int64_t T, int64_t K, int64_t N, bool wide, const int (&active)[kMaxSplit]) {
     Plan best;
-    double least = 0.0;
     const int kblocks = static_cast<int>((K + kStageK - 1) / kStageK);
     for (int tm = 0; tm < (wide ? 2 : 1); ++tm) {
         const int64_t a_len = tm ? T : N, b_len = tm ? N : T;
@@ -669,9 +677,9 @@ Plan make_plan(int64_t T, int64_t K, int64_t N, bool wide, const int (&active)[k
                 const int64_t waves = (tiles + active[ks - 1] - 1) / active[ks - 1];
                 if (ks > 1 && waves > 1) break;   // (only ever faster for a single wave)
                 const int64_t per = (kblocks + ks - 1) / ks;
-                const double cost = waves * (per * stage + nt * column) + (ks > 1 ? kJoinCycles + nt * kJoinColumnCycles : 0);
-                if (best.nt == 0 || cost < least) {
-                    least = cost;
+                const double cost = kTileCycles + waves * (per * stage + nt * column) + (ks > 1 ? kJoinCycles + nt * kJoinColumnCycles : 0);
+                if (best.nt == 0 || cost < best.cycles) {
+                    best.cycles = cost;
                     best.tokens_m = tm != 0;
                     best.nt = static_cast<int>(nt);
                     best.ksplit = ks;
@@ -685,6 +693,17 @@ Plan make_plan(int64_t T, int64_t K, int64_t N, bool wide, const int (&active)[k
     return best;
 }
 
+// Estimated time of small_kernel for more than kSmallTokens tokens (32 per block).  Few channels leave
+// tile_kernel few tiles, each with the time of a pair's prologue, ring and join; tile_kernel / small_kernel (us):
+//   33 x 2048 x 1000 7.7 / 3.7    77 x 2048 x 1000 8.1 / 5.1    128 x 4096 x 1024 10.2 / 7.9   64 x 512 x 512 6.0 / 2.5
+//   64 x 4096 x 4096 12.8 / 15.0   100 x 512 x 4096 6.4 / 9.6    256 x 8192 x 512 14.4 / 13.1   40 x 2048 x 4096 9.4 / 8.9
+double small_cycles(int64_t T, int64_t K, int64_t N, int sms) {
+    const int64_t groups = (T + kSmallTokens - 1) / kSmallTokens;
+    const double per_sm = static_cast<double>(groups * ((N + kSmallRows - 1) / kSmallRows)) / sms;
+    if (groups > 65535) return HUGE_VAL;   // a grid's limit
+    return kSmallCycles + std::max(per_sm, 1.0) * (kSmallBlockCycles + kSmallKCycles * static_cast<double>(K) / 1024.0);
+}
+
 // Steps in flight and blocks per SM, measured (us) with the weights streamed from memory:
 //   tokens x 4096 x N      4, 4096   4, 32768   16, 4096   16, 32768   32, 4096
 //   chosen                 4.7       24.0       6.0        32.7        8.2
@@ -692,16 +711,20 @@ Plan make_plan(int64_t T, int64_t K, int64_t N, bool wide, const int (&active)[k
 //   twice the steps        4.9       29.8       6.1        34.9        10.3
 // More blocks hide one another's loads and ends where there are several turns of
 // them; with one turn (at most two blocks per SM) registers for loads count.
+// Tokens per block: the fewest of 8, 16, 32 that hold all or leave one block per SM.
 template <typename T>
-cudaError_t launch_small(const LinearParams& p, int sms, cudaStream_t s) {
-    const int blocks = (p.N + kSmallRows - 1) / kSmallRows;
-    const dim3 grid(static_cast<unsigned>(blocks)), block(32 * kSmallWarps);
-    const bool turns = blocks > 2 * sms;
-    if (p.T <= 8)
-        return launch_pdl(turns ? small_kernel<T, 1, 4, 3> : small_kernel<T, 1, 4, 2>, grid, block, 0, s, p);
-    if (p.T <= 16)
-        return launch_pdl(turns ? small_kernel<T, 2, 2, 4> : small_kernel<T, 2, 2, 2>, grid, block, 0, s, p);
-    return launch_pdl(small_kernel<T, 4, 2, 2>, grid, block, 0, s, p);
+cudaError_t launch_small(const LinearParams& p, int sms, int* status, cudaStream_t s) {
+    const int64_t channels = (p.N + kSmallRows - 1) / kSmallRows;
+    auto blocks = [&](int nt) { return channels * ((p.T + 8 * nt - 1) / (8 * nt)); };
+    int nt = p.T <= 8 ? 1 : p.T <= 16 ? 2 : 4;
+    while (nt > 1 && blocks(nt / 2) <= sms) nt /= 2;
+    const dim3 grid(static_cast<unsigned>(channels), static_cast<unsigned>(blocks(nt) / channels)), block(32 * kSmallWarps);
+    const bool turns = blocks(nt) > 2 * sms;
+    if (nt == 1)
+        return launch_pdl(turns ? small_kernel<T, 1, 4, 3> : small_kernel<T, 1, 4, 2>, grid, block, 0, s, p, status);
+    if (nt == 2)
+        return launch_pdl(turns ? small_kernel<T, 2, 2, 4> : small_kernel<T, 2, 2, 2>, grid, block, 0, s, p, status);
+    return launch_pdl(small_kernel<T, 4, 2, 2>, grid, block, 0, s, p, status);
 }
 
 int cuda_error(cudaError_t e, const char* what) {
@@ -815,11 +838,14 @@ template <typename T>
 int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
     int sms = 0, max_smem = 0;
     if (int rc = device_limits(sms, max_smem)) return rc;
-    if (p.T <= kSmallTokens) return cuda_error(launch_small<T>(p, sms, s), "8-bit linear launch");
+    int* status = p.T <= kSmallTokens ? nullptr : static_cast<int*>(workspace);
+    auto small = [&] { return cuda_error(launch_small<T>(p, sms, status, s), "8-bit linear launch"); };
+    if (p.T <= kSmallTokens) return small();
     int active[kMaxSplit];
     if (int rc = active_clusters(tile_kernel<T, false, false>, max_smem, active)) return rc;
     const bool wide = p.N % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
     const Plan L = make_plan(p.T, p.K, p.N, wide, active);
+    if (small_cycles(p.T, p.K, p.N, sms) < L.cycles) return small();
     if (!L.tokens_m) return launch_tiles<T, false, false>(p, L, max_smem, active[0], workspace, s);
     // ALT / not (us), items one after another: 2048 x 4096 x 4096 45 / 47, 4096 x 4096 x 4096 83 / 90, 6000 x
     // 4096 x 4096 123 / 133; 8192 x 4096 x 4096 157 / 157 (power).  One each: 1024 x 4096 x 4096 26.5 / 26.1.
