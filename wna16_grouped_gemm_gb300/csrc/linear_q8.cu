@@ -438,16 +438,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (h == 0 && !ready && !mbar_wait_at(bempty0 + buf * 8, buf_phase, abort_flag, status)) return;
                     put(buf, h, a);
                 }
-                placed();
-                __syncwarp();
-                // The slot is given back only here, where every word read from it has been used.
+                // The slot is given back only when every word read from it has been used by a store.
                 // An arrival does not wait for the data of loads issued before it: right after
                 // them, the loads were served after the refill where the epilogue filled the
                 // memory pipe (an addend, fp32 results), and the sums were wrong.
-                if (lane == 0) {
-                    mbar_arrive_at(empty_at);
-                    mbar_arrive_cluster(bfull0 + buf * 8);
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(empty_at);
+                placed();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(bfull0 + buf * 8);
                 src += kStep * code_bytes;
                 empty_at += kStep * 8;
                 if (empty_at >= empty0 + kStages * 8) {
