@@ -217,9 +217,9 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
 constexpr int kM = 128;            // rows of A per CTA (256 per pair)
 constexpr int kStageK = 128;       // k per stage of codes: one 128-byte swizzle row
 constexpr int kHalfK = 64;         // k per converter set and stage: 32 TMEM columns, one 128-byte swizzle row of fp16
-constexpr int kStages = 3;
-constexpr int kBufs = 4;           // operand buffers, one stage each: 64 TMEM columns, two swizzle atoms of fp16
-static_assert(kBufs % 2 == 0, "a set that takes every other stage keeps to its own buffers");
+constexpr int kStages = 4;
+constexpr int kBufs = 3;           // operand buffers, one stage each: 64 TMEM columns, two swizzle atoms of fp16
+static_assert(kStages % 2 == 0, "a set of converters that takes every other stage keeps to its own slots");
 constexpr int kMaxSplit = 4;
 constexpr int kProducer = 0, kIssuer = 1, kAlloc = 2;
 constexpr int kFirstA = 4, kFirstB = 12, kFirstEpilogue = 20;   // 8 warps each, in two sets of 4
@@ -227,7 +227,7 @@ constexpr int kSet = 4, kEpilogues = 8;
 constexpr int kTileThreads = 32 * (kFirstEpilogue + kEpilogues);
 constexpr int kCols = 512;
 constexpr uint32_t kACol = 256;    // TMEM: accumulator in columns 0..nt-1, operand buffers from here
-constexpr int kBars = 3 * kStages + 2 * kBufs + 3;
+constexpr int kBars = 2 * kStages + 3 * kBufs + 3;
 constexpr int kMaxCols = 256;      // rows of B per tile (columns of the result)
 
 struct TileParams {
@@ -240,8 +240,8 @@ struct TileParams {
     int* status = nullptr;
 };
 
-// Operand A: the weights, B: the tokens; with TM the other way round.  ALT: see the converters.
-template <typename T, bool TM, bool ALT>
+// Operand A: the weights, B: the tokens; with TM the other way round.
+template <typename T, bool TM>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const TileParams tp) {
@@ -253,7 +253,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t leader = rank & ~1u, side = rank & 1u;
     const int split = static_cast<int>(rank >> 1);
     const int nt = tp.nt, brows = nt / 2, ksplit = tp.ksplit;
-    constexpr int kSets = ALT ? 1 : 2;   // sets of converters that take a part of one stage
     constexpr int a_bytes = kM * kStageK;
     const int b_bytes = brows * kStageK;
     const int h_bytes = brows * kStageK * 2;
@@ -262,12 +261,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint8_t* sH = sB + kStages * b_bytes;      // B's codes as fp16
     float* sScale = reinterpret_cast<float*>(sH + kBufs * h_bytes);   // the scales of B's rows
     uint64_t* full = reinterpret_cast<uint64_t*>(sScale + kMaxCols);
-    // Two full barriers per slot, in turns: with three slots a set that takes every other stage meets
-    // a slot again two turns later, and a wait by parity must not take the turn between for its own.
-    uint64_t* empty = full + 2 * kStages;
+    uint64_t* empty = full + kStages;
     uint64_t* bfull = empty + kStages;         // the leader's: both CTAs' operands of a buffer are in place
+    // Two bempty barriers per buffer, in turns: a set of converters that takes every other stage meets one of
+    // three buffers again two turns later, and a wait by parity must not take the turn between for its own.
     uint64_t* bempty = bfull + kBufs;
-    uint64_t* accfull = bempty + kBufs;
+    uint64_t* accfull = bempty + 2 * kBufs;
     uint64_t* accempty = accfull + 1;          // the leader's
     uint64_t* drain = accempty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -277,12 +276,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&full[kStages + i], 1);
-            mbar_init(&empty[i], 2 * kSets * kSet);    // the sets of both kinds of converters
+            mbar_init(&empty[i], 2 * kSet);    // a set of either kind of converters
         }
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&bfull[i], 2 * 2 * kSets * kSet);   // those of both CTAs
+            mbar_init(&bfull[i], 2 * 2 * kSet);   // those of both CTAs
             mbar_init(&bempty[i], 1);
+            mbar_init(&bempty[kBufs + i], 1);
         }
         mbar_init(accfull, 1);
         mbar_init(accempty, 2 * kEpilogues);
@@ -319,27 +318,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) {
             const uint64_t pol = policy_evict_normal();
             const uint32_t tx = static_cast<uint32_t>(a_bytes + b_bytes);
-            Slot st, sf;
+            Slot st;
             uint32_t kc = 0;   // stages so far
             bool ok = true;
             for (int v = first; v < items && ok; v += stride) {
                 const int a0 = a_row(v), b0 = b_row(v) + static_cast<int>(side) * brows;
-                for (int kb = kb0; kb < kb1; ++kb, ++kc, st.next(kStages), sf.next(2 * kStages)) {
+                for (int kb = kb0; kb < kb1; ++kb, ++kc, st.next(kStages)) {
                     const int slot = st.i;
                     if (!mbar_wait(&empty[slot], st.phase ^ 1u, abort_flag, status)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[sf.i], tx);
-                    tma_load_3d(sA + slot * a_bytes, &tm_a, &full[sf.i], kb * kStageK, a0, 0, pol);
-                    tma_load_3d(sB + slot * b_bytes, &tm_b, &full[sf.i], kb * kStageK, b0, 0, pol);
+                    mbar_arrive_expect_tx(&full[slot], tx);
+                    tma_load_3d(sA + slot * a_bytes, &tm_a, &full[slot], kb * kStageK, a0, 0, pol);
+                    tma_load_3d(sB + slot * b_bytes, &tm_b, &full[slot], kb * kStageK, b0, 0, pol);
                 }
             }
             // no copy may be in flight when the block ends: wait for the last issue of every slot
             for (uint32_t c = kc > kStages ? kc - kStages : 0; c < kc; ++c) {
-                const uint32_t a = smem_u32(&full[c % (2 * kStages)]);
+                const uint32_t a = smem_u32(&full[c % kStages]);
                 const uint64_t b = globaltimer_ns();
-                while (!mbar_try_wait(a, (c / (2 * kStages)) & 1u)) {
+                while (!mbar_try_wait(a, (c / kStages) & 1u)) {
                     if (globaltimer_ns() - b > kWaitLimitNs) {
                         atomicExch(status, kStatusTimeout);
                         break;
@@ -357,7 +356,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // f16 A and B, f32 D, both K-major, 256 x nt
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>((2 * kM) >> 4) << 24);
             const uint16_t mask = static_cast<uint16_t>(3u << rank);
-            Slot bs;
+            Slot bs, be;   // operand buffer, and the barrier that the stage after next but one there waits for
+            be.i = kBufs;
             uint32_t it = 0;
             bool ok = true, issued = false;
             for (int v = first; v < items && ok; v += stride, ++it) {
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     ok = false;
                     break;
                 }
-                for (int kb = kb0; kb < kb1; ++kb, bs.next(kBufs)) {
+                for (int kb = kb0; kb < kb1; ++kb, bs.next(kBufs), be.next(2 * kBufs)) {
                     const int b = bs.i;
                     if (!warp_wait(&bfull[b], bs.phase)) {
                         ok = false;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         for (int k16 = 0; k16 < kStageK / 16; ++k16)
                             tc_mma_ts_pair(tmem, a0 + k16 * 8, b_lo + (k16 >> 2) * atom + (k16 & 3) * 2,
                                            kSmemDescSw128Hi, idesc, kb > kb0 || k16 > 0 ? 1u : 0u);
-                        tc_commit_pair(&bempty[b], mask);
+                        tc_commit_pair(&bempty[be.i], mask);
                         if (kb + 1 == kb1) tc_commit_pair(accfull, mask);
                     }
                     __syncwarp();
@@ -400,29 +400,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
     } else if (warp >= kFirstA && warp < kFirstEpilogue) {
-        // Converters.  Set s of either kind takes the k half s of every stage, so that a stage is
-        // ready soon, or with ALT all of the stages s, s + 2, .., with half the waits and arrivals.
+        // Converters.  Set s of either kind takes the stages s, s + 2, .. (A half of every stage per
+        // set, with twice the waits and arrivals: 2048 x 4096 x 4096 45.3 us against 42.6, 2500 x 8192 x
+        // 1536 44.7 against 39.7; only products of a few stages were faster, 100 x 512 x 4096 6.4 against 6.6.)
         // Chunk c of a row lies at chunk c ^ (row & 7) of its 128 bytes (the swizzle), so
         // with the row's part of that in an address, c enters by one exclusive or.
-        constexpr uint32_t kStep = 3 - kSets, kHalves = 3 - kSets;
         const bool is_b = warp >= kFirstB;
         const uint32_t set = static_cast<uint32_t>(warp - (is_b ? kFirstB : kFirstA)) / kSet;
         const uint32_t row = static_cast<uint32_t>((warp & 3) * 32 + lane);   // row of A (= TMEM lane) or of this CTA's half of B
         const uint32_t bfull0 = map_shared(smem_u32(bfull), leader), bempty0 = smem_u32(bempty), empty0 = smem_u32(empty);
-        const uint32_t full0 = smem_u32(full);
-        const uint32_t half0 = kSets == 1 ? 0 : set, stage0 = kSets == 1 ? set : 0;   // this set's first half and stage
         const uint32_t turns = first < items ? static_cast<uint32_t>((items - 1 - first) / stride + 1) : 0;
         const uint32_t total = turns * static_cast<uint32_t>(kb1 - kb0);
-        // put(buffer, h, fp16 pairs): 64 converted codes of the row, for half half0 + h of operand
-        // buffer `buffer`; placed(): after the last
+        // put(buffer, h, fp16 pairs): 64 converted codes of the row, for the k half h of operand buffer
+        // `buffer`; placed(): after both
         auto convert = [&](uint32_t codes, uint32_t code_bytes, auto&& put, auto&& placed) {
-            uint32_t src = (codes ^ (half0 << 6)) + stage0 * code_bytes, empty_at = empty0 + stage0 * 8;   // this stage's codes
-            uint32_t bar = full0 + stage0 * 8, phase = 0, buf = stage0, buf_phase = 1;
-            for (uint32_t stage = stage0; stage < total; stage += kStep) {
-                if (!mbar_wait_at(bar, phase, abort_flag, status)) return;
-                const bool ready = mbar_test_wait(bempty0 + buf * 8, buf_phase);
+            uint32_t src = codes + set * code_bytes, empty_at = empty0 + set * 8;   // this stage's codes
+            uint32_t phase = 0, buf = set;
+            uint32_t free_at = bempty0 + set * 8, free_phase = 0;   // the buffer's barrier of this turn (its first one is free from the start)
+            for (uint32_t stage = set; stage < total; stage += 2) {
+                if (!mbar_wait_at(empty_at - kStages * 8, phase, abort_flag, status)) return;
+                const uint32_t parity = free_phase ^ (free_at < bempty0 + kBufs * 8 ? 1u : 0u);
+                const bool ready = mbar_test_wait(free_at, parity);
 #pragma unroll
-                for (uint32_t h = 0; h < kHalves; ++h) {
+                for (uint32_t h = 0; h < 2; ++h) {
                     uint32_t a[32];
 #pragma unroll
                     for (uint32_t c = 0; c < 4; ++c) {
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             a[c * 8 + j * 2 + 1] = v.y;
                         }
                     }
-                    if (h == 0 && !ready && !mbar_wait_at(bempty0 + buf * 8, buf_phase, abort_flag, status)) return;
+                    if (h == 0 && !ready && !mbar_wait_at(free_at, parity, abort_flag, status)) return;
                     put(buf, h, a);
                 }
                 // The slot is given back only when every word read from it has been used by a store.
@@ -447,25 +447,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 placed();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(bfull0 + buf * 8);
-                src += kStep * code_bytes;
-                empty_at += kStep * 8;
+                src += 2 * code_bytes;
+                empty_at += 2 * 8;
                 if (empty_at >= empty0 + kStages * 8) {
                     empty_at -= kStages * 8;
                     src -= kStages * code_bytes;
-                }
-                bar += kStep * 8;
-                if (bar >= full0 + 2 * kStages * 8) {
-                    bar -= 2 * kStages * 8;
                     phase ^= 1u;
                 }
-                buf = (buf + kStep) % kBufs;
-                buf_phase ^= buf == stage0 ? 1u : 0u;
+                free_at += 2 * 8;
+                if (free_at >= bempty0 + 2 * kBufs * 8) {
+                    free_at -= 2 * kBufs * 8;
+                    free_phase ^= 1u;
+                }
+                buf += 2;
+                if (buf >= kBufs) buf -= kBufs;
             }
         };
         if (is_b) {
             const bool live = row < static_cast<uint32_t>(brows);   // a tile of fewer than 256 rows leaves threads without one
             const uint32_t r = live ? row : 0;
-            const uint32_t dst0 = smem_u32(sH) + half0 * (h_bytes / 2) + r * (kHalfK * 2) + ((r & 7u) << 4);
+            const uint32_t dst0 = smem_u32(sH) + r * (kHalfK * 2) + ((r & 7u) << 4);
             convert((smem_u32(sB) + r * kStageK) ^ ((r & 7u) << 4), b_bytes, [&](uint32_t b, uint32_t h, const uint32_t (&a)[32]) {
                 if (live) {
                     const uint32_t dst = dst0 + b * h_bytes + h * (h_bytes / 2);
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             }, [] { fence_proxy_async_shared(); });
         } else {
-            const uint32_t a0 = tmem + kACol + half0 * (kHalfK / 2) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            const uint32_t a0 = tmem + kACol + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             convert((smem_u32(sA) + row * kStageK) ^ ((row & 7u) << 4), a_bytes, [&](uint32_t b, uint32_t h, const uint32_t (&a)[32]) {
                 if (h == 0) tc_fence_after();
                 tc_st_32x32b_x32(a0 + b * (kStageK / 2) + h * (kHalfK / 2), a);
@@ -644,7 +645,7 @@ constexpr int kSmallTokens = 32;   // up to here: small_kernel
 // by the tensor cores' 4 cycles per column; a column's way through the epilogue,
 // with B's rows as the tokens (2-byte stores) or as the output channels (32-byte
 // stores); the join of a shared K.
-constexpr double kStageCycles = 1250, kColumnCycles = 21, kRowColumnCycles = 8, kJoinCycles = 3000, kJoinColumnCycles = 20;
+constexpr double kStageCycles = 1050, kColumnCycles = 21, kRowColumnCycles = 8, kJoinCycles = 3000, kJoinColumnCycles = 20;
 
 // Launch, prologue and exit of a call (tile_kernel, small_kernel), a block of small_kernel, and 1024 k of its 32 tokens.
 constexpr double kTileCycles = 4500, kSmallCycles = 3800, kSmallBlockCycles = 1000, kSmallKCycles = 1500;
@@ -788,7 +789,7 @@ int active_clusters(K kern, int smem, int (&active)[kMaxSplit]) {
     return WNA16_OK;
 }
 
-template <typename T, bool TM, bool ALT>
+template <typename T, bool TM>
 int launch_tiles(const LinearParams& p, const Plan& L, int max_smem, int pairs, void* workspace, cudaStream_t s) {
     TileParams tp;
     tp.p = p;
@@ -810,7 +811,7 @@ int launch_tiles(const LinearParams& p, const Plan& L, int max_smem, int pairs, 
     CUtensorMap tm_a, tm_b;
     if (int rc = code_map(&tm_a, TM ? p.xq : p.wq, TM ? p.T : p.N, p.K, kM)) return rc;
     if (int rc = code_map(&tm_b, TM ? p.wq : p.xq, TM ? p.N : p.T, p.K, L.nt / 2)) return rc;
-    auto kern = tile_kernel<T, TM, ALT>;
+    auto kern = tile_kernel<T, TM>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return cuda_error(e, "shared memory of the 8-bit linear");
     const int64_t items = static_cast<int64_t>(L.m_tiles) * L.c_tiles;
@@ -841,16 +842,12 @@ int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
     auto small = [&] { return cuda_error(launch_small<T>(p, sms, status, s), "8-bit linear launch"); };
     if (p.T <= kSmallTokens) return small();
     int active[kMaxSplit];
-    if (int rc = active_clusters(tile_kernel<T, false, false>, max_smem, active)) return rc;
+    if (int rc = active_clusters(tile_kernel<T, false>, max_smem, active)) return rc;
     const bool wide = p.N % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
     const Plan L = make_plan(p.T, p.K, p.N, wide, active);
     if (small_cycles(p.T, p.K, p.N, sms) < L.cycles) return small();
-    if (!L.tokens_m) return launch_tiles<T, false, false>(p, L, max_smem, active[0], workspace, s);
-    // ALT / not (us), items one after another: 2048 x 4096 x 4096 45 / 47, 4096 x 4096 x 4096 83 / 90, 6000 x
-    // 4096 x 4096 123 / 133; 8192 x 4096 x 4096 157 / 157 (power).  One each: 1024 x 4096 x 4096 26.5 / 26.1.
-    return static_cast<int64_t>(L.m_tiles) * L.c_tiles > active[0]
-               ? launch_tiles<T, true, true>(p, L, max_smem, active[0], workspace, s)
-               : launch_tiles<T, true, false>(p, L, max_smem, active[0], workspace, s);
+    return L.tokens_m ? launch_tiles<T, true>(p, L, max_smem, active[0], workspace, s)
+                      : launch_tiles<T, false>(p, L, max_smem, active[0], workspace, s);
 }
 
 }  // namespace
