@@ -190,6 +190,20 @@ def test_swiglu(moe, T, N, dt, L, qt, group):
     assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("L", [7.0, float("inf")])
+def test_swiglu_over_the_range_of_gates(moe, dt, L):
+    """One gate per row, from where the exponential overflows to where it vanishes."""
+    g = torch.cat([torch.linspace(-130, 130, 1041), torch.tensor([-1e4, -1e30, -3e38, 1e4])]).to(dt).cuda()
+    gu = torch.stack([g] * 8 + [torch.full_like(g, 3.0)] * 8, dim=1).contiguous()
+    q, s = moe.swiglu_q8(gu, swiglu_limit=L)
+    v = moe.dequantize_q8(q, s, dtype=FP).double()
+    gd = g.double().clamp(max=L)
+    ref = (gd * torch.sigmoid(gd) * 3.0)[:, None].expand(-1, 8)
+    # the value's 12 roundings, of the scale 3, of the product 1; rows below 2^-100 are zeros
+    assert bool(((v - ref).abs() <= 16 * U * ref.abs() + 2.0 ** -99).all())
+
+
 def test_swiglu_nan_passes(moe):
     gu = randn(3, 64, dtype=BF)
     gu[0, 3] = float("nan")

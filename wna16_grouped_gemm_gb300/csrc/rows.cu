@@ -176,8 +176,9 @@ __device__ __forceinline__ float max_abs8(const F2 (&v)[kP]) {
 
 // silu(min(g, L)) * clamp(u, -L, L), with sigmoid(g) = 1 / (1 + 2^t), t = -g log2(e)
 // (g in [-100, 100] there: beyond, the sigmoid is 0 or 1 to fp32).  The rounding
-// of t is made good, which leaves 2^t off by 4 units of 2^-24 (and 0.2 |g| for
-// the constant); the rest is off by 1 to 2 each.  NaN passes the clamps.
+// of t is made good, which leaves 2^t off by 5 units of 2^-24 (and 0.2 |g| for
+// the constant); the rest is off by 1 to 2 each.  Below g = -87 the sigmoid is
+// taken as 0.  NaN passes the clamps.
 __device__ __forceinline__ F2 swiglu2(F2 gate, F2 up, float L) {
     constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
     float2 g = parts(gate), u = parts(up);
@@ -191,7 +192,8 @@ __device__ __forceinline__ F2 swiglu2(F2 gate, F2 up, float L) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(tt.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(tt.y));
     const F2 ee = f2(e.x, e.y);
-    const float2 d = parts(add2(fma2(ee, mul2(rest, f2(-kLn2, -kLn2)), ee), f2(1.0f, 1.0f)));
+    const F2 one = f2(1.0f, 1.0f);   // (2^t may be infinite: its factor is positive, so that the sum is too)
+    const float2 d = parts(fma2(ee, fma2(rest, f2(-kLn2, -kLn2), one), one));
     float2 r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
