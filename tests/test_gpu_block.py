@@ -362,6 +362,22 @@ def test_route_when_all_scores_are_nearly_equal(moe, score, G, Gk):
         check_route(moe, logits, k, score=score, bias=bias, G=G, Gk=Gk)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [16, 31, 32])
+def test_route_of_many_nearly_equal_pairs(moe, score, k):
+    """Many experts chosen of many: every value has another one next to it, nearer than fp32's error."""
+    T, E = 40, 1024
+    logits = randn(T, E, seed=k)
+    logits[1:] = logits[0]
+    z = logits[0].double()
+    s = 1 / (1 + torch.exp(-z)) if score == "sigmoid" else torch.softmax(z, 0)
+    bias = randn(E, seed=k + 1, scale=0.05)
+    bias[512:] = (s[:512] + bias[:512].double() - s[512:]).float()
+    logits += torch.linspace(0, 1e-6, T, device="cuda")[:, None]
+    check_route(moe, logits, k, score=score, bias=bias)
+    check_route(moe, logits, k, score=score, bias=bias, G=4, Gk=2)
+
+
 @pytest.mark.parametrize("k", [1, 7, 15, 16, 24, 31, 32])
 def test_route_topk_sizes(moe, k):
     """The bound below the chosen ones comes from the lanes' best or second best values, by k and the lanes in play."""

@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
 #pragma unroll
                 for (int i = 0; i < PL; ++i) value[i] = -INFINITY;
             }
-            float last = INFINITY, tol = 0.0f;
+            float last = INFINITY, chosen = 0.0f, tol = 0.0f;
             int last_id = 0;
             const int rounds = by_logit ? p.topk : min(p.topk + 1, p.topk_groups * L.size);   // one more, for the last one's margin
             for (int j = 0; j < rounds; ++j) {
@@ -573,8 +573,11 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
                 const uint32_t id = __reduce_min_sync(kAll, e);
 #pragma unroll
                 for (int i = 0; i < PL; ++i)
-                    if (i == at && e == id) value[i] = -INFINITY;
-                if (lane == j) my_id = static_cast<int>(id);
+                    if (i == at && e == id && j < p.topk) value[i] = -INFINITY;
+                if (lane == j) {
+                    my_id = static_cast<int>(id);
+                    chosen = key_value(all);
+                }
                 if (!by_logit) {
                     const float now = key_value(all);
                     if (j == 0) tol = top_score;
@@ -584,6 +587,17 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
                                  p.bias[last_id] != p.bias[id];
                     last = now;
                     last_id = static_cast<int>(id);
+                }
+            }
+            if (unsure) {   // the choices and what may be among them, in 64 bits
+                const float least = __shfl_sync(kAll, chosen, p.topk - 1);
+                const int more = collect(L, value, out ? INFINITY : fmaxf(least - unit * tol, kLowest), cand);
+                if (more + p.topk <= kMost) {
+                    if (lane < p.topk) cand.v[more + lane] = pack(0u, my_id);
+                    __syncwarp();
+                    settle_order(t, cand, more + p.topk);
+                    my_id = expert_of(cand.v[lane]);
+                    unsure = false;
                 }
             }
         }
