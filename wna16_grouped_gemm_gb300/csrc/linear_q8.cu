@@ -4,16 +4,17 @@
 // Two kernels: small_kernel up to 32 tokens and where it is estimated to be faster
 // (few channels: a tile's prologue, ring and join take 4 us), else tile_kernel.
 //
-// small_kernel: bound by the weights' bytes.  A block owns 16
-// output channels and up to 32 tokens (the weights come from L2 for the second and
-// later groups of tokens); its 8 warps take the K range in turns of 64, each lane
-// loading 16 consecutive bytes of two weight rows and of a token straight into
-// registers, where they become the fp16 operands of four mma.sync m16n8k16 (the
-// order of k inside a product is free, so both operands use the order in which
-// the bytes lie).  The fp32 sums of at most 1024 products are exact integers;
+// small_kernel: bound by the weights' bytes.  A block owns 16 output channels and up
+// to 32 tokens (the weights come from L2 for the second and later groups of tokens);
+// its 8 warps take the K range in turns of 64, each lane loading 16 consecutive bytes
+// of two weight rows and of a token straight into registers, where they become the
+// fp16 operands of four mma.sync m16n8k16 (the order of k inside a product is free,
+// so both operands use the order in which the bytes lie).  The fp32 sums of at most 1024 products are exact integers;
 // they are added as integers, over the warps in shared memory.  (mma.sync on
 // 8-bit integers, a 40th of the fp16 rate on this chip: 4 x 4096 x 4096 5.0 us,
-// 32 x 4096 x 4096 17.6 us.)
+// 32 x 4096 x 4096 17.6 us.)  Measured, tokens x 4096 x 4096: 4 4.7 us (3.6 TB/s),
+// 16 6.1, 32 8.3 (the conversions); 4 x 4096 x 32768 24.8 us (5.4 TB/s, 0.80 of the
+// measured copy bandwidth); 77 x 2048 x 1000 5.0.
 //
 // tile_kernel: bound by the tensor cores.  sm_103a has no 8-bit
 // integer kind of tcgen05.mma, but 8-bit integers are exact in fp16, and their
@@ -24,13 +25,18 @@
 // few (tiles of B fit them) and the tokens where they are many (a thread then
 // holds neighbouring output channels and stores 32 bytes at a time):
 //   TMA producer (warp 0)      128-k stages: codes of the CTA's rows of A and B
-//   A converters (warps 4..11) thread = row: 64 codes -> fp16 -> TMEM
-//   B converters (12..19)      thread = row: 64 codes -> fp16 -> shared memory
+//   A converters (warps 4..11) thread = row: 128 codes -> fp16 -> TMEM, in two sets for
+//   B converters (12..19)      thread = row: 128 codes -> fp16 -> shared memory, even and odd stages
 //   MMA issuer (warp 1 of the even CTA)   256 x nt x 128 per pair of operand buffers
 //   epilogue (warps 20..27)    tcgen05.ld, scales, bias, addend, store
 // Only codes cross the memory system, and A's fp16 form never passes through
-// shared memory.  When there are few tiles, 2 or 4 pairs form a cluster
+// shared memory.  When there are few tiles, 2 to 4 pairs form a cluster
 // that shares a tile's K and adds its sums through distributed shared memory.
+// Measured, tokens x 4096 x 4096 (of the 1917 TFLOP/s of a measured bf16 product):
+// 64 12.2 us, 512 20.6, 1024 24.3, 2048 42.3 (0.85), 4096 79 (0.91), 8192 151 to 160
+// (0.90 to 0.95, power); 8192 x 2048 x 4096 93 (0.77: the accumulator takes half of TMEM
+// and the operands of a stage the rest, so a tile's epilogue is not under the next
+// tile's products); 2048 has 152 tiles of 224 columns, two for each pair.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -216,7 +222,7 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
 
 constexpr int kM = 128;            // rows of A per CTA (256 per pair)
 constexpr int kStageK = 128;       // k per stage of codes: one 128-byte swizzle row
-constexpr int kHalfK = 64;         // k per converter set and stage: 32 TMEM columns, one 128-byte swizzle row of fp16
+constexpr int kHalfK = 64;         // k converted at a time: 32 TMEM columns, one 128-byte swizzle row of fp16
 constexpr int kStages = 4;
 constexpr int kBufs = 3;           // operand buffers, one stage each: 64 TMEM columns, two swizzle atoms of fp16
 static_assert(kStages % 2 == 0, "a set of converters that takes every other stage keeps to its own slots");

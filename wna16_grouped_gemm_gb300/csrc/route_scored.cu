@@ -18,6 +18,12 @@
 // in question, and only those, are computed again in 64 bits and ordered by
 // them.  Without a bias the order of the experts is the order of the logits
 // themselves, which is exact.
+//
+// Bound by instructions: 1.3 us would read the logits of 8192 tokens of 256 experts.
+// Small cases are one launch, and a token that needs 64 bits takes some 8 us by
+// itself (fp64 is slow on this chip).  Measured (us), 256 experts, 8 chosen, sigmoid
+// with a bias and 4 of 8 groups: 4 tokens 2.8, 2048 5.4, 8192 9.5 to 10.8; without
+// bias and groups 8192 6.5.  1024 experts, 32 chosen, with a bias: 8192 45.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -6,9 +6,20 @@
 //   plain   y = x
 //   m = max |y|,  scale = m / Q,  code = round(y * (Q / m))
 //
-// One block per row.  A thread owns chunks of 8 consecutive values (chunk
-// i * blockDim + thread, i < CH), which stay in registers from the one read of
-// the row to its last write; sums and maxima are fp32.
+// Bound by the bytes of the rows, each read and written once, and close behind by
+// issue slots (66 % of them used at 8192 x 4096).  One block works on one row: a
+// thread owns chunks of 8 consecutive values (chunk i * blockDim + thread, i < CH),
+// which stay in registers from the one read of the row to its last write, and one
+// block reduction gives both the sum of squares and the maximum (the greatest |h w|
+// times 1 / rms is the greatest |y|).  Sums and maxima are fp32.  A block takes row
+// after row and has the next one's reads in flight.  Few blocks of more registers
+// beat more blocks: norm 8192 x 4096 held to 38 registers and three blocks per SM
+// 55.0 us, with 45 and two 49.2.
+// Measured (us, of the measured copy bandwidth of 6782 GB/s), back to back:
+//   norm 8192 x 4096 bf16, four outputs   49.2   0.91    2047 x 5120 fp16, e4m3 in groups of 128   17.8   0.61
+//   swiglu 8192 x 2048 bf16               16.3   0.76    8192 x 4096   30.3   0.82
+//   plain 8192 x 4096 bf16                16.5   0.90    back to bf16   16.6   0.89
+//   4 rows: norm 2.2, swiglu 1.6 (a launch)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -517,9 +528,9 @@ cudaError_t launch_vec(const RowParams& p, cudaStream_t s) {
     auto threads = [&](int ch) { return ((chunks + ch - 1) / ch + 31) / 32 * 32; };
     constexpr bool pre = VEC && sizeof(T) == 2;
     if constexpr (pre) {
-        // Chunks per thread, measured at 8192 rows of 4096 (2 x 2048 for swiglu):
-        //   norm    1: 49.7 us, 2: 49.0, 4: 50.6 (without prefetch 67, 57, 71); 2047 x 5120 e4m3 in groups
-        //           18.3, 19.9, 22.1; 4 rows 2.2, 2.6, 3.1; but 512 rows 6.0, 5.4, 6.3: there 2 have all
+        // Chunks per thread, measured (us) at 8192 rows of 4096 (2 x 2048 for swiglu):
+        //   norm    1: 49.2, 2: 49.0, 4: 50.6 (without the reads ahead 67, 57, 71); 2047 x 5120 e4m3 in groups
+        //           17.8, 19.9, 22.1; 4 rows 2.2, 2.6, 3.1; but 512 rows 6.0, 5.3, 6.3: there 2 have all
         //           rows worked on at the same time and 1 has not
         //   swiglu  1: 19.4, 2: 17.0, 4: 16.8
         //   plain   1: 19.8, 2: 18.6, 4: 16.7; in groups 11.5, 10.9, 13.2 (4096 rows)
