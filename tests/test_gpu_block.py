@@ -457,6 +457,8 @@ LINEAR_CASES = [
     # and with many channels: small tiles of tokens, an odd number of channels
     (40, 256, 8192, BF), (100, 512, 4096, FP), (70, 2048, 8192, HF), (300, 16, 5003, FP), (129, 80, 6001, FP),
     (1000, 4096, 1025, FP),
+    # few tokens, long sums and many channels
+    (33, 4096, 4099, FP), (90, 8192, 2048, HF), (48, 4112, 5001, FP), (64, 4000, 16000, BF), (100, 16384, 1600, FP),
     # tokens on the M side, with ragged tiles of them
     (3001, 1008, 784, BF), (2500, 256, 1040, HF), (4100, 128, 512, BF), (5000, 1040, 4096, BF), (1700, 2048, 1408, FP),
 ]

@@ -29,11 +29,12 @@
 //   B converters (12..19)      thread = row: 128 codes -> fp16 -> shared memory, even and odd stages
 //   MMA issuer (warp 1 of the even CTA)   256 x nt x 128 per pair of operand buffers
 //   epilogue (warps 20..27)    tcgen05.ld, scales, bias, addend, store
+// (with few rows of B: four sets for A, and the epilogue's warps convert B first)
 // Only codes cross the memory system, and A's fp16 form never passes through
 // shared memory.  When there are few tiles, 2 to 4 pairs form a cluster
 // that shares a tile's K and adds its sums through distributed shared memory.
 // Measured, tokens x 4096 x 4096 (of the 1917 TFLOP/s of a measured bf16 product):
-// 64 12.2 us, 512 20.6, 1024 24.3, 2048 42.3 (0.85), 4096 79 (0.91), 8192 151 to 160
+// 64 11.6 us, 512 20.6, 1024 24.3, 2048 42.3 (0.85), 4096 79 (0.91), 8192 151 to 160
 // (0.90 to 0.95, power); 8192 x 2048 x 4096 93 (0.77: the accumulator takes half of TMEM
 // and the operands of a stage the rest, so a tile's epilogue is not under the next
 // tile's products); 2048 has 152 tiles of 224 columns, two for each pair.
@@ -223,17 +224,40 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
 constexpr int kM = 128;            // rows of A per CTA (256 per pair)
 constexpr int kStageK = 128;       // k per stage of codes: one 128-byte swizzle row
 constexpr int kHalfK = 64;         // k converted at a time: 32 TMEM columns, one 128-byte swizzle row of fp16
-constexpr int kStages = 4;
 constexpr int kBufs = 3;           // operand buffers, one stage each: 64 TMEM columns, two swizzle atoms of fp16
-static_assert(kStages % 2 == 0, "a set of converters that takes every other stage keeps to its own slots");
 constexpr int kMaxSplit = 4;
 constexpr int kProducer = 0, kIssuer = 1, kAlloc = 2;
-constexpr int kFirstA = 4, kFirstB = 12, kFirstEpilogue = 20;   // 8 warps each, in two sets of 4
+constexpr int kFirstA = 4, kFirstB = 12, kFirstEpilogue = 20;   // 8 warps each
 constexpr int kSet = 4, kEpilogues = 8;
+// How the converters are dealt out.  A set takes every kSets-th stage, and slots and
+// barriers come in multiples of that: a wait by parity must not take the turn of another
+// set at the same barrier for its own.
+template <bool SMALL_B>
+struct Roles {
+    static constexpr int kSets = 2;      // of four warps for A (warps 4..11) and four for B (12..19)
+    static constexpr int kBWarps = 4;
+    static constexpr int kStages = 4;    // slots of codes
+    static constexpr int kFree = 6;      // barriers of the operand buffers' release, in turns
+};
+// At most 96 rows of B, one item per pair, and enough stages that it is estimated to be faster:
+// four sets for A (warps 4..19), and the epilogue's warps convert B before they have anything
+// else to do, two per set; twice the slots fit.  Like this / with two sets (us): 64 x 4096 x 4096
+// 11.6 / 12.2, 100 x 8192 x 2048 15.0 / 17.6, 128 x 4096 x 4096 13.1 / 13.8, 64 x 4096 x 16384 18.2 / 21.5; but with 6
+// stages per pair, 40 x 2048 x 4096, 9.9 / 9.3.  (Six operand buffers, which fit with 64 rows: 64 x 4096 x
+// 4096 11.7, 96 x 4096 x 4096 13.1 against 12.3.)
+constexpr int kSmallCols = 96;
+template <>
+struct Roles<true> {
+    static constexpr int kSets = 4;
+    static constexpr int kBWarps = 2;
+    static constexpr int kStages = 8;
+    static constexpr int kFree = 12;
+};
+template <bool SMALL_B>
+constexpr int kBars = 2 * Roles<SMALL_B>::kStages + kBufs + Roles<SMALL_B>::kFree + 3;
 constexpr int kTileThreads = 32 * (kFirstEpilogue + kEpilogues);
 constexpr int kCols = 512;
 constexpr uint32_t kACol = 256;    // TMEM: accumulator in columns 0..nt-1, operand buffers from here
-constexpr int kBars = 2 * kStages + 3 * kBufs + 3;
 constexpr int kMaxCols = 256;      // rows of B per tile (columns of the result)
 
 struct TileParams {
@@ -247,7 +271,7 @@ struct TileParams {
 };
 
 // Operand A: the weights, B: the tokens; with TM the other way round.
-template <typename T, bool TM>
+template <typename T, bool TM, bool SMALL_B>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const TileParams tp) {
@@ -259,6 +283,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t leader = rank & ~1u, side = rank & 1u;
     const int split = static_cast<int>(rank >> 1);
     const int nt = tp.nt, brows = nt / 2, ksplit = tp.ksplit;
+    using R = Roles<SMALL_B>;
+    constexpr int kStages = R::kStages, kSets = R::kSets, kFree = R::kFree;
+    static_assert(kStages % kSets == 0 && kFree % kSets == 0 && kFree % kBufs == 0, "every set has its own");
     constexpr int a_bytes = kM * kStageK;
     const int b_bytes = brows * kStageK;
     const int h_bytes = brows * kStageK * 2;
@@ -269,10 +296,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(sScale + kMaxCols);
     uint64_t* empty = full + kStages;
     uint64_t* bfull = empty + kStages;         // the leader's: both CTAs' operands of a buffer are in place
-    // Two bempty barriers per buffer, in turns: a set of converters that takes every other stage meets one of
-    // three buffers again two turns later, and a wait by parity must not take the turn between for its own.
-    uint64_t* bempty = bfull + kBufs;
-    uint64_t* accfull = bempty + 2 * kBufs;
+    uint64_t* bempty = bfull + kBufs;          // stage s + kBufs waits for the products of stage s at barrier (s + kBufs) % kFree
+    uint64_t* accfull = bempty + kFree;
     uint64_t* accempty = accfull + 1;          // the leader's
     uint64_t* drain = accempty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -282,13 +307,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 2 * kSet);    // a set of either kind of converters
+            mbar_init(&empty[i], kSet + R::kBWarps);   // a set of either kind of converters
         }
         for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&bfull[i], 2 * 2 * kSet);   // those of both CTAs
-            mbar_init(&bempty[i], 1);
-            mbar_init(&bempty[kBufs + i], 1);
+            mbar_init(&bfull[i], 2 * (kSet + R::kBWarps));   // those of both CTAs
         }
+        for (int i = 0; i < kFree; ++i) mbar_init(&bempty[i], 1);
         mbar_init(accfull, 1);
         mbar_init(accempty, 2 * kEpilogues);
         mbar_init(drain, 1);
@@ -362,7 +386,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // f16 A and B, f32 D, both K-major, 256 x nt
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>((2 * kM) >> 4) << 24);
             const uint16_t mask = static_cast<uint16_t>(3u << rank);
-            Slot bs, be;   // operand buffer, and the barrier that the stage after next but one there waits for
+            Slot bs, be;   // operand buffer, and the barrier of its release
             be.i = kBufs;
             uint32_t it = 0;
             bool ok = true, issued = false;
@@ -371,7 +395,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     ok = false;
                     break;
                 }
-                for (int kb = kb0; kb < kb1; ++kb, bs.next(kBufs), be.next(2 * kBufs)) {
+                for (int kb = kb0; kb < kb1; ++kb, bs.next(kBufs), be.next(kFree)) {
                     const int b = bs.i;
                     if (!warp_wait(&bfull[b], bs.phase)) {
                         ok = false;
@@ -405,15 +429,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp >= kFirstA && warp < kFirstEpilogue) {
-        // Converters.  Set s of either kind takes the stages s, s + 2, .. (A half of every stage per
-        // set, with twice the waits and arrivals: 2048 x 4096 x 4096 45.3 us against 42.6, 2500 x 8192 x
-        // 1536 44.7 against 39.7; only products of a few stages were faster, 100 x 512 x 4096 6.4 against 6.6.)
+    } else if (warp >= kFirstA && (SMALL_B || warp < kFirstEpilogue)) {
+        // Converters.  Set s of either kind takes the stages s, s + kSets, .. (With two sets, a half of
+        // every stage per set, with twice the waits and arrivals: 2048 x 4096 x 4096 45.3 us against 42.6, 2500 x
+        // 8192 x 1536 44.7 against 39.7; only products of a few stages were faster, 100 x 512 x 4096 6.4 against 6.6.)
         // Chunk c of a row lies at chunk c ^ (row & 7) of its 128 bytes (the swizzle), so
         // with the row's part of that in an address, c enters by one exclusive or.
-        const bool is_b = warp >= kFirstB;
-        const uint32_t set = static_cast<uint32_t>(warp - (is_b ? kFirstB : kFirstA)) / kSet;
-        const uint32_t row = static_cast<uint32_t>((warp & 3) * 32 + lane);   // row of A (= TMEM lane) or of this CTA's half of B
+        constexpr int kFirstOfB = SMALL_B ? kFirstEpilogue : kFirstB;
+        const bool is_b = warp >= kFirstOfB;
+        const uint32_t set = is_b ? static_cast<uint32_t>(warp - kFirstOfB) / R::kBWarps : static_cast<uint32_t>(warp - kFirstA) / kSet;
+        // row of A (= TMEM lane) or of this CTA's half of B
+        const uint32_t row = static_cast<uint32_t>((is_b ? warp % R::kBWarps : warp & 3) * 32 + lane);
         const uint32_t bfull0 = map_shared(smem_u32(bfull), leader), bempty0 = smem_u32(bempty), empty0 = smem_u32(empty);
         const uint32_t turns = first < items ? static_cast<uint32_t>((items - 1 - first) / stride + 1) : 0;
         const uint32_t total = turns * static_cast<uint32_t>(kb1 - kb0);
@@ -421,9 +447,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // `buffer`; placed(): after both
         auto convert = [&](uint32_t codes, uint32_t code_bytes, auto&& put, auto&& placed) {
             uint32_t src = codes + set * code_bytes, empty_at = empty0 + set * 8;   // this stage's codes
-            uint32_t phase = 0, buf = set;
-            uint32_t free_at = bempty0 + set * 8, free_phase = 0;   // the buffer's barrier of this turn (its first one is free from the start)
-            for (uint32_t stage = set; stage < total; stage += 2) {
+            uint32_t phase = 0, buf = set % kBufs;
+            uint32_t free_at = bempty0 + set * 8, free_phase = 0;   // the buffer's barrier of this turn (the first one of each is free)
+            for (uint32_t stage = set; stage < total; stage += kSets) {
                 if (!mbar_wait_at(empty_at - kStages * 8, phase, abort_flag, status)) return;
                 const uint32_t parity = free_phase ^ (free_at < bempty0 + kBufs * 8 ? 1u : 0u);
                 const bool ready = mbar_test_wait(free_at, parity);
@@ -453,24 +479,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 placed();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(bfull0 + buf * 8);
-                src += 2 * code_bytes;
-                empty_at += 2 * 8;
+                src += kSets * code_bytes;
+                empty_at += kSets * 8;
                 if (empty_at >= empty0 + kStages * 8) {
                     empty_at -= kStages * 8;
                     src -= kStages * code_bytes;
                     phase ^= 1u;
                 }
-                free_at += 2 * 8;
-                if (free_at >= bempty0 + 2 * kBufs * 8) {
-                    free_at -= 2 * kBufs * 8;
+                free_at += kSets * 8;
+                if (free_at >= bempty0 + kFree * 8) {
+                    free_at -= kFree * 8;
                     free_phase ^= 1u;
                 }
-                buf += 2;
-                if (buf >= kBufs) buf -= kBufs;
+                buf = (buf + kSets) % kBufs;
             }
         };
         if (is_b) {
-            const bool live = row < static_cast<uint32_t>(brows);   // a tile of fewer than 256 rows leaves threads without one
+            if (SMALL_B && first < items) {   // (one item: the scales are not in its way then)
+                const float* scale = TM ? p.ws : p.xs;
+                const int i = static_cast<int>(threadIdx.x) - 32 * kFirstEpilogue;
+                if (i < nt) sScale[i] = __ldg(scale + min(b_row(first) + i, (TM ? p.N : p.T) - 1));
+            }
+            const bool live = row < static_cast<uint32_t>(brows);   // a tile of fewer rows leaves threads without one
             const uint32_t r = live ? row : 0;
             const uint32_t dst0 = smem_u32(sH) + r * (kHalfK * 2) + ((r & 7u) << 4);
             convert((smem_u32(sB) + r * kStageK) ^ ((r & 7u) << 4), b_bytes, [&](uint32_t b, uint32_t h, const uint32_t (&a)[32]) {
@@ -568,7 +598,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const float as = a < a_len ? __ldg(a_scale + a) : 0.0f;
             const float bias = !TM && a < a_len && p.bias ? __ldg(p.bias + a) : 0.0f;
             if (it > 0) named_barrier(1, 32 * kEpilogues);   // the last tile's scales have been read
-            for (int i = thread; i < nt; i += 32 * kEpilogues) sScale[i] = __ldg(b_scale + min(b0 + i, b_len - 1));
+            if (!SMALL_B)
+                for (int i = thread; i < nt; i += 32 * kEpilogues) sScale[i] = __ldg(b_scale + min(b0 + i, b_len - 1));
             // one warp polls; the others wait in a barrier, which costs the converters no issue slots
             if (warp == kFirstEpilogue) {
                 done = done && mbar_wait_bounded(accfull, it & 1u, abort_flag, status, true);
@@ -651,7 +682,9 @@ constexpr int kSmallTokens = 32;   // up to here: small_kernel
 // by the tensor cores' 4 cycles per column; a column's way through the epilogue,
 // with B's rows as the tokens (2-byte stores) or as the output channels (32-byte
 // stores); the join of a shared K.
-constexpr double kStageCycles = 1050, kColumnCycles = 21, kRowColumnCycles = 8, kJoinCycles = 3000, kJoinColumnCycles = 20;
+// With four sets of converters (see Roles) a stage takes less, but the first ones come later.
+constexpr double kStageCycles = 1050, kSmallStageCycles = 650, kSmallFillCycles = 3000;
+constexpr double kColumnCycles = 21, kRowColumnCycles = 8, kJoinCycles = 3000, kJoinColumnCycles = 20;
 
 // Launch, prologue and exit of a call (tile_kernel, small_kernel), a block of small_kernel, and 1024 k of its 32 tokens.
 constexpr double kTileCycles = 4500, kSmallCycles = 3800, kSmallBlockCycles = 1000, kSmallKCycles = 1500;
@@ -659,6 +692,7 @@ constexpr double kTileCycles = 4500, kSmallCycles = 3800, kSmallBlockCycles = 10
 struct Plan {
     double cycles = 0.0;   // estimated time
     bool tokens_m = false;
+    bool small_b = false;   // see Roles
     int nt = 0, ksplit = 1, kblocks = 0, m_tiles = 0, c_tiles = 0;
 };
 
@@ -677,16 +711,20 @@ Plan make_plan(int64_t T, int64_t K, int64_t N, bool wide, const int (&active)[k
             const int64_t nt = ((b_len + c_tiles - 1) / c_tiles + 31) / 32 * 32;
             if (nt > kMaxCols || nt * (c_tiles - 1) >= b_len) continue;
             const int64_t tiles = m_tiles * c_tiles;
-            const double stage = nt * 4 > kStageCycles ? nt * 4 : kStageCycles;
             const double column = tm ? kRowColumnCycles : kColumnCycles;
             for (int ks = 1; ks <= kMaxSplit && ks <= kblocks; ++ks) {
                 const int64_t waves = (tiles + active[ks - 1] - 1) / active[ks - 1];
                 if (ks > 1 && waves > 1) break;   // (only ever faster for a single wave)
                 const int64_t per = (kblocks + ks - 1) / ks;
-                const double cost = kTileCycles + waves * (per * stage + nt * column) + (ks > 1 ? kJoinCycles + nt * kJoinColumnCycles : 0);
+                const double two_sets = per * std::max(kStageCycles, nt * 4.0);
+                const double four_sets = kSmallFillCycles + per * std::max(kSmallStageCycles, nt * 4.0);
+                const bool small_b = tm == 0 && nt <= kSmallCols && waves == 1 && four_sets < two_sets;
+                const double cost = kTileCycles + waves * ((small_b ? four_sets : two_sets) + nt * column) +
+                                    (ks > 1 ? kJoinCycles + nt * kJoinColumnCycles : 0);
                 if (best.nt == 0 || cost < best.cycles) {
                     best.cycles = cost;
                     best.tokens_m = tm != 0;
+                    best.small_b = small_b;
                     best.nt = static_cast<int>(nt);
                     best.ksplit = ks;
                     best.kblocks = kblocks;
@@ -795,7 +833,7 @@ int active_clusters(K kern, int smem, int (&active)[kMaxSplit]) {
     return WNA16_OK;
 }
 
-template <typename T, bool TM>
+template <typename T, bool TM, bool SMALL_B>
 int launch_tiles(const LinearParams& p, const Plan& L, int max_smem, int pairs, void* workspace, cudaStream_t s) {
     TileParams tp;
     tp.p = p;
@@ -808,16 +846,16 @@ int launch_tiles(const LinearParams& p, const Plan& L, int max_smem, int pairs, 
     tp.status = static_cast<int*>(workspace);
     if (!workspace)
         if (int rc = status_word(&tp.status)) return rc;
-    const int ring = kStages * (kM + L.nt / 2) * kStageK + kBufs * (L.nt / 2) * kStageK * 2;
+    const int ring = Roles<SMALL_B>::kStages * (kM + L.nt / 2) * kStageK + kBufs * (L.nt / 2) * kStageK * 2;
     const int sums = L.ksplit > 1 ? L.ksplit * ((L.nt / 16 + L.ksplit - 1) / L.ksplit * 16) * kM * 4 : 0;
     if (sums > ring) return set_error(WNA16_ERR_UNSUPPORTED, "8-bit linear: the join does not fit");   // (the rings hold it)
-    const int smem = ring + kMaxCols * 4 + kBars * 8 + 16 + 1024;
+    const int smem = ring + kMaxCols * 4 + kBars<SMALL_B> * 8 + 16 + 1024;
     if (smem > max_smem) return set_error(WNA16_ERR_UNSUPPORTED, "8-bit linear: %d bytes of shared memory", smem);
 
     CUtensorMap tm_a, tm_b;
     if (int rc = code_map(&tm_a, TM ? p.xq : p.wq, TM ? p.T : p.N, p.K, kM)) return rc;
     if (int rc = code_map(&tm_b, TM ? p.wq : p.xq, TM ? p.N : p.T, p.K, L.nt / 2)) return rc;
-    auto kern = tile_kernel<T, TM>;
+    auto kern = tile_kernel<T, TM, SMALL_B>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return cuda_error(e, "shared memory of the 8-bit linear");
     const int64_t items = static_cast<int64_t>(L.m_tiles) * L.c_tiles;
@@ -848,12 +886,13 @@ int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
     auto small = [&] { return cuda_error(launch_small<T>(p, sms, status, s), "8-bit linear launch"); };
     if (p.T <= kSmallTokens) return small();
     int active[kMaxSplit];
-    if (int rc = active_clusters(tile_kernel<T, false>, max_smem, active)) return rc;
+    if (int rc = active_clusters(tile_kernel<T, false, false>, max_smem, active)) return rc;
     const bool wide = p.N % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
     const Plan L = make_plan(p.T, p.K, p.N, wide, active);
     if (small_cycles(p.T, p.K, p.N, sms) < L.cycles) return small();
-    return L.tokens_m ? launch_tiles<T, true>(p, L, max_smem, active[0], workspace, s)
-                      : launch_tiles<T, false>(p, L, max_smem, active[0], workspace, s);
+    if (L.tokens_m) return launch_tiles<T, true, false>(p, L, max_smem, active[0], workspace, s);
+    return L.small_b ? launch_tiles<T, false, true>(p, L, max_smem, active[0], workspace, s)
+                     : launch_tiles<T, false, false>(p, L, max_smem, active[0], workspace, s);
 }
 
 }  // namespace
