@@ -94,10 +94,14 @@ def load_peaks():
                 source="fallback (6800 GB/s, 1900 TFLOP/s)")
 
 
+#: what the forward is built from (the other sources are those of the operators around it)
+FORWARD_SOURCES = ("api.cu", "dequant.cuh", "gemm.cu", "gemm.h", "kernels.cu", "noalloc.cu", "ptx.cuh", "quant.cu")
+
+
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "wna16_grouped_gemm_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in FORWARD_SOURCES:
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode())
             h.update(f.read())
