@@ -16,7 +16,7 @@
 // beat more blocks: norm 8192 x 4096 held to 38 registers and three blocks per SM
 // 55.0 us, with 45 and two 49.2.
 // Measured (us, of the measured copy bandwidth of 6782 GB/s), back to back:
-//   norm 8192 x 4096 bf16, four outputs   49.2   0.91    2047 x 5120 fp16, e4m3 in groups of 128   17.8   0.61
+//   norm 8192 x 4096 bf16, four outputs   49.2   0.91    2047 x 5120 fp16, e4m3 in groups of 128   17.6   0.61
 //   swiglu 8192 x 2048 bf16               16.3   0.76    8192 x 4096   30.3   0.82
 //   plain 8192 x 4096 bf16                16.5   0.90    back to bf16   16.6   0.89
 //   4 rows: norm 2.2, swiglu 1.6 (a launch)
@@ -265,8 +265,8 @@ __device__ __forceinline__ void scale_of(float most, float inv, int q_type, floa
     }
 }
 
-// Sum (if SUM) and maximum over the block; every thread gets them.  red: this row's 32 + 32 words.
-template <bool SUM>
+// Sum (if SUM) and maximum (if MAX) over the block; every thread gets them.  red: this row's 32 + 32 words.
+template <bool SUM, bool MAX>
 __device__ __forceinline__ void block_reduce(float& sum, float& most, float* red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     if (SUM) {
@@ -274,21 +274,21 @@ __device__ __forceinline__ void block_reduce(float& sum, float& most, float* red
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
     // magnitudes order like their bits, with NaN above infinity
-    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most) & 0x7fffffffu));
+    if (MAX) most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most) & 0x7fffffffu));
     if (nw == 1) return;
     if (lane == 0) {
         if (SUM) red[warp] = sum;
-        red[32 + warp] = most;
+        if (MAX) red[32 + warp] = most;
     }
     __syncthreads();
-    most = lane < nw ? red[32 + lane] : 0.0f;
+    if (MAX) most = lane < nw ? red[32 + lane] : 0.0f;
     if (SUM) {
         sum = lane < nw ? red[lane] : 0.0f;
         for (int o = nw > 16 ? 16 : nw > 8 ? 8 : nw > 4 ? 4 : nw > 2 ? 2 : 1; o > 0; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
         sum = __shfl_sync(0xffffffffu, sum, 0);
     }
-    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    if (MAX) most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
 }
 
 // What a thread reads of a chunk of a row: the values, and a second tensor's
@@ -388,7 +388,10 @@ __global__ void __launch_bounds__(CH == 4 && PREFETCH ? 512 : 1024) rows_kernel(
         for (int i = 1; i < CH; ++i) row_most = max_nan(row_most, most[i]);
         const float2 halves = parts(sum2);
         float sum = halves.x + halves.y, inv = 1.0f;
-        if (OP == RowOp::norm || p.group == 0) block_reduce<OP == RowOp::norm>(sum, row_most, red[turn & 1]);
+        if (p.group == 0)
+            block_reduce<OP == RowOp::norm, true>(sum, row_most, red[turn & 1]);
+        else if (OP == RowOp::norm)
+            block_reduce<true, false>(sum, row_most, red[turn & 1]);
         if constexpr (OP == RowOp::norm) {
             inv = rsqrtf(sum / static_cast<float>(K) + p.eps);
             if (p.norm_out) {
@@ -530,7 +533,7 @@ cudaError_t launch_vec(const RowParams& p, cudaStream_t s) {
     if constexpr (pre) {
         // Chunks per thread, measured (us) at 8192 rows of 4096 (2 x 2048 for swiglu):
         //   norm    1: 49.2, 2: 49.0, 4: 50.6 (without the reads ahead 67, 57, 71); 2047 x 5120 e4m3 in groups
-        //           17.8, 19.9, 22.1; 4 rows 2.2, 2.6, 3.1; but 512 rows 6.0, 5.3, 6.3: there 2 have all
+        //           17.6, 19.9, 22.1; 4 rows 2.2, 2.6, 3.1; but 512 rows 6.0, 5.3, 6.3: there 2 have all
         //           rows worked on at the same time and 1 has not
         //   swiglu  1: 19.4, 2: 17.0, 4: 16.8
         //   plain   1: 19.8, 2: 18.6, 4: 16.7; in groups 11.5, 10.9, 13.2 (4096 rows)
