@@ -387,6 +387,20 @@ def test_route_topk_sizes(moe, k):
             check_route(moe, randn(90, E, seed=k + E + 1, dtype=BF), k, score="softmax", G=G, Gk=Gk, group_score="max")
 
 
+def test_route_weights_of_experts_far_below_the_largest(moe):
+    """Chosen by bias: softmax scores around and below fp32's smallest, divided by their sum."""
+    logits = randn(64, 64, seed=21, scale=3.0) - torch.linspace(0, 300, 64, device="cuda")[:, None]
+    logits[:, 5] = 20.0
+    bias = torch.zeros(64, device="cuda")
+    bias[16:32] = 4.0                                               # the group without the largest logit
+    for k in (1, 6, 16):
+        _, w = check_route(moe, logits, k, score="softmax", bias=bias, G=4, Gk=1)
+        assert np.abs(w.sum(axis=1) - 1).max() < 1e-5
+    z = torch.full((8, 16), -88.5, device="cuda") + randn(8, 16, seed=22, scale=0.1)
+    _, w = moe.route_scored(z, 4)                                   # sigmoids below 2^-126
+    assert bool(torch.isfinite(w).all()) and bool(((w.sum(dim=1) - 1).abs() < 1e-2).all())
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_route_masked_experts(moe, score):
     inf = float("inf")

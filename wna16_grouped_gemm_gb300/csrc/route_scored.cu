@@ -128,6 +128,12 @@ struct Token {
         if (type == kFp16) return clean(__half2float(static_cast<const __half*>(row)[e]));
         return clean(__bfloat162float(static_cast<const __nv_bfloat16*>(row)[e]));
     }
+    // Scores relative to a logit of `most` from here on: weights that are divided by their
+    // sum do not depend on it, and keep their bits where the chosen ones are far below the largest.
+    __device__ __forceinline__ void softmax_of(float most) {
+        m = most;
+        total = 1.0f;
+    }
     // For the weights.
     __device__ __forceinline__ float score(float z) const {
         if (!p.softmax) return 1.0f / (1.0f + expf(-z));
@@ -610,10 +616,13 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
         if (unsure) my_id = choose64(t, PL);
     }
 
-    float w = lane < p.topk ? t.score(t.logit(my_id)) : 0.0f;
+    const float z_mine = lane < p.topk ? t.logit(my_id) : -INFINITY;
+    if (SOFTMAX && p.renormalize) t.softmax_of(key_value(__reduce_max_sync(kAll, order_key(z_mine))));
+    float w = lane < p.topk ? t.score(z_mine) : 0.0f;
     if (p.renormalize) {
         const float sum = warp_sum(w);
-        w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
+        // (the fast division is not for sums near fp32's smallest)
+        w = sum > 0x1p-100f ? __fdividef(w, sum) : sum > 0.0f ? w / sum : 0.0f;
     }
     if (lane < p.topk) {
         p.ids[static_cast<int64_t>(ti) * p.topk + lane] = my_id;
