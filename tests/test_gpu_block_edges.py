@@ -1,0 +1,70 @@
+"""The operators around the routed experts on the GPU at the edges of their
+ranges, against plain 64-bit computations of their definitions (tolerances:
+as derived in test_gpu_block, u = 2^-24)."""
+from __future__ import annotations
+
+import ctypes
+import itertools
+
+import pytest
+import torch
+
+from tests.test_gpu_block import BF, FP, HF, I8, U, check, check_q8, half_step, moe, norm_ref, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+# ---------------------------------------------------------------- norm
+
+
+def _norm_c(x, r, w, q, s, ro, no, group=0, eps=1e-6):
+    """The C entry point itself; None: NULL."""
+    from wna16_grouped_gemm_gb300 import block
+    lib = block._load()
+    types = {BF: 0, HF: 1, FP: 2}
+    p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    T, K = x.shape
+    return lib.wna16_moe_add_rmsnorm_q8(p(x), K, p(r), K, p(w), types[w.dtype], T, K, types[x.dtype], eps, 0, group, p(q), p(s),
+                                        p(ro), p(no), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+
+
+@pytest.mark.parametrize("T,K,dt,group", [(5, 264, BF, 0), (3, 1003, BF, 0), (700, 512, HF, 64), (4, 640, FP, 128), (2, 9000, FP, 0)])
+def test_norm_with_every_choice_of_outputs(moe, T, K, dt, group):
+    """Each of residual, residual_out, norm_out and (q, scales) may be NULL by itself;
+    what is written has the bits that it has with all of them."""
+    x, w = randn(T, K, seed=1, dtype=dt), (1 + 0.2 * randn(K, seed=2)).to(dt)
+    for r in (None, randn(T, K, seed=3, dtype=dt)):
+        h, y = norm_ref(x, w, r, 1e-6)
+        full = None
+        for has_ro, has_no, has_q in itertools.product((True, False), repeat=3):
+            ro = torch.full_like(x, 77.0) if has_ro else None
+            no = torch.full_like(x, 77.0) if has_no else None
+            q = torch.full((T, K), 77, dtype=I8, device="cuda") if has_q else None
+            s = torch.full((T, K // group if group else 1), 77.0, device="cuda") if has_q else None
+            rc = _norm_c(x, r, w, q, s, ro, no, group)
+            if not has_no and not has_q:
+                assert rc == moe.ERR_INVALID_ARG
+                continue
+            assert rc == moe.OK
+            torch.cuda.synchronize()
+            if full is None:
+                full = ro, no, q, s
+                if r is None:
+                    assert torch.equal(ro, x)
+                else:
+                    check(ro, h, half_step(dt) + 2 * U, "residual_out")
+                check(no, y, half_step(dt) + 33 * U, "norm_out", floor=2.0 ** -25 if dt == HF else 0.0)
+                check_q8(moe, q, s, y, group, 32 * U, "norm")
+            for got, want in zip((ro, no, q, s), full):
+                assert got is None or torch.equal(got, want), (has_ro, has_no, has_q)
+
+
+def test_norm_residual_out_without_a_residual(moe):
+    x, w = randn(6, 512, seed=4, dtype=BF), torch.ones(512, dtype=BF, device="cuda")
+    ro = torch.zeros_like(x)
+    q, s, got, _ = moe.add_rmsnorm_q8(x, w, residual_out=ro)
+    assert got is ro and torch.equal(ro, x)
+    q2, s2, none, _ = moe.add_rmsnorm_q8(x, w)
+    assert none is None and torch.equal(q, q2) and torch.equal(s, s2)

@@ -103,8 +103,9 @@ def add_rmsnorm_q8(x, weight, residual=None, *, eps: float = 1e-6, q_dtype=torch
     x, residual: bf16, fp16 or fp32 [T, K] (rows may be strided), weight [K] of
     that type or fp32.  Returns (q, scales, residual_out, norm_out): y in 8 bits
     (q_dtype int8 or float8_e4m3fn, one scale per row or per group_size values;
-    None, None with want_q=False), h in x's type (None without a residual) and
-    y in x's type (None unless want_norm or norm_out is given).
+    None, None with want_q=False), h in x's type (without a residual, where h = x:
+    None unless residual_out is given) and y in x's type (None unless want_norm
+    or norm_out is given).
     residual_out=residual updates the residual in place."""
     lib = _lib or _load()
     if want_q:
@@ -112,10 +113,7 @@ def add_rmsnorm_q8(x, weight, residual=None, *, eps: float = 1e-6, q_dtype=torch
             q, scales = _new_q(x, _matrix(x, "x")[1], q_dtype, group_size, q, scales, stream)
     elif q is not None or scales is not None:
         raise ValueError("q or scales with want_q=False")
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out without a residual")
-    elif residual_out is None:
+    if residual is not None and residual_out is None:
         residual_out = _new(_matrix(x, "x"), x.dtype, x, stream)
     if norm_out is None and want_norm:
         norm_out = _new(_matrix(x, "x"), x.dtype, x, stream)

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(CH == 4 && PREFETCH ? 512 : 1024) rows_kernel(
             most[i] = 0.0f;
             if (k < K) {
                 if constexpr (OP == RowOp::norm) {
-                    if (p.residual) store8<T, VEC>(static_cast<T*>(p.residual_out) + t * K + k, K - k, v[i]);
+                    if (p.residual_out) store8<T, VEC>(static_cast<T*>(p.residual_out) + t * K + k, K - k, v[i]);
 #pragma unroll
                     for (int j = 0; j < kP; ++j) sum2 = fma2(v[i][j], v[i][j], sum2);
                     F2 w[kP];
