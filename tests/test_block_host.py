@@ -166,3 +166,24 @@ def test_wrappers_refuse_host_tensors_and_bad_types():
         block.route_scored(x, 2)
     with pytest.raises(TypeError, match="CUDA"):
         block.linear_q8(x.to(torch.int8), torch.ones(4), x.to(torch.int8), torch.ones(4))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(residual_out=P[2]),                                       # over the weights
+    dict(residual_out=P[2], residual=None),
+    dict(residual_out=P[0], ldx=8192),                             # x's rows are apart
+    dict(residual_out=P[0], ldx=8192, residual=P[0], ldr=4096),    # x's and the residual's, one of them contiguous
+    dict(residual_out=P[1], residual=P[1], x=P[1] + 2),            # in place for the residual, a shifted x
+    dict(residual_out=P[0], weight=P[0]),                          # in place for x, which is the weights too
+])
+def test_norm_is_in_place_for_x_and_residual_only(lib, kw):
+    assert _norm(lib, **kw) == INV
+    assert "overlaps" in lib.wna16_moe_last_error().decode()
+
+
+@pytest.mark.parametrize("over", ["xq", "xs", "wq", "ws", "bias"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_linear_is_in_place_for_the_addend_only(lib, over, in_place):
+    kw = {over: P[5], "addend": P[5] if in_place else P[4]}
+    assert _linear(lib, **kw) == INV
+    assert "overlaps" in lib.wna16_moe_last_error().decode()

@@ -59,19 +59,19 @@ struct Range {
     const void* p;
     size_t bytes;
     const char* name;
+    bool in_place = false;   // an input that outs[0] updates in place: the same elements at the same places
 };
 bool overlap(const Range& a, const Range& b) {
     if (!a.p || !b.p) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
     return x < y + b.bytes && y < x + a.bytes;
 }
-// Outputs against inputs and against one another; `same` may be named by an
-// input and by outs[0] alike (an update in place).
+// Outputs against inputs and against one another.
 template <size_t NO, size_t NI>
-int check_overlap(const Range (&outs)[NO], const Range (&ins)[NI], bool in_place0) {
+int check_overlap(const Range (&outs)[NO], const Range (&ins)[NI]) {
     for (size_t i = 0; i < NO; ++i) {
         for (const Range& r : ins)
-            if (overlap(outs[i], r) && !(i == 0 && in_place0 && r.p == outs[0].p))
+            if (overlap(outs[i], r) && !(i == 0 && r.in_place))
                 return set_error(WNA16_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, r.name);
         for (size_t j = 0; j < i; ++j)
             if (overlap(outs[i], outs[j]))
@@ -129,12 +129,11 @@ int wna16_moe_add_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, i
                            {norm_out, out_bytes, "norm_out"},
                            {q, static_cast<size_t>(T * K), "q"},
                            {scales, scale_bytes(T, K, q ? group_size : 0), "scales"}};
-    const Range ins[3] = {{x, extent(T, ldx, K, es), "x"},
-                          {residual, residual ? extent(T, ldr, K, es) : 0, "residual"},
-                          {weight, static_cast<size_t>(K) * size_of(weight_type), "weight"}};
-    // in place: the same rows at the same places
-    const bool in_place = (residual_out != x || ldx == K || T == 1) && (residual_out != residual || ldr == K || T == 1);
-    if (int rc = check_overlap(outs, ins, in_place)) return rc;
+    const Range ins[3] = {
+        {x, extent(T, ldx, K, es), "x", residual_out == x && (ldx == K || T == 1)},
+        {residual, residual ? extent(T, ldr, K, es) : 0, "residual", residual_out == residual && (ldr == K || T == 1)},
+        {weight, static_cast<size_t>(K) * size_of(weight_type), "weight"}};
+    if (int rc = check_overlap(outs, ins)) return rc;
     RowParams p;
     p.x = x;
     p.residual = residual;
@@ -171,7 +170,7 @@ int wna16_moe_swiglu_q8(const void* gu, int64_t ldg, int64_t T, int64_t N, int t
     if (int rc = check_pointer(scales, 4, "scales")) return rc;
     const Range outs[2] = {{q, static_cast<size_t>(T * N), "q"}, {scales, scale_bytes(T, N, group_size), "scales"}};
     const Range ins[1] = {{gu, extent(T, ldg, 2 * N, es), "gu"}};
-    if (int rc = check_overlap(outs, ins, false)) return rc;
+    if (int rc = check_overlap(outs, ins)) return rc;
     RowParams p;
     p.x = gu;
     p.ldx = ldg;
@@ -200,7 +199,7 @@ int wna16_moe_quantize_q8(const void* x, int64_t ldx, int64_t T, int64_t K, int 
     if (int rc = check_pointer(scales, 4, "scales")) return rc;
     const Range outs[2] = {{q, static_cast<size_t>(T * K), "q"}, {scales, scale_bytes(T, K, group_size), "scales"}};
     const Range ins[1] = {{x, extent(T, ldx, K, es), "x"}};
-    if (int rc = check_overlap(outs, ins, false)) return rc;
+    if (int rc = check_overlap(outs, ins)) return rc;
     RowParams p;
     p.x = x;
     p.ldx = ldx;
@@ -227,7 +226,7 @@ int wna16_moe_dequantize_q8(const void* q, const float* scales, int64_t T, int64
     if (int rc = check_pointer(out, es, "out")) return rc;
     const Range outs[1] = {{out, static_cast<size_t>(T * K) * es, "out"}};
     const Range ins[2] = {{q, static_cast<size_t>(T * K), "q"}, {scales, scale_bytes(T, K, group_size), "scales"}};
-    if (int rc = check_overlap(outs, ins, false)) return rc;
+    if (int rc = check_overlap(outs, ins)) return rc;
     const bool vec = K % 16 == 0 && aligned(q, 16) && aligned(out, 16);
     return launched(launch_dequantize_q8(q, scales, T, static_cast<int>(K), q_type, group_size, type, out, vec,
                                          static_cast<cudaStream_t>(stream)),
@@ -265,7 +264,7 @@ int wna16_moe_route_scored(const void* logits, int64_t ld, const float* bias, in
     const Range outs[2] = {{topk_ids, static_cast<size_t>(T) * topk * 4, "topk_ids"},
                            {topk_weights, static_cast<size_t>(T) * topk * 4, "topk_weights"}};
     const Range ins[2] = {{logits, extent(T, ld, E, es), "logits"}, {bias, static_cast<size_t>(E) * 4, "bias"}};
-    if (int rc = check_overlap(outs, ins, false)) return rc;
+    if (int rc = check_overlap(outs, ins)) return rc;
     ScoredRouteParams p;
     p.logits = logits;
     p.ld = ld;
@@ -328,8 +327,8 @@ int wna16_moe_linear_q8(const int8_t* xq, const float* x_scales, const int8_t* w
                           {x_scales, static_cast<size_t>(T) * 4, "x_scales"},
                           {w_scales, static_cast<size_t>(N) * 4, "w_scales"},
                           {bias, static_cast<size_t>(N) * 4, "bias"},
-                          {addend, static_cast<size_t>(T * N) * es, "addend"}};
-    if (int rc = check_overlap(outs, ins, addend == out)) return rc;
+                          {addend, static_cast<size_t>(T * N) * es, "addend", addend == out}};
+    if (int rc = check_overlap(outs, ins)) return rc;
     LinearParams p;
     p.xq = xq;
     p.xs = x_scales;
