@@ -9,7 +9,8 @@ import itertools
 import pytest
 import torch
 
-from tests.test_gpu_block import BF, FP, HF, I8, U, check, check_q8, half_step, moe, norm_ref, randn  # noqa: F401
+from tests.test_gpu_block import (BF, FP, HF, I8, U, check, check_q8, check_route, half_step, moe, norm_ref,  # noqa: F401
+                                  randn)
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +69,26 @@ def test_norm_residual_out_without_a_residual(moe):
     assert got is ro and torch.equal(ro, x)
     q2, s2, none, _ = moe.add_rmsnorm_q8(x, w)
     assert none is None and torch.equal(q, q2) and torch.equal(s, s2)
+
+
+# ---------------------------------------------------------------- routing
+
+
+def _group_bias(E, G, groups, value, seed=0):
+    """A small bias, and `value` for the experts of the given groups."""
+    b = randn(E, seed=seed, scale=0.02)
+    b.view(G, E // G)[groups] = value
+    return b
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("gscore", ["max", "top2"])
+@pytest.mark.parametrize("E,G,Gk", [(256, 8, 4), (36, 12, 5), (1020, 17, 6), (160, 8, 3)])
+def test_route_groups_masked_by_the_lowest_bias(moe, score, gscore, E, G, Gk):
+    """Groups with a bias of fp32's lowest value: fewer groups than are kept stay
+    unmasked, as many, one, none.  (Group sizes that leave lanes with empty slots.)"""
+    logits = randn(50, E, seed=E, scale=1.5)
+    for left in (Gk + 1, Gk, Gk - 1, 1, 0):
+        b = _group_bias(E, G, list(range(left, G)), torch.finfo(FP).min)
+        for k in (1, 6, min(32, Gk * (E // G))):
+            check_route(moe, logits, k, score=score, bias=b, G=G, Gk=Gk, group_score=gscore)

@@ -176,8 +176,9 @@ __device__ __forceinline__ uint64_t pack(uint32_t key, int expert) {
 }
 __device__ __forceinline__ int expert_of(uint64_t v) { return static_cast<int>(~static_cast<uint32_t>(v)); }
 
-// Collects the experts whose value is at least the lane's `bound` (above -INFINITY);
-// their number, of which the first 64 are in c.v (the rest of it is 0).
+// Collects the experts whose value is at least the lane's `bound`; their number, of
+// which the first 64 are in c.v (the rest of it is 0).  A bound is kLowest at least:
+// slots without an expert hold -INFINITY, and would index logits and biases past E.
 template <int PL>
 __device__ __forceinline__ int collect(const Lanes& L, const float (&value)[PL], float bound, Candidates& c) {
     const int lane = threadIdx.x & 31;
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
 #pragma unroll
                 for (int i = 0; i < PL; ++i) copy[i] = value[i];
                 bool stays = kept;
-                all64 = !settle_groups<PL>(t, L, copy, gs, lo, hi, by_logit ? from : from - tol, tol, cand, stays);
+                all64 = !settle_groups<PL>(t, L, copy, gs, lo, hi, by_logit ? from : fmaxf(from - tol, kLowest), tol, cand, stays);
                 kept = stays;
             }
         }
