@@ -92,3 +92,52 @@ def test_route_groups_masked_by_the_lowest_bias(moe, score, gscore, E, G, Gk):
         b = _group_bias(E, G, list(range(left, G)), torch.finfo(FP).min)
         for k in (1, 6, min(32, Gk * (E // G))):
             check_route(moe, logits, k, score=score, bias=b, G=G, Gk=Gk, group_score=gscore)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("gscore", ["max", "top2"])
+@pytest.mark.parametrize("E,G,Gk", [(256, 8, 4), (36, 12, 5), (160, 8, 3)])
+@pytest.mark.parametrize("value", [-1e9, -100.0, 1e9])
+def test_route_groups_far_from_the_others(moe, score, gscore, E, G, Gk, value):
+    """Groups masked or forced by a large bias: each group's score has an error of its own size."""
+    logits = randn(60, E, seed=E + 1, scale=1.5)
+    for left in (G - 1, Gk + 1, Gk, Gk - 1, 1):
+        b = _group_bias(E, G, list(range(left, G)), value)
+        for k in (1, 6, min(32, Gk * (E // G))):
+            check_route(moe, logits, k, score=score, bias=b, G=G, Gk=Gk, group_score=gscore)
+        b.view(G, E // G)[left:, 1:] = -value                       # one expert far up, the others far down, and the reverse
+        check_route(moe, logits, 6, score=score, bias=b, G=G, Gk=Gk, group_score=gscore)
+
+
+def _us(f, n=20):
+    """Time of one call among others (median of five runs of a graph of n)."""
+    f()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            f()
+    graph.replay()
+    times = []
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b) * 1e3 / n)
+    return sorted(times)[2]
+
+
+def test_route_groups_far_from_the_others_cost_no_64_bits(moe):
+    """Masked groups leave the others' order as clear as it was: no token is chosen in 64 bits for
+    them, which would take a hundred times as long."""
+    logits, b = randn(8192, 256, seed=1), randn(256, seed=2, scale=0.05)
+    ids, w = moe.route_scored(logits, 8, bias=b, groups=8, topk_groups=4)
+    time = lambda bias: _us(lambda: moe.route_scored(logits, 8, bias=bias, groups=8, topk_groups=4, ids=ids, weights=w))  # noqa: E731
+    plain = time(b)
+    for value in (-1e9, torch.finfo(FP).min):
+        for left in (7, 5, 4):
+            masked = b.clone()
+            masked.view(8, 32)[left:] = value
+            assert time(masked) < 3 * plain, (value, left)

@@ -284,16 +284,16 @@ __device__ __noinline__ int choose64(Token t, int n) {
     return my_id;
 }
 
-// Whether this lane's group stays, when 32 bits cannot tell: gs is its score,
-// `kept` the decision so far, `lo` the least of the kept groups' scores and `hi` the
-// greatest of the others'.  from: the least value that may be one of the group's two
-// best.  Returns false if there are too many values to look at.
+// Whether this lane's group stays, when 32 bits cannot tell: gs is its score, off by
+// `margin` at most, `kept` the decision so far, `lo` the least that a kept group's score
+// may be and `hi` the most that another one's may be.  from: the least value that may be
+// one of the group's two best.  Returns false if there are too many values to look at.
 template <int PL>
-__device__ __noinline__ bool settle_groups(Token t, Lanes L, const float* value, float gs, float lo, float hi,
-                                           float from, float tol, Candidates& cand, bool& kept) {
+__device__ __noinline__ bool settle_groups(Token t, Lanes L, const float* value, float gs, float margin, float lo, float hi,
+                                           float from, Candidates& cand, bool& kept) {
     const ScoredRouteParams& p = t.p;
     const int lane = threadIdx.x & 31;
-    const bool open = L.live && (kept ? gs <= hi + 2.0f * tol : gs >= lo - 2.0f * tol);
+    const bool open = L.live && (kept ? gs - margin <= hi : gs + margin >= lo);
     const int open_kept = __popc(__ballot_sync(kAll, open && kept && L.sub == 0));   // places to give
     float v[PL];
 #pragma unroll
@@ -496,16 +496,17 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
         }
         bool kept = L.live && rank < p.topk_groups;
         if (!by_logit || !best_only) {   // (the best logits' order is exact)
-            const float lo = key_value(__reduce_min_sync(kAll, kept ? order_key(gs) : 0xffffffffu));
-            const float hi = key_value(__reduce_max_sync(kAll, L.live && !kept ? order_key(gs) : 0u));
-            const float most = L.live ? fmaxf(fabsf(b0), best_only ? 0.0f : fabsf(b1)) : 0.0f;
-            const float tol = unit * fmaxf(top_score, __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most))));
-            if (lo - hi <= 2.0f * tol) {   // a sum's error is twice a value's
+            // Each group's score may be off by a margin of its own (a sum's error is twice a value's): with
+            // one margin for all, a group masked by a bias of -1e9 brought every group's order in question.
+            const float margin = unit * fmaxf(top_score, L.live ? fmaxf(fabsf(b0), best_only ? 0.0f : fabsf(b1)) : 0.0f);
+            const float lo = key_value(__reduce_min_sync(kAll, kept ? order_key(gs - margin) : 0xffffffffu));
+            const float hi = key_value(__reduce_max_sync(kAll, L.live && !kept ? order_key(gs + margin) : 0u));
+            if (!(lo > hi)) {
                 float copy[PL];
 #pragma unroll
                 for (int i = 0; i < PL; ++i) copy[i] = value[i];
                 bool stays = kept;
-                all64 = !settle_groups<PL>(t, L, copy, gs, lo, hi, by_logit ? from : fmaxf(from - tol, kLowest), tol, cand, stays);
+                all64 = !settle_groups<PL>(t, L, copy, gs, margin, lo, hi, by_logit ? from : fmaxf(from - margin, kLowest), cand, stays);
                 kept = stays;
             }
         }
