@@ -141,3 +141,30 @@ def test_route_groups_far_from_the_others_cost_no_64_bits(moe):
             masked = b.clone()
             masked.view(8, 32)[left:] = value
             assert time(masked) < 3 * plain, (value, left)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,Gk,k", [(256, 1, 1, 8), (256, 8, 4, 8), (1024, 1, 1, 32), (64, 1, 1, 31), (37, 1, 1, 5)])
+def test_route_forced_and_masked_experts(moe, score, E, G, Gk, k):
+    """Experts with large biases: neighbours are compared by their own size."""
+    logits = randn(60, E, seed=E + k, scale=1.5)
+    for value in (1e9, -1e9, 1e4, torch.finfo(FP).max, torch.finfo(FP).min):
+        for n in (1, 2, k - 1, E // 2):
+            b = randn(E, seed=n, scale=0.05)
+            b[torch.randperm(E, generator=torch.Generator().manual_seed(n))[:n].cuda()] = value
+            check_route(moe, logits, k, score=score, bias=b, G=G, Gk=Gk)
+    b = randn(E, seed=3, scale=0.05)
+    b[:6] = torch.tensor([1e9, 1e9, 1e5, 1e5 + 0.0078125, -1e9, -1e30], device="cuda")   # pairs that 32 bits cannot order
+    check_route(moe, logits, k, score=score, bias=b, G=G, Gk=Gk)
+
+
+def test_route_forced_experts_cost_no_64_bits(moe):
+    logits = randn(8192, 256, seed=1)
+    ids, w = moe.route_scored(logits, 8)
+    time = lambda bias: _us(lambda: moe.route_scored(logits, 8, bias=bias, ids=ids, weights=w))  # noqa: E731
+    b = randn(256, seed=2, scale=0.05)
+    plain = time(b)
+    for value in (1e9, torch.finfo(FP).max):
+        forced = b.clone()
+        forced[5] = value
+        assert time(forced) < 3 * plain, value

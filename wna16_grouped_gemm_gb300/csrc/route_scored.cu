@@ -545,16 +545,19 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
             if (!by_logit) {
                 const uint64_t next = lane + 1 < count ? cand.v[lane + 1] : 0ull;
                 const float mine = key_value(static_cast<uint32_t>(v >> 32));
-                const float last = __shfl_sync(kAll, mine, p.topk - 1);
-                const float tol = unit * fmaxf(top_score, fmaxf(fabsf(__shfl_sync(kAll, mine, 0)), fabsf(last)));
-                bool close = lane < p.topk && lane + 1 < count && mine - key_value(static_cast<uint32_t>(next >> 32)) <= tol;
+                // Neighbours are compared by their own size: by the largest choice's, an expert that a bias
+                // of 1e9 forces brought all the others' order in question.
+                const float after = key_value(static_cast<uint32_t>(next >> 32));
+                bool close = lane < p.topk && lane + 1 < count &&
+                             mine - after <= unit * fmaxf(top_score, fmaxf(fabsf(mine), fabsf(after)));
                 // Equal inputs give equal scores in any precision, and their order is the
                 // index's (but behind the last choice a third one may be as near).
                 if (close && lane + 1 < p.topk)
                     close = t.logit(my_id) != t.logit(expert_of(next)) || p.bias[my_id] != p.bias[expert_of(next)];
                 if (__any_sync(kAll, close)) {
                     // every value that may be among the choices, in 64 bits
-                    count = collect(L, value, out ? INFINITY : fmaxf(last - tol, kLowest), cand);
+                    const float last = __shfl_sync(kAll, mine, p.topk - 1);
+                    count = collect(L, value, out ? INFINITY : fmaxf(last - unit * fmaxf(top_score, fabsf(last)), kLowest), cand);
                     if (count <= kMost) {
                         settle_order(t, cand, count);
                         my_id = expert_of(cand.v[lane]);
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
 #pragma unroll
                 for (int i = 0; i < PL; ++i) value[i] = -INFINITY;
             }
-            float last = INFINITY, chosen = 0.0f, tol = 0.0f;
+            float last = INFINITY, chosen = 0.0f;
             int last_id = 0;
             const int rounds = by_logit ? p.topk : min(p.topk + 1, p.topk_groups * L.size);   // one more, for the last one's margin
             for (int j = 0; j < rounds; ++j) {
@@ -594,9 +597,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
                 }
                 if (!by_logit) {
                     const float now = key_value(all);
-                    if (j == 0) tol = top_score;
-                    tol = fmaxf(tol, fabsf(now));
-                    if (last - now <= unit * tol)
+                    if (j > 0 && last - now <= unit * fmaxf(top_score, fmaxf(fabsf(last), fabsf(now))))
                         unsure = unsure || j == p.topk || t.logit(last_id) != t.logit(static_cast<int>(id)) ||
                                  p.bias[last_id] != p.bias[id];
                     last = now;
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
             }
             if (unsure) {   // the choices and what may be among them, in 64 bits
                 const float least = __shfl_sync(kAll, chosen, p.topk - 1);
-                const int more = collect(L, value, out ? INFINITY : fmaxf(least - unit * tol, kLowest), cand);
+                const int more = collect(L, value, out ? INFINITY : fmaxf(least - unit * fmaxf(top_score, fabsf(least)), kLowest), cand);
                 if (more + p.topk <= kMost) {
                     if (lane < p.topk) cand.v[more + lane] = pack(0u, my_id);
                     __syncwarp();
