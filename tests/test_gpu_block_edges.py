@@ -168,3 +168,33 @@ def test_route_forced_experts_cost_no_64_bits(moe):
         forced = b.clone()
         forced[5] = value
         assert time(forced) < 3 * plain, value
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,Gk", [(64, 1, 1), (256, 8, 4), (36, 12, 5), (1020, 17, 6), (1024, 1, 1)])
+def test_route_bias_that_is_not_finite(moe, score, E, G, Gk):
+    """NaN and infinities count as the nearest finite numbers, NaN as the lowest: the choice is
+    always of topk experts there are."""
+    inf, nan = float("inf"), float("nan")
+    top = torch.finfo(FP).max
+    logits = randn(40, E, seed=E + G, scale=1.5)
+    base = randn(E, seed=E, scale=0.02)
+    biases = [torch.full_like(base, v) for v in (nan, -inf, inf)]
+    for n in (1, 3, E // 2, E - 2):
+        at = torch.randperm(E, generator=torch.Generator().manual_seed(n))[:n].cuda()
+        for v in (nan, -inf, inf):
+            b = base.clone()
+            b[at] = v
+            biases.append(b)
+    b = base.clone()
+    b.view(G, E // G)[: (G + 1) // 2, 1:] = -inf                     # groups with one expert left
+    biases.append(b)
+    mixed = base.clone()
+    mixed[0::4], mixed[1::4], mixed[2::4] = nan, -inf, inf
+    biases.append(mixed)
+    for b in biases:
+        clean = torch.where(torch.isnan(b), -top, b).clamp(-top, top)
+        for k, group_score in itertools.product((1, 5, min(32, Gk * (E // G))), ("max", "top2")):
+            ids, w = check_route(moe, logits, k, score=score, bias=clean, G=G, Gk=Gk, group_score=group_score)
+            got = moe.route_scored(logits, k, score=score, bias=b, groups=G, topk_groups=Gk, group_score=group_score)
+            assert torch.equal(got[0].cpu(), torch.from_numpy(ids)) and torch.equal(got[1].double().cpu(), torch.from_numpy(w))

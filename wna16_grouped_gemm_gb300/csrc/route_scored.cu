@@ -75,6 +75,18 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
+// a minimum that a NaN wins
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// A bias as a finite number (NaN: the lowest).  The 32-bit path takes biases as they
+// are: a choice value of NaN or -INFINITY is not collected there, and a token with one
+// of +INFINITY or with too few others is chosen in 64 bits, with these biases.
+__device__ __forceinline__ float finite_bias(float b) { return fminf(fmaxf(b, kLowest), -kLowest); }
+
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
@@ -150,7 +162,7 @@ struct Token {
             s = 0.0;
         else
             s = (z == m ? 1.0 : exp(static_cast<double>(z) - static_cast<double>(m))) / total64;
-        return p.bias ? s + static_cast<double>(p.bias[e]) : s;
+        return p.bias ? s + static_cast<double>(finite_bias(p.bias[e])) : s;
     }
     __device__ __forceinline__ double total64() const {
         if (!p.softmax || !p.bias) return 1.0;
@@ -286,19 +298,21 @@ __device__ __noinline__ int choose64(Token t, int n) {
 
 // Whether this lane's group stays, when 32 bits cannot tell: gs is its score, off by
 // `margin` at most, `kept` the decision so far, `lo` the least that a kept group's score
-// may be and `hi` the most that another one's may be.  from: the least value that may be
-// one of the group's two best.  Returns false if there are too many values to look at.
+// may be and `hi` the most that another one's may be.  from: the last of the group's best
+// two (one) values, -INFINITY if there are not as many.  Returns false if there are too many
+// values to look at, or too few.
 template <int PL>
 __device__ __noinline__ bool settle_groups(Token t, Lanes L, const float* value, float gs, float margin, float lo, float hi,
                                            float from, Candidates& cand, bool& kept) {
     const ScoredRouteParams& p = t.p;
     const int lane = threadIdx.x & 31;
     const bool open = L.live && (kept ? gs - margin <= hi : gs + margin >= lo);
+    if (__any_sync(kAll, open && !(from >= kLowest))) return false;
     const int open_kept = __popc(__ballot_sync(kAll, open && kept && L.sub == 0));   // places to give
     float v[PL];
 #pragma unroll
     for (int i = 0; i < PL; ++i) v[i] = value[i];
-    const int count = collect(L, v, open ? from : INFINITY, cand);
+    const int count = collect(L, v, open ? fmaxf(from - (p.bias ? margin : 0.0f), kLowest) : INFINITY, cand);   // what may be among them
     if (count > 32) return false;
     const double total = t.total64();
     const int e = lane < count ? expert_of(cand.v[lane]) : -1;
@@ -466,15 +480,15 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
     // total's, a sum of up to PL + 5 roundings and its terms' 5; for both values.
     constexpr float unit = SOFTMAX ? static_cast<float>(2 * PL + 48) * 0x1p-24f : 24.0f * 0x1p-24f;
 
-    float best = -INFINITY, second = -INFINITY;   // of the lane
+    float best = -INFINITY, second = -INFINITY;   // of the lane (a value of NaN is neither)
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-        second = fmaxf(second, fminf(best, value[i]));
+        second = fmaxf(second, min_nan(best, value[i]));
         best = fmaxf(best, value[i]);
     }
     bool out = !L.live;
-    bool all64 = false;
-    if (p.topk_groups < p.groups) {
+    bool all64 = !by_logit && __any_sync(kAll, best == INFINITY);
+    if (!all64 && p.topk_groups < p.groups) {
         float b0 = best, b1 = second;             // of the group
         for (int o = 1; o < L.per_group; o <<= 1) {
             const float a0 = __shfl_xor_sync(kAll, b0, o), a1 = __shfl_xor_sync(kAll, b1, o);
@@ -498,7 +512,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
         if (!by_logit || !best_only) {   // (the best logits' order is exact)
             // Each group's score may be off by a margin of its own (a sum's error is twice a value's): with
             // one margin for all, a group masked by a bias of -1e9 brought every group's order in question.
-            const float margin = unit * fmaxf(top_score, L.live ? fmaxf(fabsf(b0), best_only ? 0.0f : fabsf(b1)) : 0.0f);
+            const float margin = unit * fmaxf(top_score, L.live ? fminf(fmaxf(fabsf(b0), best_only ? 0.0f : fabsf(b1)), -kLowest) : 0.0f);
             const float lo = key_value(__reduce_min_sync(kAll, kept ? order_key(gs - margin) : 0xffffffffu));
             const float hi = key_value(__reduce_max_sync(kAll, L.live && !kept ? order_key(gs + margin) : 0u));
             if (!(lo > hi)) {
@@ -506,7 +520,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
 #pragma unroll
                 for (int i = 0; i < PL; ++i) copy[i] = value[i];
                 bool stays = kept;
-                all64 = !settle_groups<PL>(t, L, copy, gs, margin, lo, hi, by_logit ? from : fmaxf(from - margin, kLowest), cand, stays);
+                all64 = !settle_groups<PL>(t, L, copy, gs, margin, lo, hi, from, cand, stays);
                 kept = stays;
             }
         }
@@ -528,7 +542,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
         }
         const float bound = out ? INFINITY : top == 0u ? kLowest : fmaxf(key_value(top), kLowest);
         int count = collect(L, value, bound, cand);
-        bool unsure = false;
+        bool unsure = count < p.topk;   // (only by biases of NaN or -INFINITY)
         if (count <= kMost) {
             // sort: each value goes to the place of its rank
             const bool two = count > 32;
