@@ -198,3 +198,27 @@ def test_route_bias_that_is_not_finite(moe, score, E, G, Gk):
             ids, w = check_route(moe, logits, k, score=score, bias=clean, G=G, Gk=Gk, group_score=group_score)
             got = moe.route_scored(logits, k, score=score, bias=b, groups=G, topk_groups=Gk, group_score=group_score)
             assert torch.equal(got[0].cpu(), torch.from_numpy(ids)) and torch.equal(got[1].double().cpu(), torch.from_numpy(w))
+
+
+@pytest.mark.parametrize("dt", [FP, BF, HF])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("gscore", ["top2", "max"])
+def test_route_infinite_logits_in_groups_that_lose(moe, dt, score, gscore):
+    """A logit of +inf does not bring its expert back from a group that was not kept."""
+    T, E, G = 24, 64, 8
+    logits = randn(T, E, seed=12, dtype=dt)
+    logits.view(T, G, -1)[:, 2:5] += 4.0                            # three good groups
+    logits[:, 0:8] = -9.0
+    logits[0::3, 3] = INF                                           # top2: 1 + 1e-4 against 1.9
+    logits[1::3, 48:50] = INF
+    logits[2::3, [1, 9, 17, 33, 41, 57]] = INF                      # in more groups than are kept
+    logits[5::6, 20] = -INF
+    for Gk in (1, 2, 3, 5):
+        for k in (1, 4, 8):
+            for renorm in (False, True):
+                check_route(moe, logits, k, score=score, G=G, Gk=Gk, group_score=gscore, renorm=renorm)
+    wide = randn(T, 1024, seed=13, dtype=dt)
+    wide[:, 5] = INF
+    wide[:, 0:5], wide[:, 6:64] = -9.0, -9.0
+    wide[:, 64:200] = 2.0                                           # many equal values: one maximum per choice
+    check_route(moe, wide, 32, score=score, G=16, Gk=2, group_score=gscore)

@@ -191,6 +191,9 @@ __device__ __forceinline__ int expert_of(uint64_t v) { return static_cast<int>(~
 // Collects the experts whose value is at least the lane's `bound`; their number, of
 // which the first 64 are in c.v (the rest of it is 0).  A bound is kLowest at least:
 // slots without an expert hold -INFINITY, and would index logits and biases past E.
+// Of a lane with the bound kNone, which no value reaches (a logit of +INFINITY would
+// reach +INFINITY), nothing is collected.
+constexpr float kNone = __builtin_nanf("");
 template <int PL>
 __device__ __forceinline__ int collect(const Lanes& L, const float (&value)[PL], float bound, Candidates& c) {
     const int lane = threadIdx.x & 31;
@@ -312,7 +315,7 @@ __device__ __noinline__ bool settle_groups(Token t, Lanes L, const float* value,
     float v[PL];
 #pragma unroll
     for (int i = 0; i < PL; ++i) v[i] = value[i];
-    const int count = collect(L, v, open ? fmaxf(from - (p.bias ? margin : 0.0f), kLowest) : INFINITY, cand);   // what may be among them
+    const int count = collect(L, v, open ? fmaxf(from - (p.bias ? margin : 0.0f), kLowest) : kNone, cand);   // what may be among them
     if (count > 32) return false;
     const double total = t.total64();
     const int e = lane < count ? expert_of(cand.v[lane]) : -1;
@@ -540,7 +543,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
             top = __reduce_max_sync(kAll, mine);
             if (mine == top) mine = 0u;   // (several lanes at once where values are equal)
         }
-        const float bound = out ? INFINITY : top == 0u ? kLowest : fmaxf(key_value(top), kLowest);
+        const float bound = out ? kNone : top == 0u ? kLowest : fmaxf(key_value(top), kLowest);
         int count = collect(L, value, bound, cand);
         bool unsure = count < p.topk;   // (only by biases of NaN or -INFINITY)
         if (count <= kMost) {
@@ -571,7 +574,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
                 if (__any_sync(kAll, close)) {
                     // every value that may be among the choices, in 64 bits
                     const float last = __shfl_sync(kAll, mine, p.topk - 1);
-                    count = collect(L, value, out ? INFINITY : fmaxf(last - unit * fmaxf(top_score, fabsf(last)), kLowest), cand);
+                    count = collect(L, value, out ? kNone : fmaxf(last - unit * fmaxf(top_score, fabsf(last)), kLowest), cand);
                     if (count <= kMost) {
                         settle_order(t, cand, count);
                         my_id = expert_of(cand.v[lane]);
@@ -620,7 +623,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
             }
             if (unsure) {   // the choices and what may be among them, in 64 bits
                 const float least = __shfl_sync(kAll, chosen, p.topk - 1);
-                const int more = collect(L, value, out ? INFINITY : fmaxf(least - unit * fmaxf(top_score, fabsf(least)), kLowest), cand);
+                const int more = collect(L, value, out ? kNone : fmaxf(least - unit * fmaxf(top_score, fabsf(least)), kLowest), cand);
                 if (more + p.topk <= kMost) {
                     if (lane < p.topk) cand.v[more + lane] = pack(0u, my_id);
                     __syncwarp();
