@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from tests.test_gpu_block import (BF, FP, HF, I8, U, check, check_q8, check_route, half_step, moe, norm_ref,  # noqa: F401
-                                  randn)
+                                  randn, route_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -222,3 +222,26 @@ def test_route_infinite_logits_in_groups_that_lose(moe, dt, score, gscore):
     wide[:, 0:5], wide[:, 6:64] = -9.0, -9.0
     wide[:, 64:200] = 2.0                                           # many equal values: one maximum per choice
     check_route(moe, wide, 32, score=score, G=16, Gk=2, group_score=gscore)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("centre", [-86.0, -88.5, -95.0, -104.0, -200.0, -690.0])
+def test_route_weights_of_sigmoids_below_the_smallest(moe, bias, centre):
+    """Weights divided by their sum keep the scores' ratios where the scores have left fp32."""
+    T, E, k = 40, 64, 6
+    logits = centre + randn(T, E, seed=7)
+    logits[0:5, 3] = -5.0                                           # one well above the others
+    logits[5:10, 3] = 2.0
+    logits[10:15, 1::2] = -INF
+    logits[15:18] = torch.finfo(FP).min                             # masked: weights 0
+    b = randn(E, seed=8, scale=0.05) if bias else None
+    ids, w = check_route(moe, logits, k, bias=b, scale=2.5)
+    live = (ids >= 0) & (logits.cpu().gather(1, torch.from_numpy(ids)) > -1000).numpy()
+    for t in range(T):
+        if live[t].any():
+            assert abs(w[t].sum() / 2.5 - 1) < 1e-5
+        assert not w[t][~live[t]].any()
+    # without the division: below 2^-126 in steps of 2^-149 (times the scale, which is below 3)
+    _, rw = route_ref(logits, k, "sigmoid", b, 1, 1, "top2", False, 2.5)
+    _, got = moe.route_scored(logits, k, bias=b, renormalize=False, scale=2.5)
+    assert bool((torch.from_numpy(rw) - got.double().cpu()).abs().le(256 * U * torch.from_numpy(rw) + 4 * 2.0 ** -149).all())

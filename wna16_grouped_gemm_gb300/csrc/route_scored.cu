@@ -368,6 +368,18 @@ __device__ __noinline__ void settle_order(Token t, Candidates& cand, int count) 
     __syncwarp();
 }
 
+// Weights of a token with a sigmoid near or below fp32's smallest normal number (z: the
+// lane's chosen logit, -INFINITY: none).  Where they will be divided by their sum they are
+// taken relative to the largest, so that they keep their bits.  A logit below -709
+// scores 0, as where the sigmoid is 1 / (1 + exp(-z)) in 64 bits: masks with a type's
+// lowest value are down there.
+__device__ __noinline__ float deep_sigmoid(float z, int renormalize) {
+    const float most = key_value(__reduce_max_sync(kAll, order_key(z)));
+    const float shift = renormalize ? fminf(most, 0.0f) : 0.0f;
+    if (z < -709.0f) return 0.0f;
+    return z < 0.0f ? expf(z - shift) / (1.0f + expf(z)) : 1.0f / (1.0f + expf(-z));
+}
+
 template <int PL, bool SOFTMAX>
 __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_kernel(const __grid_constant__ ScoredRouteParams p, int type) {
     __shared__ Candidates shared[kWarps];
@@ -639,6 +651,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
     const float z_mine = lane < p.topk ? t.logit(my_id) : -INFINITY;
     if (SOFTMAX && p.renormalize) t.softmax_of(key_value(__reduce_max_sync(kAll, order_key(z_mine))));
     float w = lane < p.topk ? t.score(z_mine) : 0.0f;
+    if (!SOFTMAX && __any_sync(kAll, z_mine < -87.0f && z_mine > -INFINITY)) w = deep_sigmoid(z_mine, p.renormalize);
     if (p.renormalize) {
         const float sum = warp_sum(w);
         // (the fast division is not for sums near fp32's smallest)
