@@ -9,7 +9,7 @@ import itertools
 import pytest
 import torch
 
-from tests.test_gpu_block import (BF, FP, HF, I8, U, check, check_q8, check_route, half_step, moe, norm_ref,  # noqa: F401
+from tests.test_gpu_block import (_block_inputs, BF, FP, HF, I8, U, check, check_q8, check_route, half_step, moe, norm_ref,  # noqa: F401
                                   randn, route_ref)
 
 pytestmark = pytest.mark.gpu
@@ -245,3 +245,15 @@ def test_route_weights_of_sigmoids_below_the_smallest(moe, bias, centre):
     _, rw = route_ref(logits, k, "sigmoid", b, 1, 1, "top2", False, 2.5)
     _, got = moe.route_scored(logits, k, bias=b, renormalize=False, scale=2.5)
     assert bool((torch.from_numpy(rw) - got.double().cpu()).abs().le(256 * U * torch.from_numpy(rw) + 4 * 2.0 ** -149).all())
+
+
+# ---------------------------------------------------------------- the block
+
+
+def test_moe_block_without_a_residual(moe):
+    """h = x: the output of a residual of zeros, and x as the next block's residual."""
+    x, r, w, kw = _block_inputs(37)
+    out, h = moe.moe_block(x, None, w, **kw)
+    same, h0 = moe.moe_block(x, torch.zeros_like(r), w, **kw)
+    assert torch.equal(out, same) and torch.equal(h, x) and torch.equal(h0, x)
+    moe.moe_block(out, h, w, **kw)                                  # the next one takes it

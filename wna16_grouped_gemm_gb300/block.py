@@ -236,15 +236,16 @@ def moe_block(x, residual, w: MoEBlockWeights, *, topk: int, bits: int, group_si
               score: str = "sigmoid", groups: int = 1, topk_groups: int = 1, group_score: str = "top2",
               renormalize: bool = True, scale: float = 1.0, swiglu_limit: float = 7.0, eps: float = 1e-6):
     """One MoE block: (out, residual) with h = x + residual,
-    out = routed(norm(h)) + shared(norm(h)), residual = h.
+    out = routed(norm(h)) + shared(norm(h)), residual = h (residual None, as
+    before a first layer: h = x, which is returned itself).
 
     The norm's 16-bit rows go to the router and the routed experts, its 8-bit
     rows to the shared expert, whose second product adds the routed output."""
-    q, qs, residual, normed = add_rmsnorm_q8(x, w.norm, residual, eps=eps, want_norm=True)
+    q, qs, h, normed = add_rmsnorm_q8(x, w.norm, residual, eps=eps, want_norm=True)
     ids, weights = route_scored(normed @ w.gate.t(), topk, score=score, bias=w.gate_bias, groups=groups,
                                 topk_groups=topk_groups, group_score=group_score, renormalize=renormalize, scale=scale)
     routed = binding.forward(normed, ids, weights, w.w13_packed, w.w13_scales, w.w2_packed, w.w2_scales, bits=bits,
                              group_size=group_size, group_size_w2=group_size_w2, swiglu_limit=swiglu_limit)
     gu = linear_q8(q, qs, w.shared_w13, w.shared_w13_scales, dtype=x.dtype)
     hq, hs = swiglu_q8(gu, swiglu_limit=swiglu_limit)
-    return linear_q8(hq, hs, w.shared_w2, w.shared_w2_scales, addend=routed, out=routed), residual
+    return linear_q8(hq, hs, w.shared_w2, w.shared_w2_scales, addend=routed, out=routed), x if residual is None else h
