@@ -4,6 +4,7 @@ as derived in test_gpu_block, u = 2^-24)."""
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import itertools
 
 import pytest
@@ -257,3 +258,24 @@ def test_moe_block_without_a_residual(moe):
     same, h0 = moe.moe_block(x, torch.zeros_like(r), w, **kw)
     assert torch.equal(out, same) and torch.equal(h, x) and torch.equal(h0, x)
     moe.moe_block(out, h, w, **kw)                                  # the next one takes it
+
+
+def test_moe_block_with_an_fp32_gate(moe):
+    """The choice is that of fp32 logits: the block has the bits of its parts with them, and experts
+    that differ by less than bf16 can tell are told apart."""
+    x, r, w, kw = _block_inputs(300)
+    gate = w.gate.float()
+    gate[1::2] = gate[0::2] * (1 + 2.0 ** -12)                      # pairs whose logits agree to 12 bits
+    w = dataclasses.replace(w, gate=gate, gate_bias=None)
+    kw = dict(kw, groups=1, topk_groups=1)
+    out, h = moe.moe_block(x, r, w, **kw)
+    q, s, res, normed = moe.add_rmsnorm_q8(x, w.norm, r, want_norm=True)
+    ids, wts = moe.route_scored(normed.float() @ gate.t(), kw["topk"], scale=kw["scale"])
+    routed = moe.forward(normed, ids, wts, w.w13_packed, w.w13_scales, w.w2_packed, w.w2_scales, bits=4, group_size=128)
+    hq, hs = moe.swiglu_q8(moe.linear_q8(q, s, w.shared_w13, w.shared_w13_scales, dtype=x.dtype))
+    assert torch.equal(out, moe.linear_q8(hq, hs, w.shared_w2, w.shared_w2_scales, addend=routed)) and torch.equal(h, res)
+    exact = normed.double() @ gate.double().t()
+    best = exact.max(dim=1, keepdim=True).values                    # (fp32 sums of 512 terms: 1e-5 of them)
+    assert bool(((best - exact.gather(1, ids[:, :1].long())).abs() <= 1e-4 * best.abs()).all())
+    far = (best[:, 0].abs() > 0.5) & (exact.gather(1, ids[:, :1].long() ^ 1) < best)[:, 0]
+    assert int(far.sum()) > 100 and bool((exact.argmax(dim=1) == ids[:, 0].long())[far].all())

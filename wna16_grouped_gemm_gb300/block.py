@@ -219,8 +219,8 @@ def linear_q8(xq, x_scales, wq, w_scales, *, bias=None, addend=None, dtype=torch
 @dataclasses.dataclass
 class MoEBlockWeights:
     """Weights of one MoE block: norm, router, routed experts (WNA16) and shared expert (8 bits)."""
-    norm: torch.Tensor              # [K], x's type or fp32
-    gate: torch.Tensor              # [E, K], x's type: router
+    norm: torch.Tensor              # [K], bf16 or fp32
+    gate: torch.Tensor              # [E, K] router: bf16 (logits rounded to bf16) or fp32 (fp32 logits)
     gate_bias: torch.Tensor | None  # fp32 [E], for the choice only
     w13_packed: torch.Tensor        # routed experts, as for forward()
     w13_scales: torch.Tensor
@@ -239,10 +239,16 @@ def moe_block(x, residual, w: MoEBlockWeights, *, topk: int, bits: int, group_si
     out = routed(norm(h)) + shared(norm(h)), residual = h (residual None, as
     before a first layer: h = x, which is returned itself).
 
-    The norm's 16-bit rows go to the router and the routed experts, its 8-bit
-    rows to the shared expert, whose second product adds the routed output."""
+    x and residual are bf16 [T, K] (what the routed experts take).  The norm's
+    16-bit rows go to the router and the routed experts, its 8-bit rows to the
+    shared expert, whose second product adds the routed output.  The choice of
+    experts is exact for the logits that route_scored gets, which are a library
+    product in the gate's type: with a bf16 gate they are rounded to bf16, and
+    experts whose logits agree to 8 bits are taken by index; with an fp32 gate
+    they are fp32."""
     q, qs, h, normed = add_rmsnorm_q8(x, w.norm, residual, eps=eps, want_norm=True)
-    ids, weights = route_scored(normed @ w.gate.t(), topk, score=score, bias=w.gate_bias, groups=groups,
+    logits = normed.to(w.gate.dtype) @ w.gate.t()
+    ids, weights = route_scored(logits, topk, score=score, bias=w.gate_bias, groups=groups,
                                 topk_groups=topk_groups, group_score=group_score, renormalize=renormalize, scale=scale)
     routed = binding.forward(normed, ids, weights, w.w13_packed, w.w13_scales, w.w2_packed, w.w2_scales, bits=bits,
                              group_size=group_size, group_size_w2=group_size_w2, swiglu_limit=swiglu_limit)
