@@ -108,10 +108,13 @@ WNA16_API int wna16_moe_route_scored(const void* logits, int64_t ld, const float
  *   out [T, N] of `type`; all contiguous
  * K a multiple of 16, at most 65536; xq and wq 16-byte aligned.  The sums are
  * 32-bit integers for up to 32 tokens, and for more where the weights have few
- * channels; for other calls fp32 sums of exact
- * products on the tensor cores, which are the same integers while every
- * partial sum stays below 2^24 (always for K <= 1024), and otherwise off by a
- * relative 2^-23 per 16 k at most.  Workspace (256-byte aligned): its first
+ * channels (an estimate of time decides).  Other calls have fp32 sums of exact
+ * products on the tensor cores, which are the same integers while no partial sum
+ * passes 2^24 (always for K <= 1024).  Beyond that bits are dropped on the way: with
+ * S = sum_k |xq[t][k] wq[n][k]| the sum is off by 2^-20 S per 16 k at most.  That
+ * is an absolute error; where large products cancel it can pass the sum itself.
+ * (Measured at 65536 k, products of 1023 after half as many of 16129: 8e-4 of the
+ * sum.)  Workspace (256-byte aligned): its first
  * word is the status word of wna16_moe_read_status, the size is below (0 for
  * up to 32 tokens).  It may be NULL: the status word is then not readable; an
  * output whose sums are missing after a device timeout is NaN either way. */

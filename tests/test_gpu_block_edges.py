@@ -279,3 +279,32 @@ def test_moe_block_with_an_fp32_gate(moe):
     assert bool(((best - exact.gather(1, ids[:, :1].long())).abs() <= 1e-4 * best.abs()).all())
     far = (best[:, 0].abs() > 0.5) & (exact.gather(1, ids[:, :1].long() ^ 1) < best)[:, 0]
     assert int(far.sum()) > 100 and bool((exact.argmax(dim=1) == ids[:, 0].long())[far].all())
+
+
+# ---------------------------------------------------------------- linear
+
+
+@pytest.mark.parametrize("T", [4, 64, 600, 2048])
+@pytest.mark.parametrize("K", [1024, 4096, 65536])
+def test_linear_large_sums_that_cancel(moe, T, K):
+    """Partial sums far above 2^24 that cancel to small ones, and long tails of small products behind
+    them.  Up to 32 tokens and up to 1024 k the sums are exact; else they are off by at most 2^-20 of
+    the sum of the products' magnitudes per 16 k, whatever is left of it."""
+    N, h = 512, K // 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K + T)
+    r = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device="cuda", dtype=torch.int16).to(I8)  # noqa: E731
+    big = torch.full((T, K), 127, dtype=I8, device="cuda"), torch.full((N, K), 127, dtype=I8, device="cuda")
+    x, w = r(100, 128, T, K), r(100, 128, N, K)
+    x[:, h:], w[:, h:] = -x[:, :h], w[:, :h]
+    x[:, -16:] = r(-128, 128, T, 16)                                # all that is left
+    tail = big[0].clone(), big[1].clone()
+    tail[0][:, h:], tail[1][:, h:] = 31, 33
+    down = big[0].clone(), big[1]
+    down[0][:, h:] = -3
+    for xq, wq in ((x, w), tail, down):
+        S = xq.double().abs() @ wq.double().abs().t()
+        ref = xq.double() @ wq.double().t()
+        out = moe.linear_q8(xq, torch.ones(T, device="cuda"), wq, torch.ones(N, device="cuda"), dtype=FP).double()
+        tol = 0.0 if T <= 32 or K <= 1024 else K / 16 * 2.0 ** -20 * S
+        assert bool(((out - ref).abs() <= U * ref.abs() + tol).all()), float(((out - ref).abs() / S).max())

@@ -18,8 +18,13 @@
 //
 // tile_kernel: bound by the tensor cores.  sm_103a has no 8-bit
 // integer kind of tcgen05.mma, but 8-bit integers are exact in fp16, and their
-// products and sums (below 2^24) exact in the fp32 accumulator, so the
-// codes run through kind::f16.  A pair of CTAs (cta_group::2) owns 256 rows of
+// products and sums (up to 2^24) exact in the fp32 accumulator, so the
+// codes run through kind::f16.  (A larger sum loses bits in every product of 16 k:
+// each of the 16 terms is cut at about 2^-25 of the largest one or of the sum, and the result
+// at 2^-23, 5 * 2^-23 together; measured at most 1.7 * 2^-23 of the largest partial sum, for
+// 65536 k, products of 1023 after 32768 of 16129.  Sums held in integers, as the other
+// kernel has them, would need half of the accumulator's columns and a pass over it
+// every 1024 k.)  A pair of CTAs (cta_group::2) owns 256 rows of
 // operand A (the M side, 128 per CTA) and a tile of up to 256 rows of operand B
 // (half of them in each CTA's shared memory).  A is the weights where tokens are
 // few (tiles of B fit them) and the tokens where they are many (a thread then
