@@ -187,3 +187,57 @@ def test_linear_is_in_place_for_the_addend_only(lib, over, in_place):
     kw = {over: P[5], "addend": P[5] if in_place else P[4]}
     assert _linear(lib, **kw) == INV
     assert "overlaps" in lib.wna16_moe_last_error().decode()
+
+
+class _Rows:
+    """What the argument checks look at of a CUDA tensor."""
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, torch.Size(shape)
+
+    def get_device(self):
+        return 0
+
+    def stride(self):
+        return tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return P[0]
+
+
+@pytest.mark.parametrize("bad,error", [((1 << 32), OverflowError), ((1 << 32) + 64, OverflowError), (-(1 << 40), OverflowError),
+                                       (1 << 80, OverflowError), (64.0, TypeError), ("64", TypeError), (None, TypeError)])
+def test_whole_numbers_are_not_cut_or_guessed(lib, bad, error):
+    """An argument that is no whole number of 32 bits is refused as such, before anything is called
+    (the entry point's address is 0 here)."""
+    x, w = _Rows(torch.bfloat16, 4, 256), _Rows(torch.bfloat16, 256)
+    q, s, s4 = _Rows(torch.int8, 4, 256), _Rows(torch.float32, 4, 1), _Rows(torch.float32, 4, 4)
+    host = block._host
+    for scales in (s, s4):
+        with pytest.raises(error):
+            host.quantize_q8(0, x, q, scales, bad, None)
+        with pytest.raises(error):
+            host.add_rmsnorm_q8(0, x, w, None, None, None, q, scales, 1e-6, bad, None)
+        with pytest.raises(error):
+            host.swiglu_q8(0, _Rows(torch.bfloat16, 4, 512), q, scales, 7.0, bad, None)
+    ids, weights = _Rows(torch.int32, 4, 64), _Rows(torch.float32, 4, 64)
+    good = [0, 8, 4, 0, 64, 1]
+    for i in range(6):
+        args = good[:i] + [bad] + good[i + 1:]
+        with pytest.raises(error):
+            host.route_scored(0, x, None, ids, weights, *args, 1.0, None)
+
+
+@pytest.mark.parametrize("bad", ["7", None, [7.0]])
+def test_numbers_are_numbers(lib, bad):
+    x, w = _Rows(torch.bfloat16, 4, 256), _Rows(torch.bfloat16, 256)
+    q, s = _Rows(torch.int8, 4, 256), _Rows(torch.float32, 4, 1)
+    host = block._host
+    for call in (lambda: host.add_rmsnorm_q8(0, x, w, None, None, None, q, s, bad, 0, None),
+                 lambda: host.swiglu_q8(0, _Rows(torch.bfloat16, 4, 512), q, s, bad, 0, None),
+                 lambda: host.route_scored(0, x, None, _Rows(torch.int32, 4, 8), _Rows(torch.float32, 4, 8), 0, 8, 4, 0, 8, 1, bad, None)):
+        with pytest.raises(TypeError, match="float|number"):
+            call()

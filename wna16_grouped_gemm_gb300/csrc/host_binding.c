@@ -7,6 +7,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <limits.h>
 #include <stdint.h>
 
 #include "../../include/wna16_moe_block.h"
@@ -133,6 +134,23 @@ static int stream_of(PyObject* stream, const char* name, long dev, void** out) {
     return PyErr_Occurred() ? -1 : 0;
 }
 
+/* Numbers are read before the tensors: with an exception set nothing else may be called. */
+static int to_int(PyObject* o, const char* name, int* out) {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) return -1;
+    if (v < INT_MIN || v > INT_MAX) {
+        PyErr_Format(PyExc_OverflowError, "%s=%ld does not fit 32 bits", name, v);
+        return -1;
+    }
+    *out = (int)v;
+    return 0;
+}
+static int to_float(PyObject* o, float* out) {
+    const double v = PyFloat_AsDouble(o);
+    *out = (float)v;
+    return v == -1.0 && PyErr_Occurred() ? -1 : 0;
+}
+
 static int arity(Py_ssize_t got, Py_ssize_t want) {
     if (got == want) return 0;
     PyErr_Format(PyExc_TypeError, "%zd arguments, %zd expected", got, want);
@@ -153,7 +171,9 @@ static PyObject* add_rmsnorm_q8(PyObject* self, PyObject* const* a, Py_ssize_t n
     Tensor x, w, r = {0}, ro = {0}, no = {0}, q = {0}, s = {0};
     long dev;
     void* stream;
-    if (arity(n, 11) || take(a[1], "x", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "x", x.n0, x.n1) ||
+    int group;
+    float eps;
+    if (arity(n, 11) || to_float(a[8], &eps) || to_int(a[9], "group_size", &group) || take(a[1], "x", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "x", x.n0, x.n1) ||
         take(a[2], "weight", dev, NULL, 1u << x.type | 1u << FP32, 0, &w))
         return NULL;
     if (w.dims != 1 || w.n0 != x.n1) {
@@ -165,10 +185,8 @@ static PyObject* add_rmsnorm_q8(PyObject* self, PyObject* const* a, Py_ssize_t n
     if (MAYBE(a[4]) && (take(a[4], "residual_out", dev, NULL, same, 0, &ro) || want_rows(&ro, "residual_out", x.n0, x.n1)))
         return NULL;
     if (MAYBE(a[5]) && (take(a[5], "norm_out", dev, NULL, same, 0, &no) || want_rows(&no, "norm_out", x.n0, x.n1))) return NULL;
-    const int group = (int)PyLong_AsLong(a[9]);
     if (MAYBE(a[6]) && take_q(a[6], a[7], dev, x.n0, x.n1, group, &q, &s)) return NULL;
-    const float eps = (float)PyFloat_AsDouble(a[8]);
-    if (stream_of(a[10], "x", dev, &stream) || PyErr_Occurred()) return NULL;
+    if (stream_of(a[10], "x", dev, &stream)) return NULL;
     return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_add_rmsnorm_q8))(
         x.ptr, x.ld, r.ptr, r.ld, w.ptr, w.type, x.n0, x.n1, x.type, eps,
         q.type == E4M3 && MAYBE(a[6]) ? WNA16_Q8_E4M3 : WNA16_Q8_INT8, group, q.ptr, (float*)s.ptr, ro.ptr, no.ptr, stream));
@@ -180,15 +198,14 @@ static PyObject* swiglu_q8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Tensor x, q, s;
     long dev;
     void* stream;
-    if (arity(n, 7) || take(a[1], "gu", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "gu", x.n0, x.n1)) return NULL;
+    int group;
+    float limit;
+    if (arity(n, 7) || to_float(a[4], &limit) || to_int(a[5], "group_size", &group) || take(a[1], "gu", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "gu", x.n0, x.n1)) return NULL;
     if (x.n1 % 2) {
         PyErr_Format(PyExc_ValueError, "gu must have an even number of columns, got %lld", (long long)x.n1);
         return NULL;
     }
-    const int group = (int)PyLong_AsLong(a[5]);
-    const float limit = (float)PyFloat_AsDouble(a[4]);
-    if (take_q(a[2], a[3], dev, x.n0, x.n1 / 2, group, &q, &s) || stream_of(a[6], "gu", dev, &stream) || PyErr_Occurred())
-        return NULL;
+    if (take_q(a[2], a[3], dev, x.n0, x.n1 / 2, group, &q, &s) || stream_of(a[6], "gu", dev, &stream)) return NULL;
     return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_swiglu_q8))(
         x.ptr, x.ld, x.n0, x.n1 / 2, x.type, limit, q.type == E4M3 ? WNA16_Q8_E4M3 : WNA16_Q8_INT8, group, q.ptr,
         (float*)s.ptr, stream));
@@ -200,9 +217,10 @@ static PyObject* quantize_q8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Tensor x, q, s;
     long dev;
     void* stream;
-    if (arity(n, 6) || take(a[1], "x", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "x", x.n0, x.n1)) return NULL;
-    const int group = (int)PyLong_AsLong(a[4]);
-    if (take_q(a[2], a[3], dev, x.n0, x.n1, group, &q, &s) || stream_of(a[5], "x", dev, &stream) || PyErr_Occurred()) return NULL;
+    int group;
+    if (arity(n, 6) || to_int(a[4], "group_size", &group) || take(a[1], "x", -1, &dev, FLOATS, 1, &x) ||
+        want_rows(&x, "x", x.n0, x.n1) || take_q(a[2], a[3], dev, x.n0, x.n1, group, &q, &s) || stream_of(a[5], "x", dev, &stream))
+        return NULL;
     return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_quantize_q8))(
         x.ptr, x.ld, x.n0, x.n1, x.type, q.type == E4M3 ? WNA16_Q8_E4M3 : WNA16_Q8_INT8, group, q.ptr, (float*)s.ptr,
         stream));
@@ -236,15 +254,18 @@ static PyObject* route_scored(PyObject* self, PyObject* const* a, Py_ssize_t n) 
     Tensor x, b = {0}, ids, w;
     long dev;
     void* stream;
-    if (arity(n, 13) || take(a[1], "logits", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "logits", x.n0, x.n1)) return NULL;
-    if (MAYBE(a[2]) && (take(a[2], "bias", dev, NULL, 1 << FP32, 0, &b) || want_list(&b, "bias", x.n1, 0))) return NULL;
+    static const char* const names[6] = {"score", "groups", "topk_groups", "group_score", "topk", "renormalize"};
     int v[6];
-    for (int i = 0; i < 6; ++i) v[i] = (int)PyLong_AsLong(a[5 + i]);
+    float scale;
+    if (arity(n, 13) || to_float(a[11], &scale)) return NULL;
+    for (int i = 0; i < 6; ++i)
+        if (to_int(a[5 + i], names[i], &v[i])) return NULL;
+    if (take(a[1], "logits", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "logits", x.n0, x.n1)) return NULL;
+    if (MAYBE(a[2]) && (take(a[2], "bias", dev, NULL, 1 << FP32, 0, &b) || want_list(&b, "bias", x.n1, 0))) return NULL;
     if (take(a[3], "ids", dev, NULL, 1 << INT32, 0, &ids) || want_rows(&ids, "ids", x.n0, v[4]) ||
         take(a[4], "weights", dev, NULL, 1 << FP32, 0, &w) || want_rows(&w, "weights", x.n0, v[4]))
         return NULL;
-    const float scale = (float)PyFloat_AsDouble(a[11]);
-    if (stream_of(a[12], "logits", dev, &stream) || PyErr_Occurred()) return NULL;
+    if (stream_of(a[12], "logits", dev, &stream)) return NULL;
     return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_route_scored))(
         x.ptr, x.ld, (const float*)b.ptr, x.n0, x.n1, x.type, v[0], v[1], v[2], v[3], v[4], v[5], scale, (int32_t*)ids.ptr,
         (float*)w.ptr, stream));
