@@ -115,9 +115,10 @@ WNA16_API int wna16_moe_route_scored(const void* logits, int64_t ld, const float
  * is an absolute error; where large products cancel it can pass the sum itself.
  * (Measured at 65536 k, products of 1023 after half as many of 16129: 8e-4 of the
  * sum.)  Workspace (256-byte aligned): its first
- * word is the status word of wna16_moe_read_status, the size is below (0 for
- * up to 32 tokens).  It may be NULL: the status word is then not readable; an
- * output whose sums are missing after a device timeout is NaN either way. */
+ * word is the status word of wna16_moe_read_status, the size is below.  It is 0
+ * for up to 32 tokens; a workspace of at least 4 bytes gets the status word all
+ * the same.  It may be NULL: the status word is then not readable; an output
+ * whose sums are missing after a device timeout is NaN either way. */
 WNA16_API int wna16_moe_linear_q8(const int8_t* xq, const float* x_scales, const int8_t* wq, const float* w_scales,
                                   const float* bias, const void* addend, int64_t T, int64_t K, int64_t N, int type,
                                   void* out, void* workspace, size_t workspace_bytes, void* stream);

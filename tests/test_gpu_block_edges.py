@@ -308,3 +308,20 @@ def test_linear_large_sums_that_cancel(moe, T, K):
         out = moe.linear_q8(xq, torch.ones(T, device="cuda"), wq, torch.ones(N, device="cuda"), dtype=FP).double()
         tol = 0.0 if T <= 32 or K <= 1024 else K / 16 * 2.0 ** -20 * S
         assert bool(((out - ref).abs() <= U * ref.abs() + tol).all()), float(((out - ref).abs() / S).max())
+
+
+@pytest.mark.parametrize("T", [1, 32, 33, 600])
+def test_linear_status_for_any_number_of_tokens(moe, T):
+    """A workspace that is kept for larger batches holds this call's status, not what was there."""
+    K, N = 512, 384
+    ws = torch.full((256,), 0x5a, dtype=torch.uint8, device="cuda")
+    xq, wq = torch.ones(T, K, dtype=I8, device="cuda"), torch.ones(N, K, dtype=I8, device="cuda")
+    out = moe.linear_q8(xq, torch.ones(T, device="cuda"), wq, torch.ones(N, device="cuda"), workspace=ws, dtype=FP)
+    assert bool((out == K).all())
+    assert moe.read_status(ws) == moe.OK
+    assert bool((ws[4:] == 0x5a).all())
+    if T <= 32:                                                     # none is needed
+        for small in (ws[:0], ws[:3], ws[1:9], ws[8:16]):
+            again = moe.linear_q8(xq, torch.ones(T, device="cuda"), wq, torch.ones(N, device="cuda"), workspace=small, dtype=FP)
+            assert torch.equal(out, again)
+        assert bool((ws[16:] == 0x5a).all())

@@ -321,7 +321,9 @@ int wna16_moe_linear_q8(const int8_t* xq, const float* x_scales, const int8_t* w
         if (workspace_bytes < need)
             return set_error(WNA16_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     }
-    const Range outs[2] = {{out, static_cast<size_t>(T * N) * es, "out"}, {workspace, workspace ? need : 0, "workspace"}};
+    // where none is needed, the status word is written if there is room for it
+    if (workspace_bytes < sizeof(int) || !aligned(workspace, sizeof(int))) workspace = nullptr;
+    const Range outs[2] = {{out, static_cast<size_t>(T * N) * es, "out"}, {workspace, need ? need : sizeof(int), "workspace"}};
     const Range ins[6] = {{xq, static_cast<size_t>(T * K), "xq"},
                           {wq, static_cast<size_t>(N * K), "wq"},
                           {x_scales, static_cast<size_t>(T) * 4, "x_scales"},

@@ -887,7 +887,7 @@ template <typename T>
 int run_typed(const LinearParams& p, void* workspace, cudaStream_t s) {
     int sms = 0, max_smem = 0;
     if (int rc = device_limits(sms, max_smem)) return rc;
-    int* status = p.T <= kSmallTokens ? nullptr : static_cast<int*>(workspace);
+    auto* status = static_cast<int*>(workspace);
     auto small = [&] { return cuda_error(launch_small<T>(p, sms, status, s), "8-bit linear launch"); };
     if (p.T <= kSmallTokens) return small();
     int active[kMaxSplit];
