@@ -55,7 +55,11 @@ typedef enum { WNA16_GROUP_TOP2 = 0, WNA16_GROUP_MAX = 1 } wna16_group_score;
  * norm_out contiguous; weight [K] of `weight_type` (`type` or fp32).  At least
  * one of norm_out and q.  residual_out may be x or residual itself (same
  * pointer and ld = K); outputs must not overlap inputs otherwise.
- * 1 <= K <= 32768; eps >= 0. */
+ * 1 <= K <= 32768; eps >= 0.
+ * The sum of h^2 is an fp32 one: where it passes 3.4e38 (values above 1e18) y is 0, and
+ * where the mean and eps are both below 2^-126 (eps 0: values below 1e-19) y loses bits
+ * and, where they are 0, is not finite.
+ * Rows (runs) with |h weight| below 2^-119 are stored in 8 bits as zeros. */
 WNA16_API int wna16_moe_add_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                        const void* weight, int weight_type, int64_t T, int64_t K, int type, float eps,
                                        int q_type, int group_size, void* q, float* scales, void* residual_out,

@@ -72,6 +72,22 @@ def test_norm_residual_out_without_a_residual(moe):
     assert none is None and torch.equal(q, q2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("qt", [I8, torch.float8_e4m3fn])
+def test_norm_of_tiny_rows(moe, qt, group):
+    """Rows that the norm makes large again (a small eps): right as far as their codes can be made in
+    fp32, zeros below that, and never the codes of an infinite factor."""
+    x = randn(6, 256, seed=5)
+    for t, size in enumerate((1e-20, 1e-30, 1e-33, 5e-36, 1e-38, 1e-44)):
+        x[t] *= size
+    w = torch.ones(256, device="cuda")
+    q, s, _, no = moe.add_rmsnorm_q8(x, w, eps=1e-30, q_dtype=qt, group_size=group, want_norm=True)
+    _, y = norm_ref(x, w, None, float(torch.tensor(1e-30)))
+    check(no[:4], y[:4], 33 * U, "norm_out")
+    check_q8(moe, q[:4], s[:4], y[:4], group, 32 * U, "tiny")
+    assert not bool(s[4:].any()) and not bool(moe.dequantize_q8(q[4:], s[4:], dtype=FP).any())
+
+
 # ---------------------------------------------------------------- routing
 
 

@@ -262,6 +262,8 @@ __device__ __forceinline__ void scale_of(float most, float inv, int q_type, floa
         factor *= Q;
     } else {
         factor = Q / most;
+        // Below 2^-119 there is no such factor in fp32.  (For an eps above 1e-11 these rows are below 2^-100.)
+        if (factor == INFINITY) scale = factor = 0.0f;
     }
 }
 
