@@ -91,9 +91,9 @@ WNA16_API int wna16_moe_dequantize_q8(const void* q, const float* scales, int64_
  * exact scores: without a bias the experts' order is the logits' order; else it
  * is made on 32-bit scores, and again on 64-bit ones for a token in which two
  * neighbours in the order are closer than the 32-bit error.
- * A logit of -inf (a masked expert) or NaN scores 0, and so does one below -709 with
- * sigmoid scores; a token without any other gets the lowest experts (by bias) with
- * weights 0.  Softmax: logits of +inf share the whole weight.  A bias of +inf counts
+ * A logit of -inf (a masked expert) or NaN scores 0, and so does one below -709
+ * (sigmoid) or 709 below the token's largest (softmax); a token without any other
+ * gets the lowest experts (by bias) with weights 0.  Softmax: logits of +inf share the whole weight.  A bias of +inf counts
  * as fp32's largest number, one of -inf or NaN as its lowest.
  *   logits        fp32, bf16 or fp16 device [T, E], rows ld apart
  *   bias          fp32 device [E] or NULL

@@ -7,6 +7,7 @@ import ctypes
 import dataclasses
 import itertools
 
+import numpy as np
 import pytest
 import torch
 
@@ -262,6 +263,25 @@ def test_route_weights_of_sigmoids_below_the_smallest(moe, bias, centre):
     _, rw = route_ref(logits, k, "sigmoid", b, 1, 1, "top2", False, 2.5)
     _, got = moe.route_scored(logits, k, bias=b, renormalize=False, scale=2.5)
     assert bool((torch.from_numpy(rw) - got.double().cpu()).abs().le(256 * U * torch.from_numpy(rw) + 4 * 2.0 ** -149).all())
+
+
+@pytest.mark.parametrize("dt", [FP, BF, HF])
+def test_route_masked_experts_that_a_bias_chooses(moe, dt):
+    """Experts masked by their type's lowest value, or by -30000, and chosen all the same score 0: they
+    share no weight, alone or beside one that is not masked."""
+    logits = randn(30, 32, seed=5, dtype=dt)
+    bias = torch.zeros(32, device="cuda")
+    bias[8:16] = 4.0
+    for score in ("softmax", "sigmoid"):
+        for mask in (-30000.0, torch.finfo(dt).min, -INF):
+            z = logits.clone()
+            z[:, 8:16] = mask
+            z[::3, 11] = 0.5
+            for k in (1, 4, 8):
+                for G, Gk in ((1, 1), (4, 1)):
+                    ids, w = check_route(moe, z, k, score=score, bias=bias, G=G, Gk=Gk)
+                    live = (ids == 11) & (np.arange(30) % 3 == 0)[:, None]
+                    assert not w[~live].any() and np.abs(w[live] - 1).max() < 1e-6
 
 
 # ---------------------------------------------------------------- the block

@@ -371,8 +371,8 @@ __device__ __noinline__ void settle_order(Token t, Candidates& cand, int count) 
 // Weights of a token with a sigmoid near or below fp32's smallest normal number (z: the
 // lane's chosen logit, -INFINITY: none).  Where they will be divided by their sum they are
 // taken relative to the largest, so that they keep their bits.  A logit below -709
-// scores 0, as where the sigmoid is 1 / (1 + exp(-z)) in 64 bits: masks with a type's
-// lowest value are down there.
+// (softmax: 709 below the largest) scores 0, as where the score is computed in 64 bits:
+// masks with a type's lowest value are down there, and share no weight among them.
 __device__ __noinline__ float deep_sigmoid(float z, int renormalize) {
     const float most = key_value(__reduce_max_sync(kAll, order_key(z)));
     const float shift = renormalize ? fminf(most, 0.0f) : 0.0f;
@@ -648,7 +648,8 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
         if (unsure) my_id = choose64(t, PL);
     }
 
-    const float z_mine = lane < p.topk ? t.logit(my_id) : -INFINITY;
+    float z_mine = lane < p.topk ? t.logit(my_id) : -INFINITY;
+    if (SOFTMAX && z_mine < t.m - 709.0f) z_mine = -INFINITY;   // a score of 0: see deep_sigmoid
     if (SOFTMAX && p.renormalize) t.softmax_of(key_value(__reduce_max_sync(kAll, order_key(z_mine))));
     float w = lane < p.topk ? t.score(z_mine) : 0.0f;
     if (!SOFTMAX && __any_sync(kAll, z_mine < -87.0f && z_mine > -INFINITY)) w = deep_sigmoid(z_mine, p.renormalize);
