@@ -17,9 +17,10 @@
  *
  * 8-bit rows (q, scales).  A row of K values, or each run of group_size values
  * of it (group_size 0: the whole row), is held as one fp32 scale and K codes:
- *   m = max |y|,  scale = m / Q,  code = round(y / scale),  value = code * scale
+ *   m = max |y|,  scale = m / Q,  code = round(y * (Q / m)),  value = code * scale
  * with Q = 127 and codes -127..127 rounded to nearest, ties to even
- * (WNA16_Q8_INT8), or Q = 448 and codes in e4m3 (WNA16_Q8_E4M3).  m below
+ * (WNA16_Q8_INT8), or Q = 448 and codes in e4m3 (WNA16_Q8_E4M3).  The quotient and
+ * the product are fp32: a value that near to a half step may get either code.  m below
  * 2^-100 gives scale 0 and codes 0.  A row (run) that holds a NaN or an
  * infinity gets a scale that is not finite and codes 0, so that all its values
  * read back as NaN.
@@ -67,7 +68,8 @@ WNA16_API int wna16_moe_add_rmsnorm_q8(const void* x, int64_t ldx, const void* r
 
 /* h = silu(min(g, L)) * clamp(u, -L, L), g = gu[t][0..N), u = gu[t][N..2N);
  * (q, scales) = h in 8 bits.  L = swiglu_limit > 0 (+inf: no clamp), as in
- * wna16_moe_forward; NaN passes through the clamps.  1 <= N <= 32768. */
+ * wna16_moe_forward; NaN passes through the clamps.  The sigmoid below g = -87 is 0.
+ * 1 <= N <= 32768. */
 WNA16_API int wna16_moe_swiglu_q8(const void* gu, int64_t ldg, int64_t T, int64_t N, int type, float swiglu_limit,
                                   int q_type, int group_size, void* q, float* scales, void* stream);
 

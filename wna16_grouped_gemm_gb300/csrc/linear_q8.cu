@@ -36,13 +36,17 @@
 //   epilogue (warps 20..27)    tcgen05.ld, scales, bias, addend, store
 // (with few rows of B: four sets for A, and the epilogue's warps convert B first)
 // Only codes cross the memory system, and A's fp16 form never passes through
-// shared memory.  When there are few tiles, 2 to 4 pairs form a cluster
+// shared memory.  (Operands are handed to the leader's issuer by arrivals that release at CTA
+// scope, also from the other CTA; what reads them are the pair's tensor cores.  That this is
+// enough is not in the PTX memory model: it rests on the fences before the arrival and on
+// the comparison with integers.)  When there are few tiles, 2 to 4 pairs form a cluster
 // that shares a tile's K and adds its sums through distributed shared memory.
 // Measured, tokens x 4096 x 4096 (of the 1917 TFLOP/s of a measured bf16 product):
 // 64 11.6 us, 512 20.6, 1024 24.3, 2048 42.3 (0.85), 4096 79 (0.91), 8192 151 to 160
-// (0.90 to 0.95, power); 8192 x 2048 x 4096 93 (0.77: the accumulator takes half of TMEM
+// (0.90 to 0.95, power); 8192 x 2048 x 4096 88 (0.82: the accumulator takes half of TMEM
 // and the operands of a stage the rest, so a tile's epilogue is not under the next
-// tile's products); 2048 has 152 tiles of 224 columns, two for each pair.
+// tile's products; there with a bias 102, an addend 118, fp32 results 102); 2048 has 152 tiles of
+// 224 columns, two for each pair.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
