@@ -173,7 +173,8 @@ static PyObject* add_rmsnorm_q8(PyObject* self, PyObject* const* a, Py_ssize_t n
     void* stream;
     int group;
     float eps;
-    if (arity(n, 11) || to_float(a[8], &eps) || to_int(a[9], "group_size", &group) || take(a[1], "x", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "x", x.n0, x.n1) ||
+    if (arity(n, 11) || to_float(a[8], &eps) || to_int(a[9], "group_size", &group) ||
+        take(a[1], "x", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "x", x.n0, x.n1) ||
         take(a[2], "weight", dev, NULL, 1u << x.type | 1u << FP32, 0, &w))
         return NULL;
     if (w.dims != 1 || w.n0 != x.n1) {
@@ -200,7 +201,9 @@ static PyObject* swiglu_q8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     void* stream;
     int group;
     float limit;
-    if (arity(n, 7) || to_float(a[4], &limit) || to_int(a[5], "group_size", &group) || take(a[1], "gu", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "gu", x.n0, x.n1)) return NULL;
+    if (arity(n, 7) || to_float(a[4], &limit) || to_int(a[5], "group_size", &group) ||
+        take(a[1], "gu", -1, &dev, FLOATS, 1, &x) || want_rows(&x, "gu", x.n0, x.n1))
+        return NULL;
     if (x.n1 % 2) {
         PyErr_Format(PyExc_ValueError, "gu must have an even number of columns, got %lld", (long long)x.n1);
         return NULL;
