@@ -218,7 +218,11 @@ def linear_q8(xq, x_scales, wq, w_scales, *, bias=None, addend=None, dtype=torch
 
 @dataclasses.dataclass
 class MoEBlockWeights:
-    """Weights of one MoE block: norm, router, routed experts (WNA16) and shared expert (8 bits)."""
+    """Weights of one MoE block: norm, router, routed experts (WNA16, or e4m3 in blocks) and shared expert (8 bits).
+
+    Routed experts in 8-bit floats: w13_packed and w2_packed are float8_e4m3fn [E, 2N, K] and [E, K, N], their scales
+    fp32 per block of 128 x 128, as for forward_f8().  A shared expert in 8-bit floats: shared_w13 and shared_w2 are
+    float8_e4m3fn with such scales, as for linear_f8()."""
     norm: torch.Tensor              # [K], bf16 or fp32
     gate: torch.Tensor              # [E, K] router: bf16 (logits rounded to bf16) or fp32 (fp32 logits)
     gate_bias: torch.Tensor | None  # fp32 [E], for the choice only
@@ -226,13 +230,13 @@ class MoEBlockWeights:
     w13_scales: torch.Tensor
     w2_packed: torch.Tensor
     w2_scales: torch.Tensor
-    shared_w13: torch.Tensor        # int8 [2 Ns, K], gate rows then up rows
+    shared_w13: torch.Tensor        # int8 (a scale per row) or e4m3 (per block) [2 Ns, K], gate rows then up rows
     shared_w13_scales: torch.Tensor
-    shared_w2: torch.Tensor         # int8 [K, Ns]
+    shared_w2: torch.Tensor         # [K, Ns], of the same type
     shared_w2_scales: torch.Tensor
 
 
-def moe_block(x, residual, w: MoEBlockWeights, *, topk: int, bits: int, group_size: int, group_size_w2: int = 0,
+def moe_block(x, residual, w: MoEBlockWeights, *, topk: int, bits: int = 0, group_size: int = 0, group_size_w2: int = 0,
               score: str = "sigmoid", groups: int = 1, topk_groups: int = 1, group_score: str = "top2",
               renormalize: bool = True, scale: float = 1.0, swiglu_limit: float = 7.0, eps: float = 1e-6):
     """One MoE block: (out, residual) with h = x + residual,
@@ -245,13 +249,33 @@ def moe_block(x, residual, w: MoEBlockWeights, *, topk: int, bits: int, group_si
     experts is exact for the logits that route_scored gets, which are a library
     product in the gate's type: with a bf16 gate they are rounded to bf16, and
     experts whose logits agree to 8 bits are taken by index; with an fp32 gate
-    they are fp32."""
-    q, qs, h, normed = add_rmsnorm_q8(x, w.norm, residual, eps=eps, want_norm=True)
+    they are fp32.
+
+    Experts in 8-bit floats take the norm's rows in e4m3 in groups of 128 (bits and group sizes, which
+    WNA16 experts need, are not used then).  The norm writes the 8-bit rows of the shared expert's type; if the routed experts
+    are in 8-bit floats and it is not, theirs are made from its 16-bit rows."""
+    from . import f8
+
+    f8_rows = dict(q_dtype=torch.float8_e4m3fn, group_size=f8.BLOCK)
+    shared_f8, routed_f8 = (t.dtype == torch.float8_e4m3fn for t in (w.shared_w13, w.w13_packed))
+    if not routed_f8 and not (bits and group_size):
+        raise TypeError("WNA16 experts need bits and group_size")
+    q, qs, h, normed = add_rmsnorm_q8(x, w.norm, residual, eps=eps, want_norm=True, **(f8_rows if shared_f8 else {}))
     logits = normed.to(w.gate.dtype) @ w.gate.t()
     ids, weights = route_scored(logits, topk, score=score, bias=w.gate_bias, groups=groups,
                                 topk_groups=topk_groups, group_score=group_score, renormalize=renormalize, scale=scale)
-    routed = binding.forward(normed, ids, weights, w.w13_packed, w.w13_scales, w.w2_packed, w.w2_scales, bits=bits,
-                             group_size=group_size, group_size_w2=group_size_w2, swiglu_limit=swiglu_limit)
+    if routed_f8:
+        rq, rs = (q, qs) if shared_f8 else quantize_q8(normed, **f8_rows)
+        routed = f8.forward_f8(rq, rs, ids, weights, w.w13_packed, w.w13_scales, w.w2_packed, w.w2_scales,
+                               swiglu_limit=swiglu_limit, dtype=x.dtype)
+    else:
+        routed = binding.forward(normed, ids, weights, w.w13_packed, w.w13_scales, w.w2_packed, w.w2_scales, bits=bits,
+                                 group_size=group_size, group_size_w2=group_size_w2, swiglu_limit=swiglu_limit)
+    if shared_f8:
+        gu = f8.linear_f8(q, qs, w.shared_w13, w.shared_w13_scales, dtype=x.dtype)
+        hq, hs = swiglu_q8(gu, swiglu_limit=swiglu_limit, **f8_rows)
+        out = f8.linear_f8(hq, hs, w.shared_w2, w.shared_w2_scales, addend=routed, out=routed)
+        return out, x if residual is None else h
     gu = linear_q8(q, qs, w.shared_w13, w.shared_w13_scales, dtype=x.dtype)
     hq, hs = swiglu_q8(gu, swiglu_limit=swiglu_limit)
     return linear_q8(hq, hs, w.shared_w2, w.shared_w2_scales, addend=routed, out=routed), x if residual is None else h

@@ -1,0 +1,143 @@
+// Weights to e4m3 with one scale per block of 128 x 128:
+//   m = max |w|,  scale = m / 448,  code = e4m3(w * (448 / m))
+//
+// Bound by the bytes of the weights, read once.  A thread block has one block of
+// the weight in registers from its reads to the codes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "f8.h"
+#include "ptx.cuh"
+
+namespace wna16 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kV = 8;                                              // neighbouring values per load
+constexpr int kTurns = kScaleBlock * kScaleBlock / (kThreads * kV);
+constexpr int kPitch = kScaleBlock + 16;                           // of a row of codes in shared memory
+constexpr float kTiny = 7.888609052210118e-31f;                    // 2^-100
+constexpr float kQ = 448.0f;
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) {
+    if constexpr (sizeof(T) == 4)
+        return v;
+    else if constexpr (std::is_same<T, __half>::value)
+        return __half2float(v);
+    else
+        return __bfloat162float(v);
+}
+
+// COLUMNS: w's columns are contiguous (a transposed weight), else its rows.
+template <typename T, bool COLUMNS, bool VEC>
+__global__ void __launch_bounds__(kThreads) blocks_kernel(const BlocksParams p) {
+    __shared__ uint32_t warp_max[kThreads / 32];
+    __shared__ alignas(16) uint8_t tile[COLUMNS ? kScaleBlock * kPitch : 16];
+    pdl_wait();
+    pdl_trigger();
+    const int k_blocks = static_cast<int>(p.K / kScaleBlock), n_blocks = static_cast<int>((p.N + kScaleBlock - 1) / kScaleBlock);
+    const int64_t b = blockIdx.x;   // (e, n block, k block)
+    const int kb = static_cast<int>(b % k_blocks), nb = static_cast<int>(b / k_blocks % n_blocks);
+    const int64_t e = b / k_blocks / n_blocks;
+    const int64_t n0 = static_cast<int64_t>(nb) * kScaleBlock, k0 = static_cast<int64_t>(kb) * kScaleBlock;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kScaleBlock), p.N - n0));
+    const T* w = static_cast<const T*>(p.w) + e * p.se + n0 * p.sn + k0 * p.sk;
+    // a thread's 8 values of turn i: `fast` along the contiguous axis, `slow` along the other
+    const int fast = threadIdx.x % (kScaleBlock / kV) * kV, slow0 = threadIdx.x / (kScaleBlock / kV);
+    constexpr int kStep = kThreads / (kScaleBlock / kV);
+    struct alignas(16) Chunk {
+        T v[kV];
+    } c[kTurns];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int slow = slow0 + i * kStep;
+        const T* at = w + (COLUMNS ? slow * p.sk : slow * p.sn) + fast;
+        const int count = COLUMNS ? rows - fast : (slow < rows ? kV : 0);
+        if (VEC && count >= kV) {
+#pragma unroll
+            for (int j = 0; j < static_cast<int>(sizeof(Chunk) / 16); ++j)
+                reinterpret_cast<uint4*>(c[i].v)[j] = __ldg(reinterpret_cast<const uint4*>(at) + j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kV; ++j) c[i].v[j] = j < count ? at[j] : T(0.0f);
+        }
+    }
+    // the largest magnitude as bits: infinities and NaN are above all numbers
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+#pragma unroll
+        for (int j = 0; j < kV; ++j) top = max(top, __float_as_uint(to_f(c[i].v[j])) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) top = max(top, warp_max[i]);
+    const float m = __uint_as_float(top);
+    const bool some = m >= kTiny && top < 0x7f800000u;
+    const float by = some ? kQ / m : 0.0f;
+    if (threadIdx.x == 0) p.scales[b] = m < kTiny ? 0.0f : m / kQ;   // not finite where m is not
+    uint8_t* q = p.q + (e * p.N + n0) * p.K + k0;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int slow = slow0 + i * kStep;
+        uint32_t code[2] = {0, 0};
+        if (some) {
+#pragma unroll
+            for (int j = 0; j < kV; j += 2) {
+                const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(to_f(c[i].v[j]) * by, to_f(c[i].v[j + 1]) * by),
+                                                              __NV_SATFINITE, __NV_E4M3);
+                code[j / 4] |= two << (j % 4 * 8);
+            }
+        }
+        if (COLUMNS) {
+#pragma unroll
+            for (int j = 0; j < kV; ++j) tile[(fast + j) * kPitch + slow] = static_cast<uint8_t>(code[j / 4] >> (j % 4 * 8));
+        } else if (slow < rows) {
+            if (reinterpret_cast<uintptr_t>(p.q) % 8 == 0) {
+                *reinterpret_cast<uint2*>(q + slow * p.K + fast) = make_uint2(code[0], code[1]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kV; ++j) q[slow * p.K + fast + j] = static_cast<uint8_t>(code[j / 4] >> (j % 4 * 8));
+            }
+        }
+    }
+    if (COLUMNS) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * (kScaleBlock / 16); i += kThreads) {
+            const int n = i / (kScaleBlock / 16), k = i % (kScaleBlock / 16) * 16;
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + n * kPitch + k);
+            uint8_t* to = q + static_cast<int64_t>(n) * p.K + k;
+            if (reinterpret_cast<uintptr_t>(p.q) % 16 == 0) {
+                *reinterpret_cast<uint4*>(to) = v;
+            } else {
+                for (int j = 0; j < 16; ++j) to[j] = tile[n * kPitch + k + j];
+            }
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch(const BlocksParams& p, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.E * ((p.N + kScaleBlock - 1) / kScaleBlock) * (p.K / kScaleBlock)));
+    const bool columns = p.sk != 1;
+    const uint64_t pitch = static_cast<uint64_t>(columns ? p.sk : p.sn) | static_cast<uint64_t>(p.se);
+    const bool vec = (pitch * sizeof(T)) % 16 == 0 && reinterpret_cast<uintptr_t>(p.w) % 16 == 0;
+    if (columns) return launch_pdl(vec ? blocks_kernel<T, true, true> : blocks_kernel<T, true, false>, grid, dim3(kThreads), 0, s, p);
+    return launch_pdl(vec ? blocks_kernel<T, false, true> : blocks_kernel<T, false, false>, grid, dim3(kThreads), 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_blocks_f8(int type, const BlocksParams& p, cudaStream_t s) {
+    if (type == kBf16) return launch<__nv_bfloat16>(p, s);
+    if (type == kFp16) return launch<__half>(p, s);
+    return launch<float>(p, s);
+}
+
+}  // namespace wna16

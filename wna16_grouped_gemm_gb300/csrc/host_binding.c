@@ -1,5 +1,6 @@
 /* Argument checks and marshalling of the operators around the routed experts
- * (include/wna16_moe_block.h), as a CPython module: a decode step makes several
+ * (include/wna16_moe_block.h) and of routed experts in 8-bit floats
+ * (include/wna16_moe_f8.h), as a CPython module: a decode step makes several
  * small calls, and the checks of seven tensors in Python took longer than the
  * kernel (a norm call on the Grace cores: 14.5 us, and 8.4 us with lean checks
  * through ctypes).  The entry points come in as addresses, so the module serves
@@ -10,7 +11,7 @@
 #include <limits.h>
 #include <stdint.h>
 
-#include "../../include/wna16_moe_block.h"
+#include "../../include/wna16_moe_f8.h"
 
 enum { BF16, FP16, FP32, INT8, E4M3, INT32, UINT8, TYPES };
 static const char* const kTypeNames[TYPES] = {"bfloat16", "float16", "float32", "int8", "float8_e4m3fn", "int32", "uint8"};
@@ -23,11 +24,14 @@ typedef struct {
     char* ptr;
     int64_t n0, n1, ld; /* sizes ([n0] or [n0, n1]), distance of rows */
     int dims, type;
+    int64_t n[3], st[3]; /* of up to three dims: sizes, and (layout ANY) strides */
 } Tensor;
 
+enum { WHOLE, ROWS, ANY }; /* what has to be contiguous: all of it, its rows, nothing */
+
 /* Checks one tensor and takes it apart.  dev < 0: any CUDA device, returned in
- * *dev_out.  types: mask of allowed types; rows: only the rows have to be contiguous. */
-static int take(PyObject* t, const char* name, long dev, long* dev_out, unsigned types, int rows, Tensor* o) {
+ * *dev_out.  types: mask of allowed types; most: dims allowed. */
+static int take_dims(PyObject* t, const char* name, long dev, long* dev_out, unsigned types, int layout, int most, Tensor* o) {
     PyObject* v = PyObject_CallMethodNoArgs(t, s_get_device);
     long d = -1;
     if (v) {
@@ -62,16 +66,22 @@ static int take(PyObject* t, const char* name, long dev, long* dev_out, unsigned
     Py_DECREF(v);
     if (!(v = PyObject_GetAttr(t, s_shape))) return -1;
     o->dims = PyTuple_Check(v) ? (int)PyTuple_GET_SIZE(v) : 0;
-    if (o->dims != 1 && o->dims != 2) {
-        PyErr_Format(PyExc_ValueError, "%s must have 1 or 2 dims, got %R", name, v);
+    if (o->dims < 1 || o->dims > most) {
+        PyErr_Format(PyExc_ValueError, "%s must have %s dims, got %R", name, most == 2 ? "1 or 2" : "1 to 3", v);
         Py_DECREF(v);
         return -1;
     }
+    for (int i = 0; i < o->dims; ++i) o->n[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i));
     o->n0 = PyLong_AsLongLong(PyTuple_GET_ITEM(v, 0));
-    o->n1 = o->dims == 2 ? PyLong_AsLongLong(PyTuple_GET_ITEM(v, 1)) : 1;
+    o->n1 = o->dims >= 2 ? PyLong_AsLongLong(PyTuple_GET_ITEM(v, 1)) : 1;
     Py_DECREF(v);
     o->ld = o->n1 > 0 ? o->n1 : 1;
-    if (rows) {
+    if (layout == ANY) {
+        if (!(v = PyObject_CallMethodNoArgs(t, s_stride))) return -1;
+        if (PyTuple_Check(v) && PyTuple_GET_SIZE(v) == o->dims)
+            for (int i = 0; i < o->dims; ++i) o->st[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i));
+        Py_DECREF(v);
+    } else if (layout == ROWS) {
         if (!(v = PyObject_CallMethodNoArgs(t, s_stride))) return -1;
         if (o->dims == 2 && PyTuple_Check(v) && PyTuple_GET_SIZE(v) == 2) {
             if (o->n0 > 1) o->ld = PyLong_AsLongLong(PyTuple_GET_ITEM(v, 0));
@@ -95,6 +105,10 @@ static int take(PyObject* t, const char* name, long dev, long* dev_out, unsigned
     o->ptr = (char*)PyLong_AsVoidPtr(v);
     Py_DECREF(v);
     return PyErr_Occurred() ? -1 : 0;
+}
+
+static int take(PyObject* t, const char* name, long dev, long* dev_out, unsigned types, int layout, Tensor* o) {
+    return take_dims(t, name, dev, dev_out, types, layout, 2, o);
 }
 
 static int want_rows(const Tensor* t, const char* name, int64_t n0, int64_t n1) {
@@ -296,6 +310,169 @@ static PyObject* linear_q8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         x.n0, x.n1, w.n0, o.type, o.ptr, work.ptr, work.ptr ? (size_t)work.n0 : 0, stream));
 }
 
+static int want_shape(const Tensor* t, const char* name, int dims, int64_t a, int64_t b, int64_t c) {
+    const int64_t want[3] = {a, b, c};
+    int same = t->dims == dims;
+    for (int i = 0; same && i < dims; ++i) same = t->n[i] == want[i];
+    if (same) return 0;
+    if (dims == 3)
+        PyErr_Format(PyExc_ValueError, "%s must be [%lld, %lld, %lld]", name, (long long)a, (long long)b, (long long)c);
+    else
+        PyErr_Format(PyExc_ValueError, "%s must be [%lld, %lld]", name, (long long)a, (long long)b);
+    return -1;
+}
+
+/* (entry, x, x_scales, ids, E, expert_begin, rows, row_scales, offsets, inv, stream) */
+static PyObject* sort_tokens(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor x = {0}, xs = {0}, ids, rows = {0}, rs = {0}, off, inv;
+    long dev;
+    void* stream;
+    int E, begin;
+    if (arity(n, 11) || to_int(a[4], "experts", &E) || to_int(a[5], "expert_begin", &begin) ||
+        take(a[3], "topk_ids", -1, &dev, 1 << INT32, WHOLE, &ids) || want_rows(&ids, "topk_ids", ids.n0, ids.n1))
+        return NULL;
+    if (ids.n1 > 1024 || ids.n0 >= (int64_t)1 << 31) {
+        PyErr_Format(PyExc_ValueError, "topk_ids [%lld, %lld] is too large", (long long)ids.n0, (long long)ids.n1);
+        return NULL;
+    }
+    const int64_t R = ids.n0 * ids.n1;
+    if (MAYBE(a[1]) && (take(a[1], "x", dev, NULL, FLOATS | CODES, ROWS, &x) || want_rows(&x, "x", ids.n0, x.n1) ||
+                        take(a[6], "rows", dev, NULL, 1u << x.type, WHOLE, &rows) || want_rows(&rows, "rows", R, x.n1)))
+        return NULL;
+    if (MAYBE(a[2]) && (take(a[2], "scales", dev, NULL, 1 << FP32, WHOLE, &xs) || want_rows(&xs, "scales", ids.n0, xs.n1) ||
+                        take(a[7], "row_scales", dev, NULL, 1 << FP32, WHOLE, &rs) || want_rows(&rs, "row_scales", R, xs.n1)))
+        return NULL;
+    if (take(a[8], "offsets", dev, NULL, 1 << INT32, WHOLE, &off) || want_list(&off, "offsets", (int64_t)E + 1, 0) ||
+        take(a[9], "inv", dev, NULL, 1 << INT32, WHOLE, &inv) || want_rows(&inv, "inv", ids.n0, ids.n1) ||
+        stream_of(a[10], "topk_ids", dev, &stream))
+        return NULL;
+    const int type = !MAYBE(a[1]) || x.type == INT8 || x.type == E4M3 ? WNA16_TYPE_Q8 : x.type;
+    return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_sort_tokens))(
+        x.ptr, x.ld, (const float*)xs.ptr, xs.n1, ids.n0, MAYBE(a[1]) ? x.n1 : 1, type, (const int32_t*)ids.ptr, (int)ids.n1,
+        E, begin, rows.ptr, (float*)rs.ptr, (int32_t*)off.ptr, (int32_t*)inv.ptr, stream));
+}
+
+/* inv [T, topk] and weights of the same sizes */
+static int take_slots(PyObject* i, PyObject* w, long dev, int64_t T, Tensor* ti, Tensor* tw) {
+    if (take(i, "inv", dev, NULL, 1 << INT32, WHOLE, ti) || want_rows(ti, "inv", T, ti->n1)) return -1;
+    if (ti->n1 > 1024) {
+        PyErr_Format(PyExc_ValueError, "inv has %lld slots per token, at most 1024", (long long)ti->n1);
+        return -1;
+    }
+    return MAYBE(w) && (take(w, "weights", dev, NULL, 1 << FP32, WHOLE, tw) || want_rows(tw, "weights", T, ti->n1)) ? -1 : 0;
+}
+
+/* (entry, y, inv, weights, addend, out, stream) */
+static PyObject* unsort_tokens(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor y, inv, w = {0}, add = {0}, o;
+    long dev;
+    void* stream;
+    if (arity(n, 7) || take(a[1], "y", -1, &dev, FLOATS, WHOLE, &y) || want_rows(&y, "y", y.n0, y.n1) ||
+        take(a[5], "out", dev, NULL, 1u << y.type, WHOLE, &o) || want_rows(&o, "out", o.n0, y.n1) ||
+        take_slots(a[2], a[3], dev, o.n0, &inv, &w))
+        return NULL;
+    if (MAYBE(a[4]) && (take(a[4], "addend", dev, NULL, 1u << y.type, WHOLE, &add) || want_rows(&add, "addend", o.n0, y.n1)))
+        return NULL;
+    if (stream_of(a[6], "y", dev, &stream)) return NULL;
+    return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_unsort_tokens))(
+        y.ptr, y.n0, (const int32_t*)inv.ptr, (const float*)w.ptr, add.ptr, o.n0, y.n1, (int)inv.n1, y.type, o.ptr, stream));
+}
+
+/* (entry, dout, inv, y, weights, dy, dweights, stream); R is the rows of dy or y */
+static PyObject* unsort_tokens_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor d, inv, y = {0}, w = {0}, dy = {0}, dw = {0};
+    long dev;
+    void* stream;
+    if (arity(n, 8) || take(a[1], "dout", -1, &dev, FLOATS, WHOLE, &d) || want_rows(&d, "dout", d.n0, d.n1) ||
+        take_slots(a[2], a[4], dev, d.n0, &inv, &w))
+        return NULL;
+    const unsigned same = 1u << d.type;
+    if (MAYBE(a[3]) && (take(a[3], "y", dev, NULL, same, WHOLE, &y) || want_rows(&y, "y", y.n0, d.n1))) return NULL;
+    if (MAYBE(a[5]) && (take(a[5], "dy", dev, NULL, same, WHOLE, &dy) ||
+                        want_rows(&dy, "dy", MAYBE(a[3]) ? y.n0 : dy.n0, d.n1)))
+        return NULL;
+    if (MAYBE(a[6]) && (take(a[6], "dweights", dev, NULL, 1 << FP32, WHOLE, &dw) || want_rows(&dw, "dweights", d.n0, inv.n1)))
+        return NULL;
+    if (stream_of(a[7], "dout", dev, &stream)) return NULL;
+    return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_unsort_tokens_grad))(
+        d.ptr, (const int32_t*)inv.ptr, y.ptr, (const float*)w.ptr, d.n0, d.n1, (int)inv.n1, MAYBE(a[3]) ? y.n0 : dy.n0,
+        d.type, dy.ptr, (float*)dw.ptr, stream));
+}
+
+/* 8-bit float rows [T, K], their scales, weights [(E,) N, K] and theirs */
+static int take_f8(PyObject* const* a, int dims, long* dev, Tensor* x, Tensor* xs, Tensor* w, Tensor* ws) {
+    if (take(a[1], "xq", -1, dev, 1 << E4M3, WHOLE, x) || want_rows(x, "xq", x->n0, x->n1) ||
+        take(a[2], "x_scales", *dev, NULL, 1 << FP32, WHOLE, xs) || want_rows(xs, "x_scales", x->n0, x->n1 / 128) ||
+        take_dims(a[3], "wq", *dev, NULL, 1 << E4M3, WHOLE, dims, w))
+        return -1;
+    const int64_t N = w->n[dims - 2];
+    if (dims == 3 ? want_shape(w, "wq", 3, w->n[0], N, x->n1) : want_shape(w, "wq", 2, N, x->n1, 0)) return -1;
+    if (take_dims(a[4], "w_scales", *dev, NULL, 1 << FP32, WHOLE, dims, ws)) return -1;
+    return dims == 3 ? want_shape(ws, "w_scales", 3, w->n[0], (N + 127) / 128, x->n1 / 128)
+                     : want_shape(ws, "w_scales", 2, (N + 127) / 128, x->n1 / 128, 0);
+}
+
+/* (entry, xq, x_scales, wq, w_scales, bias, addend, out, workspace, stream) */
+static PyObject* linear_f8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor x, xs, w = {0}, ws = {0}, b = {0}, add = {0}, o, work = {0};
+    long dev;
+    void* stream;
+    if (arity(n, 10) || take_f8(a, 2, &dev, &x, &xs, &w, &ws) || take(a[7], "out", dev, NULL, FLOATS, WHOLE, &o) ||
+        want_rows(&o, "out", x.n0, w.n[0]))
+        return NULL;
+    if (MAYBE(a[5]) && (take(a[5], "bias", dev, NULL, 1 << FP32, WHOLE, &b) || want_list(&b, "bias", w.n[0], 0))) return NULL;
+    if (MAYBE(a[6]) && (take(a[6], "addend", dev, NULL, 1u << o.type, WHOLE, &add) || want_rows(&add, "addend", x.n0, w.n[0])))
+        return NULL;
+    if (MAYBE(a[8]) && (take(a[8], "workspace", dev, NULL, 1 << UINT8, WHOLE, &work))) return NULL;
+    if (stream_of(a[9], "xq", dev, &stream)) return NULL;
+    return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_linear_f8))(
+        x.ptr, (const float*)xs.ptr, w.ptr, (const float*)ws.ptr, (const float*)b.ptr, add.ptr, x.n0, x.n1, w.n[0], o.type,
+        o.ptr, work.ptr, work.ptr ? (size_t)work.n0 : 0, stream));
+}
+
+/* (entry, xq, x_scales, wq, w_scales, offsets, out, workspace, stream) */
+static PyObject* grouped_linear_f8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor x, xs, w = {0}, ws = {0}, off, o, work = {0};
+    long dev;
+    void* stream;
+    if (arity(n, 9) || take_f8(a, 3, &dev, &x, &xs, &w, &ws) || take(a[5], "offsets", dev, NULL, 1 << INT32, WHOLE, &off) ||
+        want_list(&off, "offsets", w.n[0] + 1, 0) || take(a[6], "out", dev, NULL, FLOATS, WHOLE, &o) ||
+        want_rows(&o, "out", x.n0, w.n[1]))
+        return NULL;
+    if (MAYBE(a[7]) && (take(a[7], "workspace", dev, NULL, 1 << UINT8, WHOLE, &work))) return NULL;
+    if (stream_of(a[8], "xq", dev, &stream)) return NULL;
+    return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_grouped_linear_f8))(
+        x.ptr, (const float*)xs.ptr, w.ptr, (const float*)ws.ptr, (const int32_t*)off.ptr, w.n[0], x.n0, x.n1, w.n[1], o.type,
+        o.ptr, work.ptr, work.ptr ? (size_t)work.n0 : 0, stream));
+}
+
+/* (entry, w, q, scales, stream); w and q [N, K] or [E, N, K] */
+static PyObject* quantize_blocks_f8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    Tensor w = {0}, q = {0}, s = {0};
+    long dev;
+    void* stream;
+    if (arity(n, 5) || take_dims(a[1], "w", -1, &dev, FLOATS, ANY, 3, &w)) return NULL;
+    if (w.dims < 2) {
+        PyErr_SetString(PyExc_ValueError, "w must have 2 or 3 dims");
+        return NULL;
+    }
+    const int d = w.dims;
+    const int64_t E = d == 3 ? w.n[0] : 1, N = w.n[d - 2], K = w.n[d - 1];
+    if (take_dims(a[2], "q", dev, NULL, 1 << E4M3, WHOLE, 3, &q) || want_shape(&q, "q", d, w.n[0], w.n[1], w.n[2]) ||
+        take_dims(a[3], "scales", dev, NULL, 1 << FP32, WHOLE, 3, &s) ||
+        (d == 3 ? want_shape(&s, "scales", 3, E, (N + 127) / 128, K / 128) : want_shape(&s, "scales", 2, (N + 127) / 128, K / 128, 0)) ||
+        stream_of(a[4], "w", dev, &stream))
+        return NULL;
+    return PyLong_FromLong(ADDRESS(__typeof__(&wna16_moe_quantize_blocks_f8))(
+        w.ptr, E, N, K, d == 3 ? w.st[0] : 0, w.st[d - 2], w.st[d - 1], w.type, q.ptr, (float*)s.ptr, stream));
+}
+
 /* ((bfloat16, float16, float32, int8, float8_e4m3fn, int32, uint8), current_device, raw_stream) */
 static PyObject* setup(PyObject* self, PyObject* args) {
     PyObject *types, *device, *raw;
@@ -319,6 +496,8 @@ static PyObject* setup(PyObject* self, PyObject* args) {
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef kMethods[] = {{"setup", setup, METH_VARARGS, NULL}, FAST(add_rmsnorm_q8), FAST(swiglu_q8),
                                  FAST(quantize_q8), FAST(dequantize_q8), FAST(route_scored), FAST(linear_q8),
+                                 FAST(sort_tokens), FAST(unsort_tokens), FAST(unsort_tokens_grad), FAST(linear_f8),
+                                 FAST(grouped_linear_f8), FAST(quantize_blocks_f8),
                                  {NULL, NULL, 0, NULL}};
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_host", "Argument checks of the block operators.", -1, kMethods,
                                      NULL, NULL, NULL, NULL};
