@@ -57,7 +57,7 @@ struct LinearF8Params {
     int* status = nullptr;
 };
 // returns a wna16_status and sets the error message
-int run_linear_f8(LinearF8Params p, cudaStream_t stream);
+int run_linear_f8(const LinearF8Params& p, cudaStream_t stream);
 
 // Weights to e4m3 in blocks (blocks_f8.cu).
 struct BlocksParams {

@@ -1,4 +1,5 @@
-// Plans of the block-scaled e4m3 products (linear_f8_thin.cu, linear_f8_wide.cu).
+// Plans of the block-scaled e4m3 products: which kernel (linear_f8_small.cu, linear_f8_thin.cu,
+// linear_f8_wide.cu), how many rows per tile, how many parts of K.
 #include <algorithm>
 
 #include "../../include/wna16_moe_f8.h"
@@ -7,6 +8,84 @@
 
 namespace wna16 {
 
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Estimated times in us, from calls timed by themselves (T x K x N with weights that are not in L2; small with 8, 16 or
+// 32 rows per block / thin with 16 to 128 rows per tile and its best split of K / wide):
+//   4 x 4096 x 4096      5.7 / 8.2 / -       77 x 2048 x 1000    6.0 / 7.4 / 10.8     200 x 4096 x 4096   - / 19.1 / 23.3
+//   16 x 4096 x 4096     7.0 / 8.3 / -       64 x 4096 x 4096    19.5 / 11.1 / 22.7   512 x 4096 x 4096   - / 22.7 / 23.4
+//   32 x 4096 x 4096     10.8 / 9.7 / 22.2   128 x 4096 x 4096   - / 15.5 / 23.4      1024 x 4096 x 4096  - / 41.5 / 22.9
+//   4 x 16384 x 4096     20.5 / 17.5 / -     128 x 4096 x 1024   - / 9.2 / 19.9       1024 x 512 x 4096   - / 15.8 / 7.4
+//   4 x 4096 x 32768     32.1 / 31.4 / -     300 x 1024 x 4096   - / 11.5 / 9.3
+// A launch and a block's way through its prologue, a stage of 128 k, a tile's end, the join of a shared K.
+constexpr double kSmallBase = 2.2, kSmallPer4096[3] = {2.2, 2.7, 4.7};   // (8, 16, 32 rows)
+constexpr double kThinBase = 4.6, kThinStage[4] = {0.31, 0.37, 0.44, 0.54}, kThinJoin = 1.0, kThinJoinRow = 0.04;   // (16 .. 128 rows)
+constexpr double kWideBase = 4.6, kWideStage = 0.486, kWideEnd = 2.2;
+constexpr double kBytesPerUs = 6.5e6;   // of weights read once
+
+struct Plan {
+    enum { small, thin, wide } kernel = wide;
+    int nt = 0, ksplit = 1;
+    double us = 1e30;
+};
+
+// Clusters of ks blocks, one block per SM, that fit at the same time (GPCs of 18 or 20 SMs).
+int64_t clusters(int ks, int sms) { return ks == 1 ? sms : sms / (ks == 2 ? 2 : ks == 4 ? 5 : 10); }
+
+void consider(Plan& best, int kernel, int nt, int ksplit, double us) {
+    if (us >= best.us) return;
+    best.kernel = static_cast<decltype(best.kernel)>(kernel);
+    best.nt = nt;
+    best.ksplit = ksplit;
+    best.us = us;
+}
+
+Plan plan_one_weight(const LinearF8Params& p, int sms) {
+    Plan best;
+    const int64_t blocks = p.K / kScaleBlock;
+    const double bytes = 3.0 + static_cast<double>(p.K) * p.N / kBytesPerUs;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t groups = ceil_div(p.T, 8 << i);
+        if (groups > 65535) continue;   // a grid's limit
+        const double per_sm = std::max(1.0, static_cast<double>(groups * ceil_div(p.N, 16)) / sms);
+        consider(best, Plan::small, 1 << i, 1, kSmallBase + per_sm * kSmallPer4096[i] * p.K / 4096.0);
+    }
+    for (int i = 0; i < 4; ++i) {
+        const int nt = 16 << i;
+        const int64_t tiles = ceil_div(p.T, nt) * ceil_div(p.N, 128);
+        for (int ks = 1; ks <= 8 && ks <= blocks; ks *= 2) {
+            const int64_t waves = ceil_div(tiles, clusters(ks, sms));
+            if (ks > 1 && waves > 1) break;   // a cluster has one tile
+            const double us = kThinBase + waves * ceil_div(blocks, ks) * kThinStage[i] + (ks > 1 ? kThinJoin + nt * kThinJoinRow : 0.0);
+            consider(best, Plan::thin, nt, ks, std::max(us, bytes));
+        }
+    }
+    const int64_t waves = ceil_div(ceil_div(p.T, 128) * ceil_div(p.N, 256), sms);
+    consider(best, Plan::wide, 0, 1, std::max(kWideBase + waves * (blocks * kWideStage + kWideEnd), bytes));
+    return best;
+}
+
+// With a weight per expert the rows of each are known on the device only; the mean decides.  Measured (us, 256 experts of
+// 4096 x 4096, rows at random; thin with 16, 32, 64 rows per tile / wide; the weights alone take 632):
+//   mean 2   517 527 605 / 583      mean 16  872 626 712 / 788      mean 64   2690 1524 1045 / 806
+//   mean 8   611 620 713 / 734      mean 32  1481 905 710 / 810     mean 128  5057 2752 1735 / 1041
+// (with skewed popularity, mean 16: 981 775 775 / 734, mean 64: 2658 1550 1161 / 904)
+Plan plan_experts(const LinearF8Params& p, int sms) {
+    Plan best;
+    const double mean = static_cast<double>(p.T) / p.E;
+    if (mean > 40.0) return best;
+    best.kernel = Plan::thin;
+    best.nt = mean <= 8.0 ? 16 : mean <= 20.0 ? 32 : 64;
+    // few tiles whatever the offsets are: a cluster for each
+    const int64_t most = (ceil_div(p.T, best.nt) + std::min(p.E, p.T) - 1) * ceil_div(p.N, 128);
+    while (best.ksplit < 8 && p.K / kScaleBlock >= 4 * best.ksplit && most <= clusters(2 * best.ksplit, sms)) best.ksplit *= 2;
+    return best;
+}
+
+}  // namespace
+
 int f8_code_map(CUtensorMap* map, const uint8_t* q, int64_t matrices, int64_t rows, int64_t K, int box_rows) {
     const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows), static_cast<uint64_t>(matrices)};
     const uint64_t strides[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(K) * static_cast<uint64_t>(rows)};
@@ -14,16 +93,13 @@ int f8_code_map(CUtensorMap* map, const uint8_t* q, int64_t matrices, int64_t ro
     return encode_tma_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-int run_linear_f8(LinearF8Params p, cudaStream_t s) {
+int run_linear_f8(const LinearF8Params& p, cudaStream_t s) {
     int sms = 0, max_smem = 0;
     if (int rc = device_limits(sms, max_smem)) return rc;
-    const int mean = p.offsets ? (p.T + p.E - 1) / p.E : p.T;
-    int nt = 16;
-    while (nt < 128 && nt < mean) nt *= 2;
-    const int64_t items = ((static_cast<int64_t>(p.T) + nt - 1) / nt + (p.offsets ? std::min(p.E, p.T) - 1 : 0)) * ((p.N + 127) / 128);
-    int ksplit = 1;
-    while (ksplit < 8 && items * ksplit * 2 <= sms && p.K / kScaleBlock >= ksplit * 4) ksplit *= 2;
-    return launch_linear_f8_thin(p, nt, ksplit, s);
+    const Plan L = p.offsets ? plan_experts(p, sms) : plan_one_weight(p, sms);
+    if (L.kernel == Plan::small) return launch_linear_f8_small(p, L.nt, s);
+    if (L.kernel == Plan::thin) return launch_linear_f8_thin(p, L.nt, L.ksplit, s);
+    return launch_linear_f8_wide(p, s);
 }
 
 }  // namespace wna16

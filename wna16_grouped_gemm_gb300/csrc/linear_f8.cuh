@@ -19,10 +19,13 @@ struct LinearF8Launch {
     int n_blocks = 0;   // rows of scales per weight
     int ksplit = 1;     // blocks of a cluster that share a tile's K
     int stages = 0;     // operand buffers
+    int wide = 0;       // rows of results are stored 16 bytes at a time
 };
 
-// kernels' launches (linear_f8_thin.cu, linear_f8_wide.cu); return a wna16_status
+// kernels' launches (linear_f8_small.cu, linear_f8_thin.cu, linear_f8_wide.cu); return a wna16_status
+int launch_linear_f8_small(const LinearF8Params& p, int nt, cudaStream_t stream);
 int launch_linear_f8_thin(const LinearF8Params& p, int nt, int ksplit, cudaStream_t stream);
+int launch_linear_f8_wide(const LinearF8Params& p, cudaStream_t stream);
 // Codes [matrices][rows][K] as boxes of `box_rows` rows x 128 k (zeros past the end)
 int f8_code_map(CUtensorMap* map, const uint8_t* q, int64_t matrices, int64_t rows, int64_t K, int box_rows);
 
@@ -69,6 +72,10 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+// acc += v * s on a value of a tensor memory load: volatile, so that it stays behind the wait for it.
+__device__ __forceinline__ void fma_loaded(float& acc, uint32_t v, float s) {
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(s));
+}
 __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
     F2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -90,6 +97,24 @@ struct RingSlot {
 // Wait of a whole warp: true only if every lane saw the phase complete.
 __device__ __forceinline__ bool warp_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
     return __all_sync(0xffffffffu, mbar_wait_at(smem_u32(bar), parity, abort, status));
+}
+
+// The same without a call: a function's registers do not go with setmaxnreg.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t began = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity)) {
+        if (*abort) return false;
+        if (globaltimer_ns() - began > kWaitLimitNs) {
+            *abort = 1;
+            atomicExch(status, kStatusTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool warp_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+    return __all_sync(0xffffffffu, wait_inline(smem_u32(bar), parity, abort, status));
 }
 
 // The list of tiles: rows[e] is the first row of expert e (rows[E] the end), tiles[e] the number

@@ -22,6 +22,7 @@ constexpr int kM = 128;
 constexpr int kProducer = 0, kIssuer = 1, kScaler = 2, kLister = 3, kFirstEpilogue = 4;
 constexpr int kScaleSlots = 16;
 constexpr int kMaxStages = 12;
+constexpr int kAloneBytes = 150 * 1024;
 
 __device__ int g_status;   // of calls without a workspace
 
@@ -94,7 +95,6 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
         tmem_relinquish();
     }
     pdl_wait();
-    pdl_trigger();
     if (warp == kLister) {
         const bool bad = f8_tile_list(p, NT, rows, tiles);
         if (blockIdx.x == 0 && lane == 0) *status = bad ? kStatusBadRouting : kStatusOk;   // any timeout is seconds away
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
     __syncthreads();
     if (ksplit > 1) cluster_sync();   // the others' shared memory is theirs
     tc_fence_after();
+    pdl_trigger();                    // (this block has its TMEM: a block of the next kernel cannot take it away)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int items = tiles[p.E] * L.n_tiles;
 
@@ -302,7 +303,9 @@ int launch(LinearF8Launch L, cudaStream_t s) {
     L.stages = std::min((max_smem - fixed) / C::kStageBytes, kMaxStages);
     if (L.ksplit > 1) L.stages = std::min(L.stages, std::max(2, (L.blocks + L.ksplit - 1) / L.ksplit));   // one turn
     if (L.stages < 2) return set_error(WNA16_ERR_UNSUPPORTED, "8-bit float linear: %d bytes of shared memory", fixed + 2 * C::kStageBytes);
-    const int smem = fixed + L.stages * C::kStageBytes;
+    // Blocks that share a K wait for one another, and each for its columns of TMEM: two such clusters side
+    // by side could hold what the other waits for.  So much shared memory keeps others off their SMs.
+    const int smem = std::max(fixed + L.stages * C::kStageBytes, L.ksplit > 1 ? kAloneBytes : 0);
     CUtensorMap tm_w, tm_x;
     if (int rc = f8_code_map(&tm_w, p.wq, p.E, p.N, p.K, kM)) return rc;
     if (int rc = f8_code_map(&tm_x, p.xq, 1, p.T, p.K, NT)) return rc;
