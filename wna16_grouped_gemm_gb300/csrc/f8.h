@@ -37,10 +37,10 @@ struct UnsortParams {
     int topk = 1;
     void* out = nullptr;              // [T, K]; gradient: dy [R, K] or NULL
     float* dweights = nullptr;
-    int vec = 0;                      // 16-byte accesses are possible
+    int access = 0;                   // bytes: 16, 4, or a value's
 };
-cudaError_t launch_unsort_tokens(int type, const UnsortParams& p, cudaStream_t stream);
-cudaError_t launch_unsort_tokens_grad(int type, const UnsortParams& p, cudaStream_t stream);
+cudaError_t launch_unsort_tokens(int type, const UnsortParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_unsort_tokens_grad(int type, const UnsortParams& p, int sms, cudaStream_t stream);
 
 // Products of e4m3 rows with block-scaled e4m3 weights (linear_f8.cu).
 struct LinearF8Params {

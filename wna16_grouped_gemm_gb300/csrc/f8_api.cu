@@ -1,5 +1,7 @@
 // C ABI of the routed experts in 8-bit floats (include/wna16_moe_f8.h):
 // argument validation and dispatch.
+#include <initializer_list>
+
 #include "../../include/wna16_moe_f8.h"
 #include "block.h"
 #include "checks.h"
@@ -24,6 +26,13 @@ int check_experts(int64_t E) {
     if (E < 1) return set_error(WNA16_ERR_INVALID_ARG, "E=%lld must be > 0", (ll)E);
     if (E > 1024) return set_error(WNA16_ERR_UNSUPPORTED, "E=%lld: at most 1024", (ll)E);
     return WNA16_OK;
+}
+
+// The widest accesses that contiguous rows of K values allow: 16 or 4 bytes, or one value.
+int access_of(int64_t K, size_t es, std::initializer_list<const void*> rows) {
+    uintptr_t all = static_cast<uintptr_t>(K) * es;
+    for (const void* p : rows) all |= reinterpret_cast<uintptr_t>(p);
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : static_cast<int>(es);
 }
 
 int64_t row_blocks(int64_t N) { return (N + kScaleBlock - 1) / kScaleBlock; }
@@ -123,8 +132,10 @@ int wna16_moe_unsort_tokens(const void* y, int64_t R, const int32_t* inv, const 
     p.R = R;
     p.topk = topk;
     p.out = out;
-    p.vec = K % 8 == 0 && aligned(y, 16) && aligned(addend, 16) && aligned(out, 16);
-    return launched(launch_unsort_tokens(type, p, static_cast<cudaStream_t>(stream)), "unsort_tokens launch");
+    p.access = access_of(K, es, {y, addend, out});
+    int sms = 0, max_smem = 0;
+    if (int rc = device_limits(sms, max_smem)) return rc;
+    return launched(launch_unsort_tokens(type, p, sms, static_cast<cudaStream_t>(stream)), "unsort_tokens launch");
 }
 
 int wna16_moe_unsort_tokens_grad(const void* dout, const int32_t* inv, const void* y, const float* weights, int64_t T,
@@ -165,8 +176,10 @@ int wna16_moe_unsort_tokens_grad(const void* dout, const int32_t* inv, const voi
     p.topk = topk;
     p.out = dy;
     p.dweights = dweights;
-    p.vec = K % 8 == 0 && aligned(y, 16) && aligned(dout, 16) && aligned(dy, 16);
-    return launched(launch_unsort_tokens_grad(type, p, static_cast<cudaStream_t>(stream)), "unsort_tokens_grad launch");
+    p.access = access_of(K, es, {y, dout, dy});
+    int sms = 0, max_smem = 0;
+    if (int rc = device_limits(sms, max_smem)) return rc;
+    return launched(launch_unsort_tokens_grad(type, p, sms, static_cast<cudaStream_t>(stream)), "unsort_tokens_grad launch");
 }
 
 static int linear_f8(const void* xq, const float* x_scales, const void* wq, const float* w_scales, const float* bias,

@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "f8.h"
@@ -25,11 +26,33 @@ constexpr unsigned kAll = 0xffffffffu;
 
 constexpr int kSmallThreads = 256;
 // Slots up to which every token counts its own positions, in one launch.
-constexpr int kSmallSlots = 4096;
+constexpr int kSmallSlots = 6144;
+
+// The sums over a warp of 8 values per lane: lane l has that of value l / 4 (halves of the values go to halves of the
+// lanes, then the lanes of each are added).
+template <typename N>
+__device__ __forceinline__ N warp_sums(const N (&v)[8], int lane) {
+    N a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        a[i] = (up ? v[4 + i] : v[i]) + __shfl_xor_sync(kAll, up ? v[i] : v[4 + i], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        b[i] = (up ? a[2 + i] : a[i]) + __shfl_xor_sync(kAll, up ? a[i] : a[2 + i], 8);
+    }
+    const bool up = lane & 4;
+    N c = (up ? b[1] : b[0]) + __shfl_xor_sync(kAll, up ? b[0] : b[1], 4);
+    c += __shfl_xor_sync(kAll, c, 2);
+    c += __shfl_xor_sync(kAll, c, 1);
+    return c;
+}
 
 // One block per token, and one for the offsets.  A slot's row is the number of slots
-// that sort before it; a warp counts them.  Experts are unsigned offsets from
-// expert_begin, so ids below it are large numbers.
+// that sort before it; the block's threads count them, for up to 8 slots at a time.  Experts are unsigned
+// offsets from expert_begin, so ids below it are large numbers.
 template <typename V>
 __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortParams p) {
     __shared__ int pos[1024];
@@ -72,29 +95,39 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortPar
         return;
     }
     const int t = blockIdx.x;
-    for (int j = warp; j < p.topk; j += kSmallThreads / 32) {
-        const int f = t * p.topk + j;
-        const unsigned e = __ldg(ids + f) - begin;
-        int n = 0;
-        if (e < E) {
-            for (int i = lane; i < R; i += 32) {
-                const unsigned o = __ldg(ids + i) - begin;
-                n += o < e || (o == e && i < f);
-            }
-            n = __reduce_add_sync(kAll, n);
-        } else {
-            n = -1;
+    __shared__ int part[kSmallThreads / 32][8];
+    for (int j0 = 0; j0 < p.topk; j0 += 8) {
+        const int f = t * p.topk + j0;
+        unsigned e[8];
+        int n[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            e[q] = j0 + q < p.topk ? __ldg(ids + f + q) - begin : ~0u;
+            n[q] = 0;
         }
-        if (lane == 0) {
-            pos[j] = n;
-            p.inv[f] = n;
+#pragma unroll 4
+        for (int i = tid; i < R; i += kSmallThreads) {
+            const unsigned o = __ldg(ids + i) - begin;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) n[q] += o < e[q] || (o == e[q] && i < f + q);
         }
+        const int sum = warp_sums(n, lane);
+        if ((lane & 3) == 0) part[warp][lane >> 2] = sum;
+        __syncthreads();
+        if (tid < 8 && j0 + tid < p.topk) {
+            int row = 0;
+#pragma unroll
+            for (int w = 0; w < kSmallThreads / 32; ++w) row += part[w][tid];
+            if (__ldg(ids + f + tid) - begin >= E) row = -1;
+            pos[j0 + tid] = row;
+            p.inv[f + tid] = row;
+        }
+        __syncthreads();
     }
     if (!p.x) return;
     const int64_t n_vec = p.row_bytes / static_cast<int64_t>(sizeof(V));
     const V* src = reinterpret_cast<const V*>(static_cast<const char*>(p.x) + t * p.x_pitch);
     V* dst = static_cast<V*>(p.rows);
-    __syncthreads();
     for (int64_t v = tid; v < n_vec; v += kSmallThreads) {
         const V a = src[v];
         for (int j = 0; j < p.topk; ++j)
@@ -110,7 +143,8 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortPar
 
 constexpr int kListThreads = 1024;
 constexpr int kListWarps = kListThreads / 32;
-constexpr int kListBlocks = 8;   // one cluster
+constexpr int kListBlocks = 16;  // one cluster
+constexpr int kKeep = 8;         // slots of a lane at a time
 
 // The lists of many slots, by one cluster: a stable counting sort.  Every warp has a run
 // of slots and counts its experts; the blocks exchange their counts through distributed
@@ -131,16 +165,36 @@ __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortP
     const int64_t R = p.T * p.topk;
     const int64_t per_warp = (R + kListBlocks * kListWarps * 32 - 1) / (kListBlocks * kListWarps * 32) * 32;
     const int64_t f0 = (rank * kListWarps + warp) * per_warp, f1 = min(R, f0 + per_warp);
+    const bool kept = per_warp <= 32 * kKeep;   // the experts and ranks of all of a lane's slots stay in registers
     int* my = hist + warp * E;
     for (int e = lane; e < E; e += 32) my[e] = 0;
     __syncwarp();
-    for (int64_t at = f0; at < f1; at += 32) {
-        const int64_t f = at + lane;
-        unsigned e = f < f1 ? __ldg(ids + f) - begin : ~0u;
-        if (e >= static_cast<unsigned>(E)) e = ~0u;
-        const unsigned peers = __match_any_sync(kAll, e);
-        if (e != ~0u && lane == __ffs(peers) - 1) my[e] += __popc(peers);
-        __syncwarp();
+    const unsigned lower = (1u << lane) - 1u;
+    unsigned e[kKeep];
+    int at_rank[kKeep];
+    auto load = [&](int64_t at) {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int64_t f = at + i * 32 + lane;
+            e[i] = f < f1 ? __ldg(ids + f) - begin : ~0u;
+        }
+    };
+    // every slot's rank among its expert's, and the counts of the warp
+    auto count = [&] {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            if (e[i] >= static_cast<unsigned>(E)) e[i] = ~0u;
+            const unsigned peers = __match_any_sync(kAll, e[i]);
+            const int before = e[i] != ~0u ? my[e[i]] : 0;
+            at_rank[i] = before + __popc(peers & lower);
+            __syncwarp();
+            if (e[i] != ~0u && lane == __ffs(peers) - 1) my[e[i]] = before + __popc(peers);
+            __syncwarp();
+        }
+    };
+    for (int64_t at = f0; at < f1; at += 32 * kKeep) {
+        load(at);
+        count();
     }
     __syncthreads();
     if (tid < E) {
@@ -184,17 +238,23 @@ __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortP
         }
     }
     __syncthreads();
-    const unsigned lower = (1u << lane) - 1u;
-    for (int64_t at = f0; at < f1; at += 32) {
-        const int64_t f = at + lane;
-        unsigned e = f < f1 ? __ldg(ids + f) - begin : ~0u;
-        if (e >= static_cast<unsigned>(E)) e = ~0u;
-        const unsigned peers = __match_any_sync(kAll, e);
-        const int pos = e != ~0u ? base[e] + my[e] + __popc(peers & lower) : -1;
-        __syncwarp();
-        if (e != ~0u && lane == __ffs(peers) - 1) my[e] += __popc(peers);
-        __syncwarp();
-        if (f < f1) p.inv[f] = pos;
+    // now hist holds the slots of the expert in the block's lower warps, and base its first row of the block
+    if (kept) {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int64_t f = f0 + i * 32 + lane;
+            if (f < f1) p.inv[f] = e[i] != ~0u ? base[e[i]] + my[e[i]] + at_rank[i] : -1;
+        }
+        return;
+    }
+    for (int64_t at = f0; at < f1; at += 32 * kKeep) {
+        load(at);
+        count();
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int64_t f = at + i * 32 + lane;
+            if (f < f1) p.inv[f] = e[i] != ~0u ? base[e[i]] + at_rank[i] : -1;
+        }
     }
 }
 
@@ -247,6 +307,8 @@ cudaError_t launch_sort(const SortParams& p, cudaStream_t s) {
     const int smem = (kListWarps + kListBlocks + 1) * p.E * 4;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(sort_lists_kernel), smem);
     if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(sort_lists_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kListBlocks);
     cfg.blockDim = dim3(kListThreads);
@@ -269,180 +331,265 @@ cudaError_t launch_sort(const SortParams& p, cudaStream_t s) {
 
 // ------------------------------------------------------------------ back
 
-constexpr int kV = 8;   // values per chunk
 constexpr int kBackThreads = 256;
 constexpr int kBatch = 8;   // rows read at the same time
+constexpr int kBackBlocks = 3, kGradBlocks = 2;   // per SM
+constexpr int kRunThreads = 128; // of a run of unsort
 
+// The values of a thread, 16 bytes of them: neighbours where rows are read 16 bytes at a time, else every 32nd access
+// of a warp's (of W = 4 or 2 bytes), so that its lanes read neighbours.
 template <typename T>
-__device__ __forceinline__ float to_f(T v) {
-    if constexpr (sizeof(T) == 4)
-        return v;
-    else if constexpr (std::is_same<T, __half>::value)
-        return __half2float(v);
-    else
-        return __bfloat162float(v);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float v) {
-    if constexpr (sizeof(T) == 4)
-        return v;
-    else if constexpr (std::is_same<T, __half>::value)
-        return __float2half_rn(v);
-    else
-        return __float2bfloat16_rn(v);
-}
-
-template <typename T>
-struct alignas(16) Chunk {
-    T v[kV];
+constexpr int kV = 16 / static_cast<int>(sizeof(T));
+constexpr int kWords = 4;
+struct Chunk {
+    uint32_t w[kWords];
 };
+// the place of a thread's first value in a run
+template <typename T, int W>
+__device__ __forceinline__ int chunk_start() {
+    constexpr int kOne = W / static_cast<int>(sizeof(T));   // values per access
+    return W == 16 ? static_cast<int>(threadIdx.x) * kV<T>
+                   : static_cast<int>(threadIdx.x / 32) * 32 * kV<T> + static_cast<int>(threadIdx.x & 31) * kOne;
+}
 
-// 8 values at p (n of them exist, the others are 0)
-template <typename T, bool VEC>
-__device__ __forceinline__ Chunk<T> load_chunk(const T* p, int64_t n) {
-    Chunk<T> c;
-    if (VEC) {
+// the chunk at p (of n values from there on; those past them are 0)
+template <typename T, int W>
+__device__ __forceinline__ Chunk load_chunk(const T* p, int64_t n) {
+    Chunk c;
+    if constexpr (W == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        c.w[0] = v.x;
+        c.w[1] = v.y;
+        c.w[2] = v.z;
+        c.w[3] = v.w;
+    } else if constexpr (W == 4) {   // (rows are of whole accesses)
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(c) / 16); ++i)
-            reinterpret_cast<uint4*>(c.v)[i] = reinterpret_cast<const uint4*>(p)[i];
+        for (int i = 0; i < 4; ++i)
+            c.w[i] = 32 * i * (4 / static_cast<int>(sizeof(T))) < n ? reinterpret_cast<const uint32_t*>(p)[32 * i] : 0u;
     } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) c.v[i] = i < n ? p[i] : from_f<T>(0.0f);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = 64 * i < n ? h[64 * i] : 0u, hi = 64 * i + 32 < n ? h[64 * i + 32] : 0u;
+            c.w[i] = lo | hi << 16;
+        }
     }
     return c;
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_chunk(T* p, int64_t n, const Chunk<T>& c) {
-    if (VEC) {
+template <typename T, int W>
+__device__ __forceinline__ void store_chunk(T* p, int64_t n, const Chunk& c) {
+    if constexpr (W == 16) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+    } else if constexpr (W == 4) {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(c) / 16); ++i)
-            reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(c.v)[i];
+        for (int i = 0; i < 4; ++i)
+            if (32 * i * (4 / static_cast<int>(sizeof(T))) < n) reinterpret_cast<uint32_t*>(p)[32 * i] = c.w[i];
     } else {
+        uint16_t* h = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-            if (i < n) p[i] = c.v[i];
+        for (int i = 0; i < 8; ++i)
+            if (32 * i < n) h[32 * i] = static_cast<uint16_t>(c.w[i / 2] >> (i % 2 * 16));
     }
 }
+template <typename T>
+__device__ __forceinline__ void to_floats(const Chunk& c, float (&v)[kV<T>]) {
+#pragma unroll
+    for (int i = 0; i < kV<T>; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            v[i] = __uint_as_float(c.w[i]);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            if (i % 2 == 0) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c.w[i / 2]));
+                v[i] = f.x;
+                v[i + 1] = f.y;
+            }
+        } else {
+            v[i] = __uint_as_float(i % 2 ? c.w[i / 2] & 0xffff0000u : c.w[i / 2] << 16);
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ Chunk from_floats(const float (&v)[kV<T>]) {
+    Chunk c;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            c.w[i] = __float_as_uint(v[i]);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            c.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            c.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    return c;
+}
 
-// A block per token and run of 2048 values; a thread has 8 of them.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kBackThreads) unsort_kernel(const UnsortParams p) {
+// The rows and weights of up to 32 slots of a token from slot j0 on, one per lane; -1: left out.
+struct Slots {
+    int row = -1;
+    float w = 1.0f;
+};
+__device__ __forceinline__ Slots load_slots(const UnsortParams& p, int64_t t, int j0, int lane) {
+    Slots s;
+    if (t < p.T && j0 + lane < p.topk) {
+        const int64_t f = t * p.topk + j0 + lane;
+        const int r = __ldg(p.inv + f);
+        s.row = r >= 0 && r < p.R ? r : -1;
+        if (p.weights) s.w = __ldg(p.weights + f);
+    }
+    return s;
+}
+
+// A block takes runs of 2 KB of one token, item after item, and has the next one's slots
+// loaded while it works on one; a thread has 16 bytes of a run.
+template <typename T, int W>
+__global__ void __launch_bounds__(kBackThreads, kBackBlocks) unsort_kernel(const UnsortParams p, int runs, int64_t items) {
     pdl_wait();
     pdl_trigger();
-    const int64_t t = blockIdx.x;
-    const int64_t k = (static_cast<int64_t>(blockIdx.y) * kBackThreads + threadIdx.x) * kV;
-    if (k >= p.K) return;
-    const int64_t n = p.K - k;
+    const int lane = threadIdx.x & 31;
+    const int start = chunk_start<T, W>(), width = static_cast<int>(blockDim.x) * kV<T>;   // values of a run
     const T* y = static_cast<const T*>(p.y);
-    float sum[kV] = {};
-    for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
-        Chunk<T> c[kBatch];
-        float w[kBatch];
-        bool used[kBatch];
+    int64_t t = blockIdx.x / runs;
+    int run = static_cast<int>(blockIdx.x - t * runs);
+    const int64_t step_t = gridDim.x / runs;
+    const int step_run = static_cast<int>(gridDim.x - step_t * runs);
+    Slots next = load_slots(p, t, 0, lane);
+    for (int64_t v = blockIdx.x; v < items; v += gridDim.x) {
+        const int64_t now = t, k = static_cast<int64_t>(run) * width + start, n = p.K - k;
+        Slots s = next;
+        t += step_t;
+        run += step_run;
+        if (run >= runs) {
+            run -= runs;
+            ++t;
+        }
+        next = load_slots(p, t, 0, lane);
+        float sum[kV<T>] = {};
+        for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+            if (j0 > 0 && j0 % 32 == 0) s = load_slots(p, now, j0, lane);
+            Chunk c[kBatch];
+            int row[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int64_t f = t * p.topk + j0 + i;
-            const int64_t r = j0 + i < p.topk ? __ldg(p.inv + f) : -1;
-            used[i] = r >= 0 && r < p.R;
-            if (used[i]) {
-                w[i] = p.weights ? __ldg(p.weights + f) : 1.0f;
-                c[i] = load_chunk<T, VEC>(y + r * p.K + k, n);
+            for (int i = 0; i < kBatch; ++i) {
+                row[i] = __shfl_sync(kAll, s.row, (j0 + i) & 31);
+                if (row[i] >= 0 && n > 0) c[i] = load_chunk<T, W>(y + row[i] * p.K + k, n);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float w = __shfl_sync(kAll, s.w, (j0 + i) & 31);
+                if (row[i] >= 0) {
+                    float f[kV<T>];
+                    to_floats<T>(c[i], f);
+#pragma unroll
+                    for (int e = 0; e < kV<T>; ++e) sum[e] = fmaf(w, f[e], sum[e]);
+                }
             }
         }
+        if (n <= 0) continue;
+        if (p.addend) {
+            float a[kV<T>];
+            to_floats<T>(load_chunk<T, W>(static_cast<const T*>(p.addend) + now * p.K + k, n), a);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (used[i]) {
-#pragma unroll
-                for (int v = 0; v < kV; ++v) sum[v] = fmaf(w[i], to_f(c[i].v[v]), sum[v]);
-            }
+            for (int e = 0; e < kV<T>; ++e) sum[e] += a[e];
+        }
+        store_chunk<T, W>(static_cast<T*>(p.out) + now * p.K + k, n, from_floats<T>(sum));
     }
-    if (p.addend) {
-        const Chunk<T> a = load_chunk<T, VEC>(static_cast<const T*>(p.addend) + t * p.K + k, n);
-#pragma unroll
-        for (int v = 0; v < kV; ++v) sum[v] += to_f(a.v[v]);
-    }
-    Chunk<T> o;
-#pragma unroll
-    for (int v = 0; v < kV; ++v) o.v[v] = from_f<T>(sum[v]);
-    store_chunk<T, VEC>(static_cast<T*>(p.out) + t * p.K + k, n, o);
 }
 
-// A block per token: a thread has its chunks of dout and, for up to 8 slots at a time,
+// A block takes token after token: a thread has its chunks of dout and, for up to 8 slots at a time,
 // the same chunks of their rows of y.  The dot products are summed over a thread's chunks, the
 // lanes and the warps, in that order.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kBackThreads) unsort_grad_kernel(const UnsortParams p) {
-    __shared__ float part[kBackThreads / 32][kBatch];
+template <typename T, int W>
+__global__ void __launch_bounds__(kBackThreads, kGradBlocks) unsort_grad_kernel(const UnsortParams p) {
+    __shared__ float part[2][kBackThreads / 32][kBatch];
     pdl_wait();
     pdl_trigger();
-    const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int start = chunk_start<T, W>(), width = static_cast<int>(blockDim.x) * kV<T>;   // values of a run
     const T* y = static_cast<const T*>(p.y);
+    const T* dout = static_cast<const T*>(p.dout);
     T* dy = static_cast<T*>(p.out);
-    for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
-        int64_t row[kBatch];
-        float w[kBatch], dot[kBatch];
+    int turn = 0;
+    Slots next = load_slots(p, blockIdx.x, 0, lane);
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        Slots s = next;
+        next = load_slots(p, t + gridDim.x, 0, lane);
+        for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+            if (j0 > 0 && j0 % 32 == 0) s = load_slots(p, t, j0, lane);
+            float dot[kBatch] = {};
+            for (int64_t k0 = 0; k0 < p.K; k0 += width) {   // the same turns for every thread
+                const int64_t k = k0 + start, n = p.K - k;
+                Chunk g, c[kBatch];
+                int row[kBatch];
+                if (n > 0) g = load_chunk<T, W>(dout + t * p.K + k, n);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int64_t f = t * p.topk + j0 + i;
-            const int64_t r = j0 + i < p.topk ? __ldg(p.inv + f) : -1;
-            row[i] = r < p.R ? r : -1;
-            w[i] = row[i] >= 0 && p.weights ? __ldg(p.weights + f) : 1.0f;
-            dot[i] = 0.0f;
-        }
-        for (int64_t k = threadIdx.x * kV; k < p.K; k += kBackThreads * kV) {
-            const int64_t n = p.K - k;
-            const Chunk<T> d = load_chunk<T, VEC>(static_cast<const T*>(p.dout) + t * p.K + k, n);
-            if (p.dweights) {
-                Chunk<T> c[kBatch];
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = __shfl_sync(kAll, s.row, (j0 + i) & 31);
+                    row[i] = n > 0 ? r : -1;
+                    if (p.dweights && row[i] >= 0) c[i] = load_chunk<T, W>(y + row[i] * p.K + k, n);
+                }
+                float d[kV<T>];
+                to_floats<T>(g, d);
+                if (p.dweights) {
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (row[i] >= 0) c[i] = load_chunk<T, VEC>(y + row[i] * p.K + k, n);
+                    for (int i = 0; i < kBatch; ++i)
+                        if (row[i] >= 0) {
+                            float f[kV<T>];
+                            to_floats<T>(c[i], f);
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (row[i] >= 0) {
+                            for (int e = 0; e < kV<T>; ++e) dot[i] = fmaf(d[e], f[e], dot[i]);
+                        }
+                }
+                if (dy) {
 #pragma unroll
-                        for (int v = 0; v < kV; ++v) dot[i] = fmaf(to_f(d.v[v]), to_f(c[i].v[v]), dot[i]);
+                    for (int i = 0; i < kBatch; ++i) {
+                        const float w = __shfl_sync(kAll, s.w, (j0 + i) & 31);
+                        if (row[i] >= 0) {
+                            float o[kV<T>];
+#pragma unroll
+                            for (int e = 0; e < kV<T>; ++e) o[e] = w * d[e];
+                            store_chunk<T, W>(dy + row[i] * p.K + k, n, from_floats<T>(o));
+                        }
                     }
+                }
             }
-            if (dy) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (row[i] >= 0) {
-                        Chunk<T> o;
-#pragma unroll
-                        for (int v = 0; v < kV; ++v) o.v[v] = from_f<T>(w[i] * to_f(d.v[v]));
-                        store_chunk<T, VEC>(dy + row[i] * p.K + k, n, o);
-                    }
+            if (!p.dweights) continue;
+            const float sum = warp_sums(dot, lane);
+            if ((lane & 3) == 0) part[turn][warp][lane >> 2] = sum;
+            __syncthreads();   // (and the other half of `part` has been read)
+            if (threadIdx.x < kBatch && j0 + static_cast<int>(threadIdx.x) < p.topk) {
+                float total = 0.0f;
+                for (int i = 0; i < static_cast<int>(blockDim.x / 32); ++i) total += part[turn][i][threadIdx.x];
+                p.dweights[t * p.topk + j0 + threadIdx.x] = total;
             }
+            turn ^= 1;
         }
-        if (!p.dweights) continue;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) dot[i] += __shfl_xor_sync(kAll, dot[i], d);
-            if (lane == 0) part[warp][i] = dot[i];
-        }
-        __syncthreads();
-        if (threadIdx.x < kBatch && j0 + static_cast<int>(threadIdx.x) < p.topk) {
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kBackThreads / 32; ++i) s += part[i][threadIdx.x];
-            p.dweights[t * p.topk + j0 + threadIdx.x] = s;
-        }
-        __syncthreads();
     }
 }
 
+// Threads of a block: those that a row needs, `most` at most.
 template <typename T>
-cudaError_t launch_back(const UnsortParams& p, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>((p.K + kBackThreads * kV - 1) / (kBackThreads * kV)));
-    return launch_pdl(p.vec ? unsort_kernel<T, true> : unsort_kernel<T, false>, grid, dim3(kBackThreads), 0, s, p);
+int back_threads(int64_t K, int most) {
+    return static_cast<int>(std::min<int64_t>(most, (K + 32 * kV<T> - 1) / (32 * kV<T>) * 32));
+}
+
+template <typename T>
+cudaError_t launch_back(const UnsortParams& p, int sms, cudaStream_t s) {
+    const int threads = back_threads<T>(p.K, kRunThreads), width = threads * kV<T>;
+    const int runs = static_cast<int>((p.K + width - 1) / width);
+    const int64_t items = p.T * runs;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, static_cast<int64_t>(sms) * kBackBlocks * kBackThreads / threads)));
+    const auto kernel = p.access == 16 ? unsort_kernel<T, 16> : p.access == 4 ? unsort_kernel<T, 4> : unsort_kernel<T, sizeof(T)>;
+    return launch_pdl(kernel, grid, dim3(threads), 0, s, p, runs, items);
 }
 template <typename T>
-cudaError_t launch_back_grad(const UnsortParams& p, cudaStream_t s) {
-    return launch_pdl(p.vec ? unsort_grad_kernel<T, true> : unsort_grad_kernel<T, false>, dim3(static_cast<unsigned>(p.T)),
-                      dim3(kBackThreads), 0, s, p);
+cudaError_t launch_back_grad(const UnsortParams& p, int sms, cudaStream_t s) {
+    const int threads = back_threads<T>(p.K, kBackThreads);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.T, static_cast<int64_t>(sms) * kGradBlocks * kBackThreads / threads)));
+    const auto kernel = p.access == 16 ? unsort_grad_kernel<T, 16> : p.access == 4 ? unsort_grad_kernel<T, 4> : unsort_grad_kernel<T, sizeof(T)>;
+    return launch_pdl(kernel, grid, dim3(threads), 0, s, p);
 }
 
 }  // namespace
@@ -452,21 +599,22 @@ cudaError_t launch_sort_tokens(const SortParams& p, cudaStream_t s) {
     const uint64_t all = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.rows) |
                          (p.T > 1 ? static_cast<uint64_t>(p.x_pitch) : 0) | static_cast<uint64_t>(p.row_bytes);
     if (all % 16 == 0) return launch_sort<uint4>(p, s);
+    if (all % 8 == 0) return launch_sort<uint2>(p, s);
     if (all % 4 == 0) return launch_sort<uint32_t>(p, s);
     if (all % 2 == 0) return launch_sort<uint16_t>(p, s);
     return launch_sort<uint8_t>(p, s);
 }
 
-cudaError_t launch_unsort_tokens(int type, const UnsortParams& p, cudaStream_t s) {
-    if (type == kBf16) return launch_back<__nv_bfloat16>(p, s);
-    if (type == kFp16) return launch_back<__half>(p, s);
-    return launch_back<float>(p, s);
+cudaError_t launch_unsort_tokens(int type, const UnsortParams& p, int sms, cudaStream_t s) {
+    if (type == kBf16) return launch_back<__nv_bfloat16>(p, sms, s);
+    if (type == kFp16) return launch_back<__half>(p, sms, s);
+    return launch_back<float>(p, sms, s);
 }
 
-cudaError_t launch_unsort_tokens_grad(int type, const UnsortParams& p, cudaStream_t s) {
-    if (type == kBf16) return launch_back_grad<__nv_bfloat16>(p, s);
-    if (type == kFp16) return launch_back_grad<__half>(p, s);
-    return launch_back_grad<float>(p, s);
+cudaError_t launch_unsort_tokens_grad(int type, const UnsortParams& p, int sms, cudaStream_t s) {
+    if (type == kBf16) return launch_back_grad<__nv_bfloat16>(p, sms, s);
+    if (type == kFp16) return launch_back_grad<__half>(p, sms, s);
+    return launch_back_grad<float>(p, sms, s);
 }
 
 }  // namespace wna16
