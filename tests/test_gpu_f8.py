@@ -92,6 +92,10 @@ SORTS = [
     (600, 7, 1024, 1024, 0, 100, HF, False, 0.2), (2047, 8, 256, 64, 64, 384, FP, True, 0.0), (5000, 1, 8, 8, 0, 17, I8, True, 0.0),
     (8192, 8, 256, 256, 0, 512, BF, True, 0.0), (300, 33, 3, 3, 0, 64, BF, False, 0.0), (3, 1024, 5, 5, 0, 32, E4, False, 0.5),
     (70, 100, 9, 9, 0, 48, HF, False, 0.0), (40000, 8, 60, 60, 0, 32, E4, False, 0.0),
+    # around the largest batch that is counted by its own blocks, and lists of every size by the cluster
+    (768, 8, 256, 256, 0, 128, BF, False, 0.0), (769, 8, 256, 256, 0, 128, BF, True, 0.3), (6145, 1, 1024, 1024, 0, 64, HF, False, 0.0),
+    (3000, 7, 1024, 512, 512, 72, FP, True, 0.1), (9363, 7, 64, 64, 0, 16, E4, True, 0.0), (20000, 5, 1024, 1024, 0, 20, BF, True, 0.0),
+    (2, 800, 6, 6, 0, 1000, BF, True, 0.0), (7000, 1, 1, 1, 0, 33, I8, False, 0.5),
 ]
 
 
@@ -196,6 +200,30 @@ def test_unsort_grad(moe, T, topk, E, K, dt, weighted, added, padding):
     assert only[0] is None and torch.equal(only[1], dw)
     only = moe.unsort_tokens_grad(d, inv, None, w, dy=torch.full_like(y, 5.0))
     assert only[1] is None and torch.equal(only[0], dy)
+
+
+def test_rows_past_32_bits(moe):
+    """Elements and bytes past 2^31 and 2^32: the rows of the last experts and tokens."""
+    T, topk, E, K = 9000, 8, 16, 32768
+    x = torch.empty(T, K, dtype=HF, device="cuda")
+    for a in range(0, T, 3000):
+        x[a:a + 3000] = randn(3000, K, seed=a, dtype=HF)
+    ids = make_ids(T, topk, E, seed=1)
+    rows, _, off, inv = moe.sort_tokens(x, ids, E)
+    order, inv_ref, off_ref = lists_ref(ids, E, 0)
+    assert np.array_equal(inv.cpu().numpy(), inv_ref) and np.array_equal(off.cpu().numpy(), off_ref)
+    for a in (0, T * topk // 2, T * topk - 500):
+        assert torch.equal(rows[a:a + 500], x[torch.from_numpy(order[a:a + 500] // topk).cuda()])
+    w = torch.rand(T, topk, device="cuda")
+    out = moe.unsort_tokens(rows, inv, w)
+    for t in (0, T // 2, T - 1):
+        ref = (x[t].double() * w[t].double().sum())
+        check(out[t], ref, half_step(HF) + 20 * U, "unsort", floor=floor_of(HF))
+    dy, dw = moe.unsort_tokens_grad(x, inv, rows, w, dy=torch.empty_like(rows))
+    for t in (0, T - 1):
+        check(dy[inv[t].long()], x[t].double() * w[t].double().unsqueeze(1), half_step(HF) + 2 * U, "dy", floor=floor_of(HF))
+        sq = (x[t].double() ** 2).sum()
+        check(dw[t], sq.expand(topk), (K / 256 + 64) * U, "dweights")
 
 
 def test_unsort_leaves_out_rows_outside(moe):
@@ -343,6 +371,20 @@ def test_linear_extreme_codes_and_scales(moe, T):
     assert bool(out[:2].isnan().all()) and bool(out[2:].isfinite().all())
 
 
+@pytest.mark.parametrize("T", [2, 40, 300])
+def test_linear_codes_that_are_nan(moe, T):
+    """A NaN code makes its row or its channel NaN, and no other."""
+    K, N = 512, 264
+    xq, xs = rows_f8(T, K, 1)
+    wq, ws = rows_f8(N, K, 2)[0], torch.full((3, K // B), 0.001, device="cuda")
+    xq.view(torch.uint8)[1, 200] = 0x7f
+    wq.view(torch.uint8)[N - 1, 500] = 0xff
+    bad = moe.linear_f8(xq, xs, wq, ws, dtype=FP).isnan()
+    want = torch.zeros_like(bad)
+    want[1], want[:, N - 1] = True, True
+    assert torch.equal(bad, want)
+
+
 @pytest.mark.parametrize("T", [3, 50, 300])
 def test_linear_is_reproducible(moe, T):
     a = check_linear(moe, T, 2048, 520, FP, seed=1)
@@ -425,6 +467,30 @@ def test_grouped_equals_linear_rows(moe):
     K, N = 1024, 300
     a = check_grouped(moe, [40, 50, 30], K, N, FP, seed=2)
     assert torch.equal(a, check_grouped(moe, [40, 50, 30], K, N, FP, seed=2))
+
+
+def test_products_past_32_bits(moe):
+    """Weights past 2^32 codes, and outputs past 2^31 elements: the last experts, rows and channels."""
+    E, N, K = 270, 4096, 4096
+    wq = torch.randint(0, 0x7f, (E, N, K), dtype=torch.uint8, device="cuda").view(E4)
+    ws = torch.full((E, N // B, K // B), 2.0 ** -12, device="cuda")
+    for counts in ([0] * (E - 3) + [2, 0, 3], [0] * (E - 2) + [60, 200]):   # weights for few rows; with a mean of few, too
+        offsets = torch.tensor([0, *np.cumsum(counts)], dtype=I32, device="cuda")
+        n = int(offsets[-1])
+        xq, xs = rows_f8(n, K, 3)
+        out = moe.grouped_linear_f8(xq, xs, wq, ws, offsets, dtype=FP)
+        for e in (E - 3, E - 2, E - 1):
+            a, b = int(offsets[e]), int(offsets[e + 1])
+            if a < b:
+                ref, S = product_ref(xq[a:b], xs[a:b], wq[e], ws[e])
+                check(out[a:b], ref, U, f"expert {e}", extra=product_tol(K, S))
+    T, N, K = 70000, 32768, 128
+    xq, xs = rows_f8(T, K, 5)
+    w, s = rows_f8(N, K, 6)[0], torch.rand(N // B, 1, device="cuda")
+    out = moe.linear_f8(xq, xs, w, s)
+    for a in (0, 65500, T - 100):
+        ref, S = product_ref(xq[a:a + 100], xs[a:a + 100], w, s)
+        check(out[a:a + 100], ref, half_step(BF) + U, "linear", extra=product_tol(K, S))
 
 
 @pytest.mark.parametrize("n", [12, 900])
@@ -562,6 +628,15 @@ def test_forward(moe, T, begin):
     check(with_add, ref + add.double(), half_step(BF) + 8 * U, "forward", extra=1.01 * tol + 4 * U * add.double().abs())
 
 
+def test_forward_without_rows(moe):
+    """No token, and tokens none of whose experts are here."""
+    xq, xs, ids, w, w13, s13, w2, s2 = f8_inputs(5, seed=1)
+    assert moe.forward_f8(xq[:0], xs[:0], ids[:0], w[:0], w13, s13, w2, s2).shape == (0, 512)
+    assert bool((moe.forward_f8(xq, xs, ids, w, w13, s13, w2, s2, expert_begin=100) == 0).all())
+    add = randn(5, 512, dtype=BF)
+    assert torch.equal(moe.forward_f8(xq, xs, ids, w, w13, s13, w2, s2, expert_begin=100, addend=add), add)
+
+
 def test_forward_expert_ranges_add_up(moe):
     """Two halves of the experts, the second with the first's output as its addend: one more rounding (2^-8 of what the first gives)."""
     xq, xs, ids, w, w13, s13, w2, s2 = f8_inputs(40, seed=3)
@@ -637,9 +712,10 @@ def test_other_stream_and_graph(moe, T):
         assert torch.equal(go, eo) and torch.equal(gr, er)
 
 
-def test_backward_in_a_graph(moe):
+@pytest.mark.parametrize("T", [300, 4000])
+def test_backward_in_a_graph(moe, T):
     """The gradients, captured and replayed, while an eager result of the same tensors lives."""
-    T, topk, E, K = 300, 4, 16, 512
+    topk, E, K = 4, 16, 512
     ids, w = make_ids(T, topk, E), torch.rand(T, topk, device="cuda")
     x, d = randn(T, K, dtype=BF), randn(T, K, seed=1, dtype=BF)
 
@@ -675,6 +751,28 @@ def test_two_streams_at_once(moe):
                 T, K, N = c
                 xq, xs = rows_f8(T, K, T)
                 got.append(moe.linear_f8(xq, xs, rows_f8(N, K, T + 10)[0], torch.exp(randn(-(-N // B), K // B, seed=T + 12)) * 0.001, dtype=FP))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_two_graphs_at_once(moe):
+    """Two captured layers, replayed at the same time on two streams, share nothing."""
+    graphs, got, want = [], [], []
+    for T in (30, 2500):
+        xq, xs, ids, w, w13, s13, w2, s2 = f8_inputs(T, seed=T)
+        want.append(moe.forward_f8(xq, xs, ids, w, w13, s13, w2, s2))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = moe.forward_f8(xq, xs, ids, w, w13, s13, w2, s2)
+        graphs.append((g, xq, xs, ids, w, w13, s13, w2, s2))
+        got.append(out)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (g, *_), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)

@@ -14,19 +14,19 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Estimated times in us, from calls timed by themselves (T x K x N with weights that are not in L2; small with 8, 16 or
 // 32 rows per block / thin with 16 to 128 rows per tile and its best split of K / wide):
-//   4 x 4096 x 4096      5.7 / 8.2 / -       77 x 2048 x 1000    5.9 / 7.4 / 11.4     200 x 4096 x 4096   - / 19.0 / 19.5
-//   16 x 4096 x 4096     7.0 / 8.3 / -       64 x 4096 x 4096    19.5 / 11.0 / 18.8   512 x 4096 x 4096   - / 22.7 / 19.7
-//   32 x 4096 x 4096     10.8 / 9.7 / 18.5   128 x 4096 x 4096   - / 15.2 / 19.3      1024 x 4096 x 4096  - / 41.5 / 19.8
-//   4 x 16384 x 4096     20.5 / 17.5 / -     128 x 4096 x 1024   10.3 / 9.2 / 18.8    1024 x 512 x 4096   - / 15.8 / 7.4
-//   4 x 4096 x 32768     32.1 / 31.4 / 70    300 x 1024 x 4096   - / 11.5 / 9.1       8192 x 4096 x 4096  - / 263 / 118
+//   4 x 4096 x 4096      4.3 / 8.2 / -       77 x 2048 x 1000    4.8 / 7.4 / 11.4     200 x 4096 x 4096   - / 19.0 / 19.5
+//   16 x 4096 x 4096     5.8 / 8.3 / -       64 x 4096 x 4096    15.5 / 11.0 / 18.8   512 x 4096 x 4096   - / 22.7 / 19.7
+//   32 x 4096 x 4096     8.7 / 9.7 / 18.5   128 x 4096 x 4096   - / 15.2 / 19.3      1024 x 4096 x 4096  - / 41.5 / 19.8
+//   4 x 16384 x 4096     15 / 17.5 / -     128 x 4096 x 1024   8.4 / 9.2 / 18.8    1024 x 512 x 4096   - / 15.8 / 7.4
+//   4 x 4096 x 32768     26.6 / 31.4 / 70    300 x 1024 x 4096   - / 11.5 / 9.1       8192 x 4096 x 4096  - / 263 / 118
 // (Wide tiles with a K shared over a cluster: 128 x 4096 x 4096 17.2 at best, 77 x 2048 x 1000 13.4; the join of 128 x 256
 // sums takes 8 us.  Few rows make wide tiles slow where many read the same ones at a time.)
 // A launch and a block's way through its prologue, a stage of 128 k, a tile's end, the join of a shared K.
-constexpr double kSmallBase = 2.2, kSmallPer4096[3] = {2.2, 2.7, 4.7};   // (8, 16, 32 rows)
+constexpr double kSmallBase = 1.5, kSmallPer4096[3] = {1.8, 2.5, 4.1};   // (8, 16, 32 rows)
 constexpr double kThinBase = 4.3, kThinEndRow = 0.018, kThinStage[4] = {0.31, 0.37, 0.44, 0.54}, kThinJoin = 1.0, kThinJoinRow = 0.04;   // (16 .. 128 rows)
 constexpr double kWideBase = 3.4, kWideStage = 0.42, kWideEnd = 2.4;
 constexpr int kWideRows = 32;   // at least
-constexpr double kBytesPerUs = 6.5e6;   // of weights read once
+constexpr double kBytesPerUs = 5.5e6;   // of weights read once by tiles
 
 struct Plan {
     enum { small, thin, wide } kernel = wide;

@@ -2,12 +2,9 @@
 //
 // Bound by latency and the weights' bytes.  A block of the grid owns 16 output channels and up to 32 rows (the weights
 // come from L2 for the second and later groups of rows); its 8 warps take the blocks of 128 k in turns, each lane
-// loading 16 consecutive bytes of two weight rows and of a row of the input straight into registers, where the codes
-// become the fp16 operands of mma.sync m16n8k16 (exact: e4m3 has 4 significant bits and exponents within fp16's; the
-// order of k inside a product is free, so both operands use the order in which the bytes lie).  A block's fp32 sums are
-// scaled and added in registers, the warps' through shared memory.
-#include <cuda_fp8.h>
-
+// loading 16 consecutive bytes of two weight rows and of a row of the input straight into registers, as operands of
+// mma.sync m16n8k32 (the order of k inside a product is free, so both operands use the order in which the bytes lie).
+// A block's fp32 sums are scaled and added in registers, the warps' through shared memory.
 #include "../../include/wna16_moe_f8.h"
 #include "gemm.h"
 #include "linear_f8.cuh"
@@ -28,25 +25,22 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// 4 codes -> 4 fp16 (exact)
-__device__ __forceinline__ uint2 fp16x4_of(uint32_t w) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-    return make_uint2(static_cast<uint32_t>(lo.x) | static_cast<uint32_t>(lo.y) << 16,
-                      static_cast<uint32_t>(hi.x) | static_cast<uint32_t>(hi.y) << 16);
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT tiles of 8 rows; U blocks of 128 k in flight per warp, at least PER_SM blocks of the grid per SM
-template <typename T, int NT, int U, int PER_SM>
-__global__ void __launch_bounds__(32 * kWarps, PER_SM) small_kernel(const LinearF8Params p) {
+// Blocks of 128 k in flight per warp, and blocks of the grid per SM.  Measured (us; 4 x 4096 x 4096 / 16 x 4096 x 4096 /
+// 32 x 4096 x 4096, then x 32768 channels):  2, 2: 4.3 5.8 8.7, 27 35 55   2, 3: 5.3 9.6 -, 27 41 -   4, 2: 4.6 - -, 28 - -
+// 4, 1: - 7.6 -, - 46 -   2, 1: - - 10.1, - - 64   1, 2: - - 9.1, - - 58.
+constexpr int kInFlight = 2, kPerSm = 2;
+
+// NT tiles of 8 rows
+template <typename T, int NT>
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) small_kernel(const LinearF8Params p) {
     __shared__ float part[kWarps][kChannels][NT * 8 + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
@@ -72,45 +66,38 @@ __global__ void __launch_bounds__(32 * kWarps, PER_SM) small_kernel(const Linear
     }
     float sum[NT][4] = {};
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int b0 = warp; b0 < blocks; b0 += kWarps * U) {   // the same turns for every lane of the warp
-        uint4 a[U][4], c[U][2];
-        float s[U];
+    for (int b0 = warp; b0 < blocks; b0 += kWarps * kInFlight) {   // the same turns for every lane of the warp
+        uint4 a[kInFlight][4], c[kInFlight][NT][2];
+        float s[kInFlight];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < kInFlight; ++u) {
             const int b = b0 + u * kWarps, k = b * kScaleBlock;
             const bool some = b < blocks;
             a[u][0] = some ? ld_stream(w0 + k) : zero;
             a[u][1] = some ? ld_stream(w1 + k) : zero;
             a[u][2] = some ? ld_stream(w0 + k + 64) : zero;
             a[u][3] = some ? ld_stream(w1 + k + 64) : zero;
-            c[u][0] = some ? __ldg(reinterpret_cast<const uint4*>(x[0] + k)) : zero;
-            c[u][1] = some ? __ldg(reinterpret_cast<const uint4*>(x[0] + k + 64)) : zero;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                c[u][j][0] = some ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : zero;
+                c[u][j][1] = some ? __ldg(reinterpret_cast<const uint4*>(x[j] + k + 64)) : zero;
+            }
             s[u] = some ? __ldg(ws + b) : 0.0f;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int b = b0 + u * kWarps, k = b * kScaleBlock;
+        for (int u = 0; u < kInFlight; ++u) {
+            const int b = b0 + u * kWarps;
             if (b >= blocks) break;
             float acc[NT][4] = {};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t aw[4] = {a[u][2 * h].x, a[u][2 * h].y, a[u][2 * h].z, a[u][2 * h].w};
                 const uint32_t bw[4] = {a[u][2 * h + 1].x, a[u][2 * h + 1].y, a[u][2 * h + 1].z, a[u][2 * h + 1].w};
-                uint2 fa[4], fb[4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    fa[m] = fp16x4_of(aw[m]);
-                    fb[m] = fp16x4_of(bw[m]);
-                }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const uint4 xc = j == 0 ? c[u][h] : __ldg(reinterpret_cast<const uint4*>(x[j] + k + 64 * h));
-                    const uint32_t xw[4] = {xc.x, xc.y, xc.z, xc.w};
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const uint2 fx = fp16x4_of(xw[m]);
-                        mma_f16(acc[j], fa[m].x, fb[m].x, fa[m].y, fb[m].y, fx.x, fx.y);
-                    }
+                    const uint32_t xw[4] = {c[u][j][h].x, c[u][j][h].y, c[u][j][h].z, c[u][j][h].w};
+                    mma_e4m3(acc[j], aw[0], bw[0], aw[1], bw[1], xw[0], xw[1]);
+                    mma_e4m3(acc[j], aw[2], bw[2], aw[3], bw[3], xw[2], xw[3]);
                 }
             }
 #pragma unroll
@@ -145,24 +132,20 @@ __global__ void __launch_bounds__(32 * kWarps, PER_SM) small_kernel(const Linear
 }
 
 template <typename T>
-cudaError_t launch(const LinearF8Params& p, int nt, int sms, cudaStream_t s) {
+cudaError_t launch(const LinearF8Params& p, int nt, cudaStream_t s) {
     const unsigned channels = static_cast<unsigned>((p.N + kChannels - 1) / kChannels);
     const unsigned groups = static_cast<unsigned>((p.T + 8 * nt - 1) / (8 * nt));
     const dim3 grid(channels, groups), block(32 * kWarps);
-    const bool turns = static_cast<int64_t>(channels) * groups > 2 * sms;
-    if (nt == 1) return launch_pdl(turns ? small_kernel<T, 1, 2, 3> : small_kernel<T, 1, 2, 2>, grid, block, 0, s, p);
-    if (nt == 2) return launch_pdl(turns ? small_kernel<T, 2, 1, 4> : small_kernel<T, 2, 2, 2>, grid, block, 0, s, p);
-    return launch_pdl(small_kernel<T, 4, 1, 2>, grid, block, 0, s, p);
+    const auto kernel = nt == 1 ? small_kernel<T, 1> : nt == 2 ? small_kernel<T, 2> : small_kernel<T, 4>;
+    return launch_pdl(kernel, grid, block, 0, s, p);
 }
 
 }  // namespace
 
 int launch_linear_f8_small(const LinearF8Params& p, int nt, cudaStream_t s) {
-    int sms = 0, max_smem = 0;
-    if (int rc = device_limits(sms, max_smem)) return rc;
-    const cudaError_t e = p.type == kBf16 ? launch<__nv_bfloat16>(p, nt, sms, s)
-                          : p.type == kFp16 ? launch<__half>(p, nt, sms, s)
-                                            : launch<float>(p, nt, sms, s);
+    const cudaError_t e = p.type == kBf16 ? launch<__nv_bfloat16>(p, nt, s)
+                          : p.type == kFp16 ? launch<__half>(p, nt, s)
+                                            : launch<float>(p, nt, s);
     return e == cudaSuccess ? WNA16_OK : set_error(WNA16_ERR_CUDA, "8-bit float linear launch: %s", cudaGetErrorString(e));
 }
 
