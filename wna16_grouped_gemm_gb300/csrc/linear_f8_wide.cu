@@ -22,6 +22,7 @@ namespace wna16 {
 namespace {
 
 constexpr int kRows = 128;           // rows of a tile (the M side)
+constexpr int kLowRows = 64;         // rows of a lower box (boxes of 32 rows, as many as a tile has: 8192 x 4096 x 4096 142 us, not 118)
 constexpr int kTile = 256;           // output channels of a tile
 constexpr int kHalf = 128;           // channels of an accumulator: those of one scale
 constexpr int kHalves = kTile / kHalf;
@@ -53,7 +54,7 @@ __device__ __forceinline__ void more_registers() {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-    wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+    wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_low, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_out, const LinearF8Launch L) {
     extern __shared__ __align__(1024) uint8_t smem[];   // (the swizzled tiles need it)
     const LinearF8Params& p = L.p;
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_low);
         tma_prefetch_desc(&tm_w);
         if (L.wide) tma_prefetch_desc(&tm_out);
     }
@@ -118,13 +120,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int v = first; v < items && ok; v += stride) {
                     tile.locate(v, L.n_tiles, kRows, rows, tiles);
+                    // a tile of few rows has a lower box (what lies in the others' place goes to sums that are not stored)
+                    const bool low = tile.r1 - tile.r0 <= kLowRows;
+                    const uint32_t bytes = ((low ? kLowRows : kRows) + kTile) * kScaleBlock;
                     for (int kb = 0; kb < blocks; ++kb, ++issued, st.next(stages)) {
                         if (!wait_inline(smem_u32(&empty[st.i]), st.phase ^ 1u, abort_flag, status)) {
                             ok = false;
                             break;
                         }
-                        mbar_arrive_expect_tx(&full[st.i], kStageBytes);
-                        tma_load_3d(sX + st.i * kRows * kScaleBlock, &tm_x, &full[st.i], kb * kScaleBlock, tile.r0, 0, pol);
+                        mbar_arrive_expect_tx(&full[st.i], bytes);
+                        tma_load_3d(sX + st.i * kRows * kScaleBlock, low ? &tm_low : &tm_x, &full[st.i], kb * kScaleBlock, tile.r0, 0, pol);
                         tma_load_3d(sW + st.i * kTile * kScaleBlock, &tm_w, &full[st.i], kb * kScaleBlock, tile.nt * kTile, tile.e, pol);
                     }
                 }
@@ -318,8 +323,9 @@ int launch(LinearF8Launch L, cudaStream_t s) {
     if (L.stages < 2) return set_error(WNA16_ERR_UNSUPPORTED, "8-bit float linear: %d bytes of shared memory", fixed + 2 * kStageBytes);
     const int smem = fixed + L.stages * kStageBytes;
     L.wide = p.N * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
-    CUtensorMap tm_x, tm_w;
+    CUtensorMap tm_x, tm_low, tm_w;
     if (int rc = f8_code_map(&tm_x, p.xq, 1, p.T, p.K, kRows)) return rc;
+    if (int rc = f8_code_map(&tm_low, p.xq, 1, p.T, p.K, kLowRows)) return rc;
     if (int rc = f8_code_map(&tm_w, p.wq, p.E, p.N, p.K, kTile)) return rc;
     CUtensorMap tm_out = {};
     if (L.wide) {
@@ -355,7 +361,7 @@ int launch(LinearF8Launch L, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_error(cudaLaunchKernelEx(&cfg, kern, tm_x, tm_w, tm_out, L), "8-bit float linear launch");
+    return cuda_error(cudaLaunchKernelEx(&cfg, kern, tm_x, tm_low, tm_w, tm_out, L), "8-bit float linear launch");
 }
 
 }  // namespace
