@@ -19,7 +19,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kV = 8;                                              // neighbouring values per load
 constexpr int kTurns = kScaleBlock * kScaleBlock / (kThreads * kV);
-constexpr int kPitch = kScaleBlock + 16;                           // of a row of codes in shared memory
 constexpr float kTiny = 7.888609052210118e-31f;                    // 2^-100
 constexpr float kQ = 448.0f;
 
@@ -35,9 +34,9 @@ __device__ __forceinline__ float to_f(T v) {
 
 // COLUMNS: w's columns are contiguous (a transposed weight), else its rows.
 template <typename T, bool COLUMNS, bool VEC>
-__global__ void __launch_bounds__(kThreads) blocks_kernel(const BlocksParams p) {
+__global__ void __launch_bounds__(kThreads, 3) blocks_kernel(const BlocksParams p) {
     __shared__ uint32_t warp_max[kThreads / 32];
-    __shared__ alignas(16) uint8_t tile[COLUMNS ? kScaleBlock * kPitch : 16];
+    __shared__ alignas(16) uint8_t tile[COLUMNS ? kScaleBlock * kScaleBlock : 16];
     pdl_wait();
     pdl_trigger();
     const int k_blocks = static_cast<int>(p.K / kScaleBlock), n_blocks = static_cast<int>((p.N + kScaleBlock - 1) / kScaleBlock);
@@ -47,16 +46,19 @@ __global__ void __launch_bounds__(kThreads) blocks_kernel(const BlocksParams p) 
     const int64_t n0 = static_cast<int64_t>(nb) * kScaleBlock, k0 = static_cast<int64_t>(kb) * kScaleBlock;
     const int rows = static_cast<int>(min(static_cast<int64_t>(kScaleBlock), p.N - n0));
     const T* w = static_cast<const T*>(p.w) + e * p.se + n0 * p.sn + k0 * p.sk;
-    // a thread's 8 values of turn i: `fast` along the contiguous axis, `slow` along the other
-    const int fast = threadIdx.x % (kScaleBlock / kV) * kV, slow0 = threadIdx.x / (kScaleBlock / kV);
-    constexpr int kStep = kThreads / (kScaleBlock / kV);
+    // a thread's 8 values of turn i: `fast` along the contiguous axis, `slow` along the other (with columns,
+    // neighbouring k in its turns: 8 x 8 values, whose codes are 8 bytes of each of 8 rows)
+    const int fast = threadIdx.x % (kScaleBlock / kV) * kV, group = threadIdx.x / (kScaleBlock / kV);
+    constexpr int kGroups = kThreads / (kScaleBlock / kV);
+    static_assert(kTurns == kV, "8 x 8");
+    auto slow_of = [&](int i) { return COLUMNS ? group * kTurns + i : group + i * kGroups; };
     struct alignas(16) Chunk {
         T v[kV];
     } c[kTurns];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
-        const int slow = slow0 + i * kStep;
+        const int slow = slow_of(i);
         const T* at = w + (COLUMNS ? slow * p.sk : slow * p.sn) + fast;
         const int count = COLUMNS ? rows - fast : (slow < rows ? kV : 0);
         if (VEC && count >= kV) {
@@ -83,40 +85,61 @@ __global__ void __launch_bounds__(kThreads) blocks_kernel(const BlocksParams p) 
     const float by = some ? kQ / m : 0.0f;
     if (threadIdx.x == 0) p.scales[b] = m < kTiny ? 0.0f : m / kQ;   // not finite where m is not
     uint8_t* q = p.q + (e * p.N + n0) * p.K + k0;
+    // the codes of turn i
+    auto codes_of = [&](int i, uint32_t (&code)[2]) {
+        code[0] = code[1] = 0;
+        if (!some) return;
 #pragma unroll
-    for (int i = 0; i < kTurns; ++i) {
-        const int slow = slow0 + i * kStep;
-        uint32_t code[2] = {0, 0};
-        if (some) {
-#pragma unroll
-            for (int j = 0; j < kV; j += 2) {
-                const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(to_f(c[i].v[j]) * by, to_f(c[i].v[j + 1]) * by),
-                                                              __NV_SATFINITE, __NV_E4M3);
-                code[j / 4] |= two << (j % 4 * 8);
-            }
+        for (int j = 0; j < kV; j += 2) {
+            const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(to_f(c[i].v[j]) * by, to_f(c[i].v[j + 1]) * by),
+                                                          __NV_SATFINITE, __NV_E4M3);
+            code[j / 4] |= two << (j % 4 * 8);
         }
-        if (COLUMNS) {
+    };
+    if constexpr (!COLUMNS) {
 #pragma unroll
-            for (int j = 0; j < kV; ++j) tile[(fast + j) * kPitch + slow] = static_cast<uint8_t>(code[j / 4] >> (j % 4 * 8));
-        } else if (slow < rows) {
+        for (int i = 0; i < kTurns; ++i) {
+            const int slow = slow_of(i);
+            uint32_t code[2];
+            codes_of(i, code);
+            if (slow >= rows) continue;
+            uint8_t* to = q + slow * p.K + fast;
             if (reinterpret_cast<uintptr_t>(p.q) % 8 == 0) {
-                *reinterpret_cast<uint2*>(q + slow * p.K + fast) = make_uint2(code[0], code[1]);
+                *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
             } else {
 #pragma unroll
-                for (int j = 0; j < kV; ++j) q[slow * p.K + fast + j] = static_cast<uint8_t>(code[j / 4] >> (j % 4 * 8));
+                for (int j = 0; j < kV; ++j) to[j] = static_cast<uint8_t>(code[j / 4] >> (j % 4 * 8));
             }
         }
-    }
-    if (COLUMNS) {
+    } else {
+        uint32_t code[kTurns][2];
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) codes_of(i, code[i]);
+        // Row n's 8 bytes of group g lie at place g ^ (n / 8) of its 16: the writes of a warp, 8 bytes to each of 16 rows
+        // of different n / 8, then meet no bank twice.
+        const int f = fast / kV;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo |= (code[i][j / 4] >> (j % 4 * 8) & 0xffu) << (i * 8);
+                hi |= (code[i + 4][j / 4] >> (j % 4 * 8) & 0xffu) << (i * 8);
+            }
+            *reinterpret_cast<uint2*>(tile + (fast + j) * kScaleBlock + (group ^ f) * 8) = make_uint2(lo, hi);
+        }
         __syncthreads();
         for (int i = threadIdx.x; i < rows * (kScaleBlock / 16); i += kThreads) {
-            const int n = i / (kScaleBlock / 16), k = i % (kScaleBlock / 16) * 16;
-            const uint4 v = *reinterpret_cast<const uint4*>(tile + n * kPitch + k);
-            uint8_t* to = q + static_cast<int64_t>(n) * p.K + k;
+            const int n = i / (kScaleBlock / 16), piece = i % (kScaleBlock / 16), r = n / kV;
+            uint4 v = *reinterpret_cast<const uint4*>(tile + n * kScaleBlock + (piece ^ (r >> 1)) * 16);
+            if (r & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+            uint8_t* to = q + static_cast<int64_t>(n) * p.K + piece * 16;
             if (reinterpret_cast<uintptr_t>(p.q) % 16 == 0) {
                 *reinterpret_cast<uint4*>(to) = v;
             } else {
-                for (int j = 0; j < 16; ++j) to[j] = tile[n * kPitch + k + j];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 16; ++j) to[j] = static_cast<uint8_t>(w[j / 4] >> (j % 4 * 8));
             }
         }
     }
