@@ -40,6 +40,7 @@ enum { WNA16_TYPE_Q8 = 3 };
  * Rows from offsets[E] on are left as they were.  x [T, K] of `type` (wna16_type or
  * WNA16_TYPE_Q8), rows ldx elements apart; x_scales fp32 [T, groups], contiguous, or
  * NULL.  x and rows NULL (then x_scales too): offsets and inv only.
+ * An empty batch gets offsets of 0.
  * 1 <= E <= 1024, 1 <= topk <= 1024, T * topk < 2^31; K up to 2^26.
  * The gradient of rows with respect to x is wna16_moe_unsort_tokens without weights.  */
 WNA16_API int wna16_moe_sort_tokens(const void* x, int64_t ldx, const float* x_scales, int64_t groups, int64_t T,
@@ -73,7 +74,8 @@ WNA16_API int wna16_moe_unsort_tokens_grad(const void* dout, const int32_t* inv,
  *   bias fp32 [N] or NULL, addend [T, N] of `type` or NULL (may be out), out [T, N] of `type`; all contiguous
  * K a multiple of 128, at most 65536; xq and wq 16-byte aligned.  A block's sum is an fp32
  * one of the tensor cores; it is multiplied by the fp32 product of its two scales and added
- * in fp32, b ascending (in up to 8 parts of consecutive blocks that are added in order).
+ * in fp32, in an order that the sizes fix (up to 8 parts of the blocks, b ascending in each, then
+ * the parts).  Another number of rows may have another order.
  * A product of two scales outside fp32's range is 0 or infinite.  Rows whose scale is not
  * finite (see wna16_moe_block.h) give NaN.
  * The gradient with respect to the rows' values is the same product of dout's 8-bit rows

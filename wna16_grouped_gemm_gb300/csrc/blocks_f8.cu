@@ -2,7 +2,9 @@
 //   m = max |w|,  scale = m / 448,  code = e4m3(w * (448 / m))
 //
 // Bound by the bytes of the weights, read once.  A thread block has one block of
-// the weight in registers from its reads to the codes.
+// the weight in registers from its reads to the codes (three of them per SM: with two, 16 x 4096 x 4096 bf16 153 us).
+// Measured (us), 16 x 4096 x 4096: fp32 184 (7.3 TB/s), transposed 190; bf16 128 (6.3), transposed 254.  1000 x 2048
+// bf16 2.6, transposed 4.2.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

