@@ -118,8 +118,13 @@ __device__ __forceinline__ bool warp_wait_inline(uint64_t* bar, uint32_t parity,
 }
 
 // The list of tiles: rows[e] is the first row of expert e (rows[E] the end), tiles[e] the number
-// of tiles of `tile` rows before it.  Written by one warp, from the offsets held to
-// [their predecessor, T]; returns whether one had to be.
+// of tiles of `tile` rows before it.  Written by one warp, from the offsets (which the block has
+// loaded into rows) held to [their predecessor, T]; returns whether one had to be.
+__device__ __forceinline__ void f8_load_offsets(const LinearF8Params& p, int* rows) {
+    if (!p.offsets) return;
+    for (int i = threadIdx.x; i <= p.E; i += blockDim.x) rows[i] = __ldg(p.offsets + i);
+    __syncthreads();
+}
 __device__ inline bool f8_tile_list(const LinearF8Params& p, int tile, int* rows, int* tiles) {
     const int lane = threadIdx.x & 31;
     if (!p.offsets) {
@@ -136,7 +141,7 @@ __device__ inline bool f8_tile_list(const LinearF8Params& p, int tile, int* rows
         const int per = (p.E + 1 + 31) / 32, i0 = lane * per, i1 = min(i0 + per, p.E + 1);
         int top = 0;
         for (int i = i0; i < i1; ++i) {
-            const int o = __ldg(p.offsets + i), c = min(max(o, 0), p.T);
+            const int o = rows[i], c = min(max(o, 0), p.T);
             bad = bad || c != o;
             rows[i] = c;
             top = max(top, c);

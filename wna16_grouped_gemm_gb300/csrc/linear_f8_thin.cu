@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
         tmem_relinquish();
     }
     pdl_wait();
+    f8_load_offsets(p, rows);
     if (warp == kLister) {
         const bool bad = f8_tile_list(p, NT, rows, tiles);
         if (blockIdx.x == 0 && lane == 0) *status = bad ? kStatusBadRouting : kStatusOk;   // any timeout is seconds away
@@ -219,6 +220,8 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
     } else if (warp >= kFirstEpilogue) {
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
         RingSlot buf, sl;
+        // A slot of scales is given back a block later: an arrival does not wait for the data of loads issued before it.
+        int held = -1;
         for (int v = first; v < items; v += stride) {
             tile.locate(v, L.n_tiles, NT, rows, tiles);
 #pragma unroll
@@ -254,8 +257,9 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&accempty[buf.i]);
-                    mbar_arrive(&sempty[sl.i]);
+                    if (held >= 0) mbar_arrive(&sempty[held]);
                 }
+                held = sl.i;
             }
             if (ksplit > 1) break;   // one tile per cluster: joined below
 #pragma unroll

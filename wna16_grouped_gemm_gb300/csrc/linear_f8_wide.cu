@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     pdl_wait();
+    f8_load_offsets(p, rows);
     if (warp == kIssuer) {
         const bool bad = f8_tile_list(p, kRows, rows, tiles);
         if (blockIdx.x == 0 && lane == 0) *status = bad ? kStatusBadRouting : kStatusOk;   // any timeout is seconds away
