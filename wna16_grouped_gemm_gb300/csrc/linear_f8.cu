@@ -14,16 +14,16 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Estimated times in us, from calls timed by themselves (T x K x N with weights that are not in L2; small with 8, 16 or
 // 32 rows per block / thin with 16 to 128 rows per tile and its best split of K / wide):
-//   4 x 4096 x 4096      4.3 / 8.2 / -       77 x 2048 x 1000    4.8 / 7.4 / 11.4     200 x 4096 x 4096   - / 19.0 / 19.5
-//   16 x 4096 x 4096     5.8 / 8.3 / -       64 x 4096 x 4096    15.5 / 11.0 / 18.8   512 x 4096 x 4096   - / 22.7 / 19.7
-//   32 x 4096 x 4096     8.7 / 9.7 / 18.5   128 x 4096 x 4096   - / 15.2 / 19.3      1024 x 4096 x 4096  - / 41.5 / 19.8
-//   4 x 16384 x 4096     15 / 17.5 / -     128 x 4096 x 1024   8.4 / 9.2 / 18.8    1024 x 512 x 4096   - / 15.8 / 7.4
-//   4 x 4096 x 32768     26.6 / 31.4 / 70    300 x 1024 x 4096   - / 11.5 / 9.1       8192 x 4096 x 4096  - / 263 / 118
+//   4 x 4096 x 4096      4.3 / 8.2 / -       77 x 2048 x 1000    4.8 / 7.4 / 10.9     200 x 4096 x 4096   - / 16.7 / 18.8
+//   16 x 4096 x 4096     5.8 / 8.2 / -       64 x 4096 x 4096    15.5 / 10.8 / 18.4   512 x 4096 x 4096   - / 22.9 / 19.2
+//   32 x 4096 x 4096     8.7 / 9.6 / 18.1   128 x 4096 x 4096   - / 14.7 / 19.2      1024 x 4096 x 4096  - / 41.5 / 19.8
+//   4 x 16384 x 4096     15 / 15.9 / -     128 x 4096 x 1024   8.4 / 9.1 / 18.0    1024 x 512 x 4096   - / 16.1 / 7.4
+//   4 x 4096 x 32768     26.6 / 29.6 / 43    300 x 1024 x 4096   - / 11.7 / 8.7       64 x 4096 x 16384   - / 18.1 / 21.2
 // (Wide tiles with a K shared over a cluster: 128 x 4096 x 4096 17.2 at best, 77 x 2048 x 1000 13.4; the join of 128 x 256
 // sums takes 8 us.  Few rows make wide tiles slow where many read the same ones at a time.)
 // A launch and a block's way through its prologue, a stage of 128 k, a tile's end, the join of a shared K.
 constexpr double kSmallBase = 1.5, kSmallPer4096[3] = {1.8, 2.5, 4.1};   // (8, 16, 32 rows)
-constexpr double kThinBase = 4.3, kThinEndRow = 0.018, kThinStage[4] = {0.31, 0.37, 0.44, 0.54}, kThinJoin = 1.0, kThinJoinRow = 0.04;   // (16 .. 128 rows)
+constexpr double kThinBase = 4.3, kThinEndRow = 0.018, kThinStage[4] = {0.26, 0.30, 0.34, 0.47}, kThinJoin = 1.0, kThinJoinRow = 0.025;   // (16 .. 128 rows)
 constexpr double kWideBase = 3.4, kWideStage = 0.42, kWideEnd = 2.4;
 constexpr int kWideRows = 32;   // at least
 constexpr double kBytesPerUs = 5.5e6;   // of weights read once by tiles
@@ -72,15 +72,15 @@ Plan plan_one_weight(const LinearF8Params& p, int sms) {
 
 // With a weight per expert the rows of each are known on the device only; the mean decides.  Measured (us, 256 experts of
 // 4096 x 4096, rows at random; thin with 16, 32, 64 rows per tile / wide; the weights alone take 632):
-//   mean 2   517 527 605 / 583      mean 16  872 626 712 / 788      mean 64   2690 1524 1045 / 806
-//   mean 8   611 620 713 / 734      mean 32  1481 905 710 / 810     mean 128  5057 2752 1735 / 1041
-// (with skewed popularity, mean 16: 981 775 775 / 734, mean 64: 2658 1550 1161 / 904)
+//   mean 2   516 517 533 / 545      mean 16  715 623 623 / 702      mean 48  1640 1178 667 / 725
+//   mean 8   607 608 613 / 650      mean 32  1179 862 654 / 696     mean 64  2095 1325 942 / 722
+// (with skewed popularity, mean 8: 643 588 580 / 577, mean 16: 851 718 673 / 660, mean 32: 1250 935 784 / 705)
 Plan plan_experts(const LinearF8Params& p, int sms) {
     Plan best;
     const double mean = static_cast<double>(p.T) / p.E;
     if (mean > 40.0) return best;
     best.kernel = Plan::thin;
-    best.nt = mean <= 8.0 ? 16 : mean <= 20.0 ? 32 : 64;
+    best.nt = mean <= 4.0 ? 16 : mean <= 12.0 ? 32 : 64;
     // few tiles whatever the offsets are: a cluster for each
     const int64_t most = (ceil_div(p.T, best.nt) + std::min(p.E, p.T) - 1) * ceil_div(p.N, 128);
     while (best.ksplit < 8 && p.K / kScaleBlock >= 4 * best.ksplit && most <= clusters(2 * best.ksplit, sms)) best.ksplit *= 2;

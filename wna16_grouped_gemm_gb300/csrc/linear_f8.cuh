@@ -50,38 +50,10 @@ __device__ __forceinline__ T elem_from_f(float v) {
         return __float2bfloat16_rn(v);
 }
 
-// Two floats in a register pair, for the packed fp32 instructions.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 f2_of(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ F2 f2_of_bits(uint32_t a, uint32_t b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ float2 f2_parts(F2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 // acc += v * s on a value of a tensor memory load: volatile, so that it stays behind the wait for it.
 __device__ __forceinline__ void fma_loaded(float& acc, uint32_t v, float s) {
     asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(s));
 }
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Position in a ring of n slots and the parity of its current phase.
 struct RingSlot {
     int i = 0;

@@ -8,10 +8,11 @@
 //   epilogue (4 or 8 warps)  thread = channel: sum += P_b * (xs * ws) in registers, then the stores
 // A block of the grid takes tile after tile; with few tiles a cluster shares a tile's K, and
 // the parts are added in order through distributed shared memory.
-// Up to 12 stages of 16 KB of weights are in flight per SM.  Measured (us): 256 experts of 4096 x 4096 with 8 rows each 611
-// (7.0 TB/s), 30 experts with a row or two 87 (5.8 TB/s; start and the last turn of tiles 10); 64 x 4096 x 4096 11.0 (K in
-// four parts), 4 x 16384 x 4096 17.5.  With many rows per tile the reads of the rows' scales from shared memory count (every
-// lane needs all of them): a stage takes 0.31 us with 16 rows, 0.54 with 128.
+// Nine stages of 16 KB of weights are in flight per SM.  The epilogue takes as many blocks at a time as fill 64 registers (half
+// as many: 8192 rows of 256 experts 698 us).  Measured (us): 256 experts of 4096 x 4096 with a row each 590 (7.3 TB/s), with 32
+// each 660, 30 experts with a row or two 85 (5.9 TB/s; start and the last turn of tiles 10); 64 x 4096 x 4096 10.7 (K in four
+// parts), 4 x 16384 x 4096 15.9.  With many rows per tile the reads of the rows' scales from shared memory count (every lane
+// needs all of them): a stage takes 0.26 us with 16 rows, 0.47 with 128.
 #include <algorithm>
 
 #include "../../include/wna16_moe_f8.h"
@@ -25,7 +26,9 @@ namespace {
 constexpr int kM = 128;
 constexpr int kProducer = 0, kIssuer = 1, kScaler = 2, kLister = 3, kFirstEpilogue = 4;
 constexpr int kScaleSlots = 16;
-constexpr int kMaxStages = 12;
+// More requests in flight make memory slower, fewer do not fill it.  us with 6, 9, 12 stages, 256 experts of 4096 x 4096:
+// 32 rows 89, 86, 86, 512 rows 556, 540, 569, 2048 rows 636, 617, 658.
+constexpr int kMaxStages = 9;
 constexpr int kAloneBytes = 150 * 1024;
 
 __device__ int g_status;   // of calls without a workspace
@@ -37,6 +40,8 @@ struct Thin {
     static constexpr int kCols = NT * 4 / kEpilogues;          // rows of the input per epilogue warp
     static constexpr int kBufs = 512 / NT < 8 ? 512 / NT : 8;  // accumulators
     static constexpr int kTmem = NT * kBufs;
+    static constexpr int kBatch = kCols < 64 ? 64 / kCols : 1; // blocks that the epilogue takes at a time
+    static_assert(kBufs >= 2 * kBatch && kBufs % kBatch == 0 && kScaleSlots >= 2 * kBatch, "one batch is on its way while another is added");
     static constexpr int kStageBytes = (kM + NT) * kScaleBlock;
     static constexpr int kScalePitch = NT + 4;                 // floats of a block's scales: the rows', the weight's
     static constexpr int kBars = 2 * kMaxStages + 2 * kBufs + 2 * kScaleSlots + 1;
@@ -160,17 +165,13 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
             }
         }
     } else if (warp == kIssuer) {
-        auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-            bool r = true;
-            if (lane == 0) r = mbar_wait(bar, parity, abort_flag, status);
-            return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
-        };
         constexpr uint32_t idesc = idesc_e4m3_f32(kM, NT);
         RingSlot st, buf;
         bool ok = true, issued = false;
         for (int v = first; v < items && ok; v += stride) {
             for (int kb = kb0; kb < kb1; ++kb, st.next(stages), buf.next(kBufs)) {
-                if (!warp_wait(&accempty[buf.i], buf.phase ^ 1u) || !warp_wait(&full[st.i], st.phase)) {
+                // even lanes watch the operands, odd ones the accumulator
+                if (!warp_wait_all(lane & 1 ? &accempty[buf.i] : &full[st.i], lane & 1 ? buf.phase ^ 1u : st.phase, abort_flag, status)) {
                     ok = false;
                     break;
                 }
@@ -180,8 +181,8 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < 4; ++k) tc_mma_f8(tmem + buf.i * NT, a + k * 2, b + k * 2, idesc, k > 0);
-                    tc_commit(&empty[st.i]);
                     tc_commit(&accfull[buf.i]);
+                    tc_commit(&empty[st.i]);
                 }
                 __syncwarp();
                 issued = true;
@@ -219,47 +220,52 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
         cp_async_wait_all();
     } else if (warp >= kFirstEpilogue) {
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        RingSlot buf, sl;
-        // A slot of scales is given back a block later: an arrival does not wait for the data of loads issued before it.
-        int held = -1;
+        constexpr int kBatch = C::kBatch;
+        // Blocks so far: block i has accumulator i % kBufs and slot i % kScaleSlots of the scales.  Products and copies complete in
+        // order, so a batch waits for its last block's (even lanes for the products, odd ones for the scales).  Slots of scales
+        // are given back a batch later: an arrival does not wait for the data of loads issued before it.
+        uint32_t at = 0;
+        int held = 0;
         for (int v = first; v < items; v += stride) {
             tile.locate(v, L.n_tiles, NT, rows, tiles);
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
-            for (int kb = kb0; kb < kb1; ++kb, buf.next(kBufs), sl.next(kScaleSlots)) {
-                done = done && warp_wait_all(&sfull[sl.i], sl.phase, abort_flag, status) &&
-                       warp_wait_all(&accfull[buf.i], buf.phase, abort_flag, status);
+            for (int kb = kb0; kb < kb1; kb += kBatch) {
+                const int count = min(kBatch, kb1 - kb);
+                const uint32_t end = at + count - 1;
+                done = done && warp_wait_all(lane & 1 ? &sfull[end % kScaleSlots] : &accfull[end % kBufs],
+                                             (lane & 1 ? end / kScaleSlots : end / kBufs) & 1u, abort_flag, status);
                 if (!done) break;
                 tc_fence_after();
-                const float* s = scales + sl.i * C::kScalePitch;
-                const float ws = s[NT];
-                const F2 ws2 = f2_of(ws, ws);
+                uint32_t d[kBatch][kCols];
 #pragma unroll
-                for (int c = 0; c < kCols; c += 16) {
-                    uint32_t d[16];
-                    tc_ld_32x32b_x16(tmem + lane_base + static_cast<uint32_t>(buf.i * NT + col0 + c), d);
-                    F2 by[8];
+                for (int i = 0; i < kBatch; ++i)
+                    if (i < count) {
+                        const uint32_t from = tmem + lane_base + (at + i) % kBufs * NT + static_cast<uint32_t>(col0);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(s + col0 + c + j);
-                        by[j / 2] = f2_mul(f2_of(x.x, x.y), ws2);
-                        by[j / 2 + 1] = f2_mul(f2_of(x.z, x.w), ws2);
+                        for (int c = 0; c < kCols; c += 16) tc_ld_32x32b_x16(from + c, d[i] + c);
                     }
-                    tc_wait_ld_of(d);
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 r = f2_parts(f2_fma(f2_of_bits(d[j], d[j + 1]), by[j / 2], f2_of(acc[c + j], acc[c + j + 1])));
-                        acc[c + j] = r.x;
-                        acc[c + j + 1] = r.y;
-                    }
-                }
+                tc_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&accempty[buf.i]);
-                    if (held >= 0) mbar_arrive(&sempty[held]);
-                }
-                held = sl.i;
+                if (lane < count) mbar_arrive(&accempty[(at + lane) % kBufs]);
+                if (lane < held) mbar_arrive(&sempty[(at - held + lane) % kScaleSlots]);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    if (i < count) {
+                        const float* s = scales + (at + i) % kScaleSlots * C::kScalePitch;
+                        const float ws = s[NT];
+#pragma unroll
+                        for (int j = 0; j < kCols; j += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(s + col0 + j);
+                            fma_loaded(acc[j], d[i][j], x.x * ws);
+                            fma_loaded(acc[j + 1], d[i][j + 1], x.y * ws);
+                            fma_loaded(acc[j + 2], d[i][j + 2], x.z * ws);
+                            fma_loaded(acc[j + 3], d[i][j + 3], x.w * ws);
+                        }
+                    }
+                at += count;
+                held = count;
             }
             if (ksplit > 1) break;   // one tile per cluster: joined below
 #pragma unroll
