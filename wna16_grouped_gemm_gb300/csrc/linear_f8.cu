@@ -14,11 +14,11 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Estimated times in us, from calls timed by themselves (T x K x N with weights that are not in L2; small with 8, 16 or
 // 32 rows per block / thin with 16 to 128 rows per tile and its best split of K / wide):
-//   4 x 4096 x 4096      4.3 / 8.2 / -       77 x 2048 x 1000    4.8 / 7.4 / 10.9     200 x 4096 x 4096   - / 16.7 / 18.8
-//   16 x 4096 x 4096     5.8 / 8.2 / -       64 x 4096 x 4096    15.5 / 10.8 / 18.4   512 x 4096 x 4096   - / 22.9 / 19.2
-//   32 x 4096 x 4096     8.7 / 9.6 / 18.1   128 x 4096 x 4096   - / 14.7 / 19.2      1024 x 4096 x 4096  - / 41.5 / 19.8
+//   4 x 4096 x 4096      4.3 / 8.2 / -       77 x 2048 x 1000    4.8 / 7.4 / 10.9     200 x 4096 x 4096   - / 15.4 / 18.2
+//   16 x 4096 x 4096     5.8 / 8.2 / -       64 x 4096 x 4096    15.5 / 10.1 / 18.4   512 x 4096 x 4096   - / 22.9 / 18.3
+//   32 x 4096 x 4096     8.7 / 9.6 / 18.1   128 x 4096 x 4096   - / 13.7 / 19.2      1024 x 4096 x 4096  - / 41.5 / 19.0
 //   4 x 16384 x 4096     15 / 15.9 / -     128 x 4096 x 1024   8.4 / 9.1 / 18.0    1024 x 512 x 4096   - / 16.1 / 7.4
-//   4 x 4096 x 32768     26.6 / 29.6 / 43    300 x 1024 x 4096   - / 11.7 / 8.7       64 x 4096 x 16384   - / 18.1 / 21.2
+//   4 x 4096 x 32768     26.6 / 29.6 / 43    300 x 1024 x 4096   - / 11.7 / 8.2       64 x 4096 x 16384   - / 17.0 / 21.2
 // (Wide tiles with a K shared over a cluster: 128 x 4096 x 4096 17.2 at best, 77 x 2048 x 1000 13.4; the join of 128 x 256
 // sums takes 8 us.  Few rows make wide tiles slow where many read the same ones at a time.)
 // A launch and a block's way through its prologue, a stage of 128 k, a tile's end, the join of a shared K.

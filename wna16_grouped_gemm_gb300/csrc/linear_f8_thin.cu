@@ -8,11 +8,11 @@
 //   epilogue (4 or 8 warps)  thread = channel: sum += P_b * (xs * ws) in registers, then the stores
 // A block of the grid takes tile after tile; with few tiles a cluster shares a tile's K, and
 // the parts are added in order through distributed shared memory.
-// Nine stages of 16 KB of weights are in flight per SM.  The epilogue takes as many blocks at a time as fill 64 registers (half
-// as many: 8192 rows of 256 experts 698 us).  Measured (us): 256 experts of 4096 x 4096 with a row each 590 (7.3 TB/s), with 32
-// each 660, 30 experts with a row or two 85 (5.9 TB/s; start and the last turn of tiles 10); 64 x 4096 x 4096 10.7 (K in four
-// parts), 4 x 16384 x 4096 15.9.  With many rows per tile the reads of the rows' scales from shared memory count (every lane
-// needs all of them): a stage takes 0.26 us with 16 rows, 0.47 with 128.
+// Eight stages of 16 KB of weights are in flight per SM.  The epilogue takes as many blocks at a time as fill 64 registers (half
+// as many: 8192 rows of 256 experts 698 us, not 654).  Measured (us): 256 experts of 4096 x 4096 with a row each 599 (7.2 TB/s),
+// with 32 each 648, 30 experts with a row or two 83 (6.1 TB/s; start and the last turn of tiles 10); 64 x 4096 x 4096 10.1 (K in
+// four parts), 4 x 16384 x 4096 15.9.  With many rows per tile the reads of the rows' scales from shared memory count (every lane
+// needs all of them): a stage takes 0.23 us with 16 rows, 0.45 with 128.
 #include <algorithm>
 
 #include "../../include/wna16_moe_f8.h"
@@ -26,9 +26,9 @@ namespace {
 constexpr int kM = 128;
 constexpr int kProducer = 0, kIssuer = 1, kScaler = 2, kLister = 3, kFirstEpilogue = 4;
 constexpr int kScaleSlots = 16;
-// More requests in flight make memory slower, fewer do not fill it.  us with 6, 9, 12 stages, 256 experts of 4096 x 4096:
-// 32 rows 89, 86, 86, 512 rows 556, 540, 569, 2048 rows 636, 617, 658.
-constexpr int kMaxStages = 9;
+// More requests in flight make memory slower, fewer do not fill it.  us with 6, 7, 8, 9 stages, 256 experts of 4096 x 4096:
+// 32 rows 86, 85, 84, 84, 512 rows 535, 528, 526, 532, 2048 rows 627, 618, 615, 631 (and 658 with 12).
+constexpr int kMaxStages = 8;
 constexpr int kAloneBytes = 150 * 1024;
 
 __device__ int g_status;   // of calls without a workspace
@@ -136,19 +136,22 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
             const uint64_t first_use = policy_evict_first(), again = policy_evict_normal();
             RingSlot st;
             uint32_t issued = 0;
-            bool ok = true;
+            bool ok = true, is_free = false;
             for (int v = first; v < items && ok; v += stride) {
                 tile.locate(v, L.n_tiles, NT, rows, tiles);
                 // weights that no other tile reads need not stay in L2
                 const uint64_t pol = tiles[tile.e + 1] - tiles[tile.e] > 1 ? again : first_use;
-                for (int kb = kb0; kb < kb1; ++kb, ++issued, st.next(stages)) {
-                    if (!mbar_wait(&empty[st.i], st.phase ^ 1u, abort_flag, status)) {
+                for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+                    if (!is_free && !wait_inline(smem_u32(&empty[st.i]), st.phase ^ 1u, abort_flag, status)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[st.i], C::kStageBytes);
-                    tma_load_3d(sW + st.i * kM * kScaleBlock, &tm_w, &full[st.i], kb * kScaleBlock, tile.nt * kM, tile.e, pol);
-                    tma_load_3d(sX + st.i * NT * kScaleBlock, &tm_x, &full[st.i], kb * kScaleBlock, tile.r0, 0, again);
+                    const int at = st.i;
+                    st.next(stages);
+                    is_free = mbar_test_wait(smem_u32(&empty[st.i]), st.phase ^ 1u);   // (of the next turn: it takes a while)
+                    mbar_arrive_expect_tx(&full[at], C::kStageBytes);
+                    tma_load_3d(sW + at * kM * kScaleBlock, &tm_w, &full[at], kb * kScaleBlock, tile.nt * kM, tile.e, pol);
+                    tma_load_3d(sX + at * NT * kScaleBlock, &tm_x, &full[at], kb * kScaleBlock, tile.r0, 0, again);
                 }
             }
             // no copy may be in flight when the block ends: wait for the last issue of every slot
@@ -165,31 +168,30 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
             }
         }
     } else if (warp == kIssuer) {
+        // One thread, without the warp's votes: what a stage costs here bounds a block's rate while memory is not full (votes, and
+        // an election per stage: 64 x 4096 x 4096 10.7 us, not 10.1).
         constexpr uint32_t idesc = idesc_e4m3_f32(kM, NT);
-        RingSlot st, buf;
-        bool ok = true, issued = false;
-        for (int v = first; v < items && ok; v += stride) {
-            for (int kb = kb0; kb < kb1; ++kb, st.next(stages), buf.next(kBufs)) {
-                // even lanes watch the operands, odd ones the accumulator
-                if (!warp_wait_all(lane & 1 ? &accempty[buf.i] : &full[st.i], lane & 1 ? buf.phase ^ 1u : st.phase, abort_flag, status)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t a = smem_desc_sw128_lo(smem_u32(sW + st.i * kM * kScaleBlock));
-                const uint32_t b = smem_desc_sw128_lo(smem_u32(sX + st.i * NT * kScaleBlock));
-                if (elect_one(status)) {
+        if (elect_one(status)) {
+            RingSlot st, buf;
+            bool ok = true, issued = false;
+            for (int v = first; v < items && ok; v += stride) {
+                for (int kb = kb0; kb < kb1; ++kb, st.next(stages), buf.next(kBufs)) {
+                    if (!wait_inline(smem_u32(&accempty[buf.i]), buf.phase ^ 1u, abort_flag, status) ||
+                        !wait_inline(smem_u32(&full[st.i]), st.phase, abort_flag, status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a = smem_desc_sw128_lo(smem_u32(sW + st.i * kM * kScaleBlock));
+                    const uint32_t b = smem_desc_sw128_lo(smem_u32(sX + st.i * NT * kScaleBlock));
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < 4; ++k) tc_mma_f8(tmem + buf.i * NT, a + k * 2, b + k * 2, idesc, k > 0);
-                    tc_commit(&accfull[buf.i]);
                     tc_commit(&empty[st.i]);
+                    tc_commit(&accfull[buf.i]);
+                    issued = true;
                 }
-                __syncwarp();
-                issued = true;
             }
-        }
-        if (issued && (!ok || *abort_flag)) {   // no MMA may still run when TMEM is released
-            if (elect_one(status)) {
+            if (issued && (!ok || *abort_flag)) {   // no MMA may still run when TMEM is released
                 tc_commit(drain);
                 const uint32_t a = smem_u32(drain);
                 const uint64_t began = globaltimer_ns();
@@ -197,8 +199,8 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
                     if (globaltimer_ns() - began > kWaitLimitNs) break;
                 }
             }
-            __syncwarp();
         }
+        __syncwarp();
     } else if (warp == kScaler) {
         RingSlot sl;
         bool ok = true;

@@ -10,15 +10,15 @@
 // the next block.  That needs 128 sums, two batches of 32 loaded values and little else per thread: the epilogue's
 // warps take registers from the others (setmaxnreg).
 //
-// Bound by what an SM gets from L2: a stage is 48 KB, at 64 bytes a cycle 770 cycles, of 860 that it takes (the tensor cores
-// need 512, the multiply-adds 256 issue slots).  Measured (us, 8192 x 4096 x 4096): 118 by itself (2.3 PFLOP/s), 129 among
-// other calls; 109 without the multiply-adds or with a quarter of the products, 102 with neither.  8192 x 2048 x 4096 68,
-// 1024 x 4096 x 4096 20 (one tile per SM).  256 experts of 4096 x 4096, 65536 rows with skewed popularity: 1420 to 1550 (1.5
-// PFLOP/s: 640 tiles of 128 rows for 512 that would be full).
+// Bound by what an SM gets from L2: a stage is 48 KB, at 64 bytes a cycle 770 cycles, of 835 that it takes (the tensor cores
+// need 512, the multiply-adds 256 issue slots).  Measured (us, 8192 x 4096 x 4096): 114 by itself (2.4 PFLOP/s), 125 among
+// other calls (with the issuers' waits and elections by whole warps 117; then 109 without the multiply-adds or with a quarter
+// of the products, 102 with neither).  8192 x 2048 x 4096 64, 1024 x 4096 x 4096 19 (one tile per SM).  256 experts of
+// 4096 x 4096, 65536 rows with skewed popularity: 1380 to 1500 (1.6 PFLOP/s: 640 tiles of 128 rows for 512 that would be full).
 // Tried and not kept: pairs of CTAs (cta_group::2; 32 KB per stage and CTA) 116, but tiles of 256 rows make that 1790 for the
 // experts; two blocks per SM with 128 x 128 tiles 147; 16 epilogue warps of 64 channels 128; packed multiply-adds
 // (fma.rn.f32x2) 140; stages of weights sent to L2 four to 32 blocks ahead 137, experts 1600 to 2170; three stages and twice
-// the room for results 124; results stored without TMA 147.
+// the room for results 124; results stored without TMA 147.  (All beside 118.)
 #include <algorithm>
 #include <atomic>
 
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp >= kIssuer && warp < kIssuer + kHalves) {
-            {
+            if (elect_one(status)) {
                 const int half = warp - kIssuer;
                 constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kHalf);
                 RingSlot st, buf;
@@ -165,36 +165,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int v = first; v < items && ok; v += stride) {
                     for (int kb = 0; kb < blocks; ++kb, st.next(stages), buf.next(kBufs)) {
                         const int acc = half * kBufs + buf.i;
-                        // even lanes watch the operands, odd ones the accumulator
-                        if (!warp_wait_inline(lane & 1 ? &accempty[acc] : &full[st.i], lane & 1 ? buf.phase ^ 1u : st.phase, abort_flag, status)) {
+                        if (!wait_inline(smem_u32(&full[st.i]), st.phase, abort_flag, status) ||
+                            !wait_inline(smem_u32(&accempty[acc]), buf.phase ^ 1u, abort_flag, status)) {
                             ok = false;
                             break;
                         }
                         const uint32_t a = smem_desc_sw128_lo(smem_u32(sX + st.i * kRows * kScaleBlock));
                         const uint32_t b = smem_desc_sw128_lo(smem_u32(sW + (st.i * kHalves + half) * kHalf * kScaleBlock));
-                        if (elect_one(status)) {
-                            tc_fence_after();
+                        tc_fence_after();
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) tc_mma_f8(tmem + acc * kHalf, a + k * 2, b + k * 2, idesc, k > 0);
-                            tc_commit(&accfull[acc]);
-                            tc_commit(&empty[st.i]);
-                        }
-                        __syncwarp();
+                        for (int k = 0; k < 4; ++k) tc_mma_f8(tmem + acc * kHalf, a + k * 2, b + k * 2, idesc, k > 0);
+                        tc_commit(&accfull[acc]);
+                        tc_commit(&empty[st.i]);
                         issued = true;
                     }
                 }
                 if (issued && (!ok || *abort_flag)) {   // no MMA may still run when TMEM is released
-                    if (elect_one(status)) {
-                        tc_commit(&drain[half]);
-                        const uint32_t a = smem_u32(&drain[half]);
-                        const uint64_t began = globaltimer_ns();
-                        while (!mbar_try_wait(a, 0)) {
-                            if (globaltimer_ns() - began > kWaitLimitNs) break;
-                        }
+                    tc_commit(&drain[half]);
+                    const uint32_t a = smem_u32(&drain[half]);
+                    const uint64_t began = globaltimer_ns();
+                    while (!mbar_try_wait(a, 0)) {
+                        if (globaltimer_ns() - began > kWaitLimitNs) break;
                     }
-                    __syncwarp();
                 }
             }
+            __syncwarp();
         }
     } else {
         more_registers<kEpilogueRegs>();
