@@ -456,6 +456,12 @@ def test_grouped(moe, counts, K, N, first, behind, dt):
     check_grouped(moe, counts, K, N, dt, first, behind, seed=len(counts))
 
 
+@pytest.mark.parametrize("mean,K", [(2, 640), (3, 1152), (9, 896), (30, 640), (36, 1408), (60, 640)])
+def test_grouped_several_tiles_per_block(moe, mean, K):
+    """More tiles than SMs, of every kind, with numbers of blocks of 128 k that no batch or ring divides."""
+    check_grouped(moe, np.random.default_rng(K).integers(0, 2 * mean + 1, 60).tolist(), K, 700, BF, first=1, behind=2, seed=mean)
+
+
 def test_grouped_many_experts(moe):
     counts = np.random.default_rng(0).integers(0, 5, 1024).tolist()
     check_grouped(moe, counts, 128, 128, HF)
