@@ -202,6 +202,17 @@ def test_unsort_grad(moe, T, topk, E, K, dt, weighted, added, padding):
     assert only[1] is None and torch.equal(only[0], dy)
 
 
+@pytest.mark.parametrize("T,topk,E,K,dt,weighted,added,padding", [
+    # few slots per token: several runs of a row at a time, the last ones partly or wholly past its end
+    (3000, 1, 16, 4096, BF, True, False, 0.0), (2500, 2, 8, 2568, FP, True, True, 0.2), (3000, 4, 64, 1544, HF, False, True, 0.1),
+    (700, 2, 8, 16384, FP, True, False, 0.0), (1000, 4, 8, 4104, BF, True, True, 0.4), (4000, 1, 8, 8, FP, True, False, 0.5),
+    (1, 2, 8, 8192, BF, True, True, 0.0), (1500, 3, 8, 3080, BF, False, False, 0.0), (1200, 2, 8, 1026, HF, True, False, 0.0),
+])
+def test_unsort_few_slots(moe, T, topk, E, K, dt, weighted, added, padding):
+    test_unsort(moe, T, topk, E, K, dt, weighted, added, padding)
+    test_unsort_grad(moe, T, topk, E, K, dt, weighted, added, padding)
+
+
 def test_rows_past_32_bits(moe):
     """Elements and bytes past 2^31 and 2^32: the rows of the last experts and tokens."""
     T, topk, E, K = 9000, 8, 16, 32768

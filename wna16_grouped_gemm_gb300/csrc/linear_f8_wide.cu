@@ -106,6 +106,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(tmem_slot, kTmem);
         tmem_relinquish();
     }
+    // one weight: the first stages of it on their way to L2 while the kernel before finishes (1024 x 4096 x 4096 19.4 us, not 19.9;
+    // the tiles for few rows lose by it: 128 x 4096 x 4096 14.4, not 13.8)
+    if (!p.offsets) {
+        const int nt = first / ((p.T + kRows - 1) / kRows), n = min(kTile, p.N - nt * kTile);
+        for (int i = threadIdx.x; i < n * min(stages, blocks); i += kThreads)
+            prefetch_l2(p.wq + static_cast<int64_t>(nt * kTile + i % n) * p.K + i / n * kScaleBlock);
+    }
     pdl_wait();
     f8_load_offsets(p, rows);
     if (warp == kIssuer) {

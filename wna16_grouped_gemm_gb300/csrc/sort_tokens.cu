@@ -7,9 +7,9 @@
 //
 // Bound by the bytes of the rows.  Sums are fp32, in an order that the sizes alone fix.
 // Measured (us; 8 slots per token on 256 experts, rows of 4096 bf16; of a measured copy's 6793 GB/s):
-//   8192 tokens   lists 8.8, lists and rows 106 (0.84 of it; the copies alone 0.91), back 99 (0.90), gradient 177 (0.95)
-//   4 tokens      3.0, 2.1, 3.9 (a launch); 1024 tokens: 19, 16, 28
-//   8192 tokens   fp32 202, 171, 335; e4m3 58; rows of 4100 bf16 (4-byte accesses) 134, 116, 213; of 4097 207, 244, 497
+//   8192 tokens   lists 8.8, lists and rows 106 (0.84 of it; the copies alone 0.91), back 99 (0.90), gradient 173 (0.97)
+//   4 tokens      3.0, 2.1, 3.9 (a launch); 1024 tokens: 17.5, 16, 25
+//   8192 tokens   fp32 202, 171, 335; e4m3 56; rows of 4100 bf16 (4-byte accesses) 132, 116, 212; of 4097 207, 244, 443
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -264,17 +264,24 @@ __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortP
 }
 
 constexpr int kCopyWarps = 8;
+// The rows go ahead to L2 while the lists are made, 8 KB of each, if those of all tokens are few: 1024 tokens of 8 KB 19.2 us
+// without and 17.6 with, 2047 31.9 and 30.0, 8192 of 4 KB 57.7 and 56.3; of 8 KB 105.8 and 107.1, 32768 of 4 KB 221.7 and 223.9.
+constexpr int64_t kAheadBytes = 8192, kAheadTotal = 40 << 20;
 
 // rows[inv[t][j]] = x[t]: a warp per token, which reads its row once.
 template <typename V>
 __global__ void __launch_bounds__(32 * kCopyWarps) sort_copy_kernel(const SortParams p) {
-    pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5);
+    const char* row = static_cast<const char*>(p.x) + t * p.x_pitch;
+    const int64_t ahead = min(p.row_bytes, kAheadBytes);
+    if (t < p.T && p.T * ahead <= kAheadTotal)
+        for (int64_t b = lane * 128; b < ahead; b += 32 * 128) prefetch_l2(row + b);
+    pdl_wait();
+    pdl_trigger();
     if (t >= p.T) return;
     const int64_t n_vec = p.row_bytes / static_cast<int64_t>(sizeof(V));
-    const V* src = reinterpret_cast<const V*>(static_cast<const char*>(p.x) + t * p.x_pitch);
+    const V* src = reinterpret_cast<const V*>(row);
     V* dst = static_cast<V*>(p.rows);
     const int32_t* inv = p.inv + t * p.topk;
     for (int j0 = 0; j0 < p.topk; j0 += 32) {
@@ -341,7 +348,7 @@ constexpr int kBatch = 8;   // rows read at the same time
 // Per SM.  (The gradient of 8192 x 8 slots with three blocks, whose registers then spill, 179 us, with two 177; of 512
 // x 8 slots 17.8 and 14.6.)
 constexpr int kBackBlocks = 3, kGradBlocks = 2;
-constexpr int kRunThreads = 128; // of a run of unsort
+constexpr int kRunThreads = 128; // of a run of unsort, and of the gradient's of short rows
 
 // The values of a thread, 16 bytes of them: neighbours where rows are read 16 bytes at a time, else every 32nd access
 // of a warp's (of W = 4 or 2 bytes), so that its lanes read neighbours.
@@ -449,67 +456,79 @@ __device__ __forceinline__ Slots load_slots(const UnsortParams& p, int64_t t, in
     return s;
 }
 
-// A block takes runs of 2 KB of one token, item after item, and has the next one's slots
-// loaded while it works on one; a thread has 16 bytes of a run.
-template <typename T, int W>
-__global__ void __launch_bounds__(kBackThreads, kBackBlocks) unsort_kernel(const UnsortParams p, int runs, int64_t items) {
+// A block takes RUNS neighbouring runs of 2 KB of one token, item after item, and has the next one's slots
+// loaded while it works on one; a thread has 16 bytes of a run.  Several runs at a time keep as many loads in flight
+// with few slots per token as one does with eight.
+template <typename T, int W, int RUNS>
+__global__ void __launch_bounds__(kBackThreads, RUNS == 4 ? kGradBlocks : kBackBlocks) unsort_kernel(const UnsortParams p, int groups, int64_t items) {
+    constexpr int kSlots = kBatch / RUNS;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int start = chunk_start<T, W>(), width = static_cast<int>(blockDim.x) * kV<T>;   // values of a run
     const T* y = static_cast<const T*>(p.y);
-    int64_t t = blockIdx.x / runs;
-    int run = static_cast<int>(blockIdx.x - t * runs);
-    const int64_t step_t = gridDim.x / runs;
-    const int step_run = static_cast<int>(gridDim.x - step_t * runs);
+    int64_t t = blockIdx.x / groups;
+    int group = static_cast<int>(blockIdx.x - t * groups);
+    const int64_t step_t = gridDim.x / groups;
+    const int step_group = static_cast<int>(gridDim.x - step_t * groups);
     Slots next = load_slots(p, t, 0, lane);
     for (int64_t v = blockIdx.x; v < items; v += gridDim.x) {
-        const int64_t now = t, k = static_cast<int64_t>(run) * width + start, n = p.K - k;
+        const int64_t now = t, k = static_cast<int64_t>(group) * RUNS * width + start, n = p.K - k;
         Slots s = next;
         t += step_t;
-        run += step_run;
-        if (run >= runs) {
-            run -= runs;
+        group += step_group;
+        if (group >= groups) {
+            group -= groups;
             ++t;
         }
         next = load_slots(p, t, 0, lane);
-        float sum[kV<T>] = {};
-        for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+        float sum[RUNS][kV<T>] = {};
+        for (int j0 = 0; j0 < p.topk; j0 += kSlots) {
             if (j0 > 0 && j0 % 32 == 0) s = load_slots(p, now, j0, lane);
-            Chunk c[kBatch];
-            int row[kBatch];
+            Chunk c[kSlots][RUNS];
+            int row[kSlots];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+            for (int i = 0; i < kSlots; ++i) {
                 row[i] = __shfl_sync(kAll, s.row, (j0 + i) & 31);
-                if (row[i] >= 0 && n > 0) c[i] = load_chunk<T, W>(y + row[i] * p.K + k, n);
+#pragma unroll
+                for (int q = 0; q < RUNS; ++q)
+                    if (row[i] >= 0 && n > q * width) c[i][q] = load_chunk<T, W>(y + row[i] * p.K + k + q * width, n - q * width);
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+            for (int i = 0; i < kSlots; ++i) {
                 const float w = __shfl_sync(kAll, s.w, (j0 + i) & 31);
                 if (row[i] >= 0) {
-                    float f[kV<T>];
-                    to_floats<T>(c[i], f);
 #pragma unroll
-                    for (int e = 0; e < kV<T>; ++e) sum[e] = fmaf(w, f[e], sum[e]);
+                    for (int q = 0; q < RUNS; ++q) {
+                        float f[kV<T>];
+                        to_floats<T>(c[i][q], f);
+#pragma unroll
+                        for (int e = 0; e < kV<T>; ++e) sum[q][e] = fmaf(w, f[e], sum[q][e]);
+                    }
                 }
             }
         }
-        if (n <= 0) continue;
-        if (p.addend) {
-            float a[kV<T>];
-            to_floats<T>(load_chunk<T, W>(static_cast<const T*>(p.addend) + now * p.K + k, n), a);
 #pragma unroll
-            for (int e = 0; e < kV<T>; ++e) sum[e] += a[e];
+        for (int q = 0; q < RUNS; ++q) {
+            if (n <= q * width) break;
+            const int64_t at = now * p.K + k + q * width;
+            if (p.addend) {
+                float a[kV<T>];
+                to_floats<T>(load_chunk<T, W>(static_cast<const T*>(p.addend) + at, n - q * width), a);
+#pragma unroll
+                for (int e = 0; e < kV<T>; ++e) sum[q][e] += a[e];
+            }
+            store_chunk<T, W>(static_cast<T*>(p.out) + at, n - q * width, from_floats<T>(sum[q]));
         }
-        store_chunk<T, W>(static_cast<T*>(p.out) + now * p.K + k, n, from_floats<T>(sum));
     }
 }
 
-// A block takes token after token: a thread has its chunks of dout and, for up to 8 slots at a time,
+// A block takes token after token: a thread has its chunks of dout, RUNS of them at a time, and, for up to 8 / RUNS slots at a time,
 // the same chunks of their rows of y.  The dot products are summed over a thread's chunks, the
 // lanes and the warps, in that order.
-template <typename T, int W>
+template <typename T, int W, int RUNS>
 __global__ void __launch_bounds__(kBackThreads, kGradBlocks) unsort_grad_kernel(const UnsortParams p) {
+    constexpr int kSlots = kBatch / RUNS;
     __shared__ float part[2][kBackThreads / 32][kBatch];
     pdl_wait();
     pdl_trigger();
@@ -523,41 +542,49 @@ __global__ void __launch_bounds__(kBackThreads, kGradBlocks) unsort_grad_kernel(
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         Slots s = next;
         next = load_slots(p, t + gridDim.x, 0, lane);
-        for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+        for (int j0 = 0; j0 < p.topk; j0 += kSlots) {
             if (j0 > 0 && j0 % 32 == 0) s = load_slots(p, t, j0, lane);
             float dot[kBatch] = {};
-            for (int64_t k0 = 0; k0 < p.K; k0 += width) {   // the same turns for every thread
+            for (int64_t k0 = 0; k0 < p.K; k0 += RUNS * width) {   // the same turns for every thread
                 const int64_t k = k0 + start, n = p.K - k;
-                Chunk g, c[kBatch];
-                int row[kBatch];
-                if (n > 0) g = load_chunk<T, W>(dout + t * p.K + k, n);
+                Chunk g[RUNS], c[kSlots][RUNS];
+                int row[kSlots];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int r = __shfl_sync(kAll, s.row, (j0 + i) & 31);
-                    row[i] = n > 0 ? r : -1;
-                    if (p.dweights && row[i] >= 0) c[i] = load_chunk<T, W>(y + row[i] * p.K + k, n);
+                for (int q = 0; q < RUNS; ++q)
+                    if (n > q * width) g[q] = load_chunk<T, W>(dout + t * p.K + k + q * width, n - q * width);
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) {
+                    row[i] = __shfl_sync(kAll, s.row, (j0 + i) & 31);
+#pragma unroll
+                    for (int q = 0; q < RUNS; ++q)
+                        if (p.dweights && row[i] >= 0 && n > q * width)
+                            c[i][q] = load_chunk<T, W>(y + row[i] * p.K + k + q * width, n - q * width);
                 }
-                float d[kV<T>];
-                to_floats<T>(g, d);
-                if (p.dweights) {
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i)
-                        if (row[i] >= 0) {
-                            float f[kV<T>];
-                            to_floats<T>(c[i], f);
+                for (int q = 0; q < RUNS; ++q) {
+                    const bool mine = n > q * width;
+                    float d[kV<T>];
+                    to_floats<T>(g[q], d);
+                    if (p.dweights) {
 #pragma unroll
-                            for (int e = 0; e < kV<T>; ++e) dot[i] = fmaf(d[e], f[e], dot[i]);
-                        }
-                }
-                if (dy) {
+                        for (int i = 0; i < kSlots; ++i)
+                            if (mine && row[i] >= 0) {
+                                float f[kV<T>];
+                                to_floats<T>(c[i][q], f);
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const float w = __shfl_sync(kAll, s.w, (j0 + i) & 31);
-                        if (row[i] >= 0) {
-                            float o[kV<T>];
+                                for (int e = 0; e < kV<T>; ++e) dot[i] = fmaf(d[e], f[e], dot[i]);
+                            }
+                    }
+                    if (dy) {
 #pragma unroll
-                            for (int e = 0; e < kV<T>; ++e) o[e] = w * d[e];
-                            store_chunk<T, W>(dy + row[i] * p.K + k, n, from_floats<T>(o));
+                        for (int i = 0; i < kSlots; ++i) {
+                            const float w = __shfl_sync(kAll, s.w, (j0 + i) & 31);
+                            if (mine && row[i] >= 0) {
+                                float o[kV<T>];
+#pragma unroll
+                                for (int e = 0; e < kV<T>; ++e) o[e] = w * d[e];
+                                store_chunk<T, W>(dy + row[i] * p.K + k + q * width, n - q * width, from_floats<T>(o));
+                            }
                         }
                     }
                 }
@@ -566,7 +593,7 @@ __global__ void __launch_bounds__(kBackThreads, kGradBlocks) unsort_grad_kernel(
             const float sum = warp_sums(dot, lane);
             if ((lane & 3) == 0) part[turn][warp][lane >> 2] = sum;
             __syncthreads();   // (and the other half of `part` has been read)
-            if (threadIdx.x < kBatch && j0 + static_cast<int>(threadIdx.x) < p.topk) {
+            if (threadIdx.x < kSlots && j0 + static_cast<int>(threadIdx.x) < p.topk) {
                 float total = 0.0f;
                 for (int i = 0; i < static_cast<int>(blockDim.x / 32); ++i) total += part[turn][i][threadIdx.x];
                 p.dweights[t * p.topk + j0 + threadIdx.x] = total;
@@ -582,20 +609,46 @@ int back_threads(int64_t K, int most) {
     return static_cast<int>(std::min<int64_t>(most, (K + 32 * kV<T> - 1) / (32 * kV<T>) * 32));
 }
 
+// Runs at a time: what keeps eight loads in flight, of those that a row has, and fewer if blocks would go without items.
+// us with one run / so, 8192 tokens of 4096 bf16: 1 slot 53 / 28, gradient 81 / 40; 2 slots 66 / 34, 93 / 54; 4 slots 76 / 52,
+// 119 / 93.
+int runs_at_a_time(const UnsortParams& p, int64_t runs, int64_t blocks) {
+    if (p.access != 16) return 1;
+    int q = p.topk <= 2 ? 4 : p.topk <= 4 ? 2 : 1;
+    while (q > 1 && (q > runs || p.T * ((runs + q - 1) / q) < blocks)) q /= 2;
+    return q;
+}
+
 template <typename T>
 cudaError_t launch_back(const UnsortParams& p, int sms, cudaStream_t s) {
     const int threads = back_threads<T>(p.K, kRunThreads), width = threads * kV<T>;
-    const int runs = static_cast<int>((p.K + width - 1) / width);
-    const int64_t items = p.T * runs;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, static_cast<int64_t>(sms) * kBackBlocks * kBackThreads / threads)));
-    const auto kernel = p.access == 16 ? unsort_kernel<T, 16> : p.access == 4 ? unsort_kernel<T, 4> : unsort_kernel<T, sizeof(T)>;
-    return launch_pdl(kernel, grid, dim3(threads), 0, s, p, runs, items);
+    const int64_t runs = (p.K + width - 1) / width, per_sm = kBackThreads / threads;
+    const int q = runs_at_a_time(p, runs, sms * kBackBlocks * per_sm);
+    const int64_t blocks = sms * (q == 4 ? kGradBlocks : kBackBlocks) * per_sm;
+    const int groups = static_cast<int>((runs + q - 1) / q);
+    const int64_t items = p.T * groups;
+    const dim3 grid(static_cast<unsigned>(std::min(items, blocks)));
+    const auto kernel = q == 4             ? unsort_kernel<T, 16, 4>
+                        : q == 2           ? unsort_kernel<T, 16, 2>
+                        : p.access == 16   ? unsort_kernel<T, 16, 1>
+                        : p.access == 4    ? unsort_kernel<T, 4, 1>
+                                           : unsort_kernel<T, sizeof(T), 1>;
+    return launch_pdl(kernel, grid, dim3(threads), 0, s, p, groups, items);
 }
 template <typename T>
 cudaError_t launch_back_grad(const UnsortParams& p, int sms, cudaStream_t s) {
-    const int threads = back_threads<T>(p.K, kBackThreads);
+    // Short rows have more blocks with half the threads, if there are tokens for them: 8192 x 8 slots of 4096 bf16 173 us, not 178, 1024
+    // x 8 25.1 (27.2), 4096 x 8 of 2048 47.2 (52.7), 8192 x 2 54 (75); 2047 x 8 49.4 (48.0), 200 x 8 9.7 (7.9), 8192 x 8 of 4096
+    // fp32 352 (335).
+    const bool narrow = p.K * static_cast<int64_t>(sizeof(T)) <= 8192 && p.T >= 2 * sms;
+    const int threads = back_threads<T>(p.K, narrow ? kRunThreads : kBackThreads), width = threads * kV<T>;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(p.T, static_cast<int64_t>(sms) * kGradBlocks * kBackThreads / threads)));
-    const auto kernel = p.access == 16 ? unsort_grad_kernel<T, 16> : p.access == 4 ? unsort_grad_kernel<T, 4> : unsort_grad_kernel<T, sizeof(T)>;
+    const int q = runs_at_a_time(p, (p.K + width - 1) / width, 0);
+    const auto kernel = q == 4             ? unsort_grad_kernel<T, 16, 4>
+                        : q == 2           ? unsort_grad_kernel<T, 16, 2>
+                        : p.access == 16   ? unsort_grad_kernel<T, 16, 1>
+                        : p.access == 4    ? unsort_grad_kernel<T, 4, 1>
+                                           : unsort_grad_kernel<T, sizeof(T), 1>;
     return launch_pdl(kernel, grid, dim3(threads), 0, s, p);
 }
 
