@@ -2,9 +2,10 @@
 //   m = max |w|,  scale = m / 448,  code = e4m3(w * (448 / m))
 //
 // Bound by the bytes of the weights, read once.  A thread block has one block of
-// the weight in registers from its reads to the codes (three of them per SM: with two, 16 x 4096 x 4096 bf16 153 us).
-// Measured (us), 16 x 4096 x 4096: fp32 184 (7.3 TB/s), transposed 190; bf16 128 (6.3), transposed 254.  1000 x 2048
-// bf16 2.6, transposed 4.2.
+// the weight in registers from its reads to the codes (four of them per SM with 16-bit values, three with fp32; with three, 16 x
+// 4096 x 4096 bf16 126 us and transposed 134; with five fp16 135 and 150).
+// Measured (us), 16 x 4096 x 4096: fp32 183 (7.3 TB/s), transposed 186; bf16 120 (6.7), transposed 121; fp16 121, 126.  1000 x
+// 2048 bf16 2.6, transposed 2.9.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -24,19 +25,51 @@ constexpr int kTurns = kScaleBlock * kScaleBlock / (kThreads * kV);
 constexpr float kTiny = 7.888609052210118e-31f;                    // 2^-100
 constexpr float kQ = 448.0f;
 
+// A thread's 8 neighbouring values, in words (as an array of 16-bit values they cost a permutation each).
 template <typename T>
-__device__ __forceinline__ float to_f(T v) {
-    if constexpr (sizeof(T) == 4)
-        return v;
-    else if constexpr (std::is_same<T, __half>::value)
-        return __half2float(v);
-    else
-        return __bfloat162float(v);
+struct alignas(16) Chunk {
+    static constexpr int kPer = 4 / static_cast<int>(sizeof(T));   // values per word
+    uint32_t w[kV / kPer];
+    __device__ __forceinline__ float operator[](int j) const {
+        const uint32_t v = w[j / kPer];
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(v);
+        else if constexpr (std::is_same<T, __half>::value)
+            return __half2float(__ushort_as_half(static_cast<unsigned short>(j % 2 ? v >> 16 : v & 0xffffu)));
+        else
+            return __uint_as_float(j % 2 ? v & 0xffff0000u : v << 16);
+    }
+};
+// the values at p, `count` of them, then zeros
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_some(const T* p, int count) {
+    using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+    const Bits* b = reinterpret_cast<const Bits*>(p);
+    Chunk<T> c;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+        const uint32_t v = j < count ? b[j] : 0u;
+        if (j % Chunk<T>::kPer == 0)
+            c.w[j / Chunk<T>::kPer] = v;
+        else
+            c.w[j / Chunk<T>::kPer] |= v << 16;
+    }
+    return c;
+}
+
+// Bytes r of the words a become the bytes of word r (byte by byte, by shifts: 16 x 4096 x 4096 bf16 transposed 254 us).
+__device__ __forceinline__ void transpose_bytes(const uint32_t (&a)[4], uint32_t (&o)[4]) {
+    const uint32_t t0 = __byte_perm(a[0], a[1], 0x5140), t1 = __byte_perm(a[2], a[3], 0x5140);
+    const uint32_t t2 = __byte_perm(a[0], a[1], 0x7362), t3 = __byte_perm(a[2], a[3], 0x7362);
+    o[0] = __byte_perm(t0, t1, 0x5410);
+    o[1] = __byte_perm(t0, t1, 0x7632);
+    o[2] = __byte_perm(t2, t3, 0x5410);
+    o[3] = __byte_perm(t2, t3, 0x7632);
 }
 
 // COLUMNS: w's columns are contiguous (a transposed weight), else its rows.
 template <typename T, bool COLUMNS, bool VEC>
-__global__ void __launch_bounds__(kThreads, 3) blocks_kernel(const BlocksParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) blocks_kernel(const BlocksParams p) {
     __shared__ uint32_t warp_max[kThreads / 32];
     __shared__ alignas(16) uint8_t tile[COLUMNS ? kScaleBlock * kScaleBlock : 16];
     pdl_wait();
@@ -54,9 +87,7 @@ __global__ void __launch_bounds__(kThreads, 3) blocks_kernel(const BlocksParams 
     constexpr int kGroups = kThreads / (kScaleBlock / kV);
     static_assert(kTurns == kV, "8 x 8");
     auto slow_of = [&](int i) { return COLUMNS ? group * kTurns + i : group + i * kGroups; };
-    struct alignas(16) Chunk {
-        T v[kV];
-    } c[kTurns];
+    Chunk<T> c[kTurns];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
@@ -65,18 +96,17 @@ __global__ void __launch_bounds__(kThreads, 3) blocks_kernel(const BlocksParams 
         const int count = COLUMNS ? rows - fast : (slow < rows ? kV : 0);
         if (VEC && count >= kV) {
 #pragma unroll
-            for (int j = 0; j < static_cast<int>(sizeof(Chunk) / 16); ++j)
-                reinterpret_cast<uint4*>(c[i].v)[j] = __ldg(reinterpret_cast<const uint4*>(at) + j);
+            for (int j = 0; j < static_cast<int>(sizeof(c[i]) / 16); ++j)
+                reinterpret_cast<uint4*>(c[i].w)[j] = __ldg(reinterpret_cast<const uint4*>(at) + j);
         } else {
-#pragma unroll
-            for (int j = 0; j < kV; ++j) c[i].v[j] = j < count ? at[j] : T(0.0f);
+            c[i] = load_some(at, count);
         }
     }
     // the largest magnitude as bits: infinities and NaN are above all numbers
 #pragma unroll
     for (int i = 0; i < kTurns; ++i)
 #pragma unroll
-        for (int j = 0; j < kV; ++j) top = max(top, __float_as_uint(to_f(c[i].v[j])) & 0x7fffffffu);
+        for (int j = 0; j < kV; ++j) top = max(top, __float_as_uint(c[i][j]) & 0x7fffffffu);
     top = __reduce_max_sync(0xffffffffu, top);
     if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = top;
     __syncthreads();
@@ -93,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 3) blocks_kernel(const BlocksParams 
         if (!some) return;
 #pragma unroll
         for (int j = 0; j < kV; j += 2) {
-            const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(to_f(c[i].v[j]) * by, to_f(c[i].v[j + 1]) * by),
+            const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(c[i][j] * by, c[i][j + 1] * by),
                                                           __NV_SATFINITE, __NV_E4M3);
             code[j / 4] |= two << (j % 4 * 8);
         }
@@ -121,14 +151,14 @@ __global__ void __launch_bounds__(kThreads, 3) blocks_kernel(const BlocksParams 
         // of different n / 8, then meet no bank twice.
         const int f = fast / kV;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            uint32_t lo = 0, hi = 0;
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {code[0][h], code[1][h], code[2][h], code[3][h]}, b[4] = {code[4][h], code[5][h], code[6][h], code[7][h]};
+            uint32_t lo[4], hi[4];
+            transpose_bytes(a, lo);
+            transpose_bytes(b, hi);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo |= (code[i][j / 4] >> (j % 4 * 8) & 0xffu) << (i * 8);
-                hi |= (code[i + 4][j / 4] >> (j % 4 * 8) & 0xffu) << (i * 8);
-            }
-            *reinterpret_cast<uint2*>(tile + (fast + j) * kScaleBlock + (group ^ f) * 8) = make_uint2(lo, hi);
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint2*>(tile + (fast + h * 4 + j) * kScaleBlock + (group ^ f) * 8) = make_uint2(lo[j], hi[j]);
         }
         __syncthreads();
         for (int i = threadIdx.x; i < rows * (kScaleBlock / 16); i += kThreads) {
