@@ -9,7 +9,7 @@
 // Measured (us; 8 slots per token on 256 experts, rows of 4096 bf16; of a measured copy's 6793 GB/s):
 //   8192 tokens   lists 8.8, lists and rows 106 (0.84 of it; the copies alone 0.91), back 99 (0.90), gradient 173 (0.97)
 //   4 tokens      3.0, 2.1, 3.9 (a launch); 1024 tokens: 17.5, 16, 25
-//   8192 tokens   fp32 202, 171, 335; e4m3 56; rows of 4100 bf16 (4-byte accesses) 132, 116, 212; of 4097 207, 244, 443
+//   8192 tokens   fp32 202, 171, 335; e4m3 56; rows of 4100 bf16 (4-byte accesses) 122, 116, 212; of 4097 203, 244, 443
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -268,9 +268,10 @@ constexpr int kCopyWarps = 8;
 // without and 17.6 with, 2047 31.9 and 30.0, 8192 of 4 KB 57.7 and 56.3; of 8 KB 105.8 and 107.1, 32768 of 4 KB 221.7 and 223.9.
 constexpr int64_t kAheadBytes = 8192, kAheadTotal = 40 << 20;
 
-// rows[inv[t][j]] = x[t]: a warp per token, which reads its row once.
+// rows[inv[t][j]] = x[t]: a warp per token, which reads its row once.  (Six blocks per SM: with five, 8192 x 8 of 4100 bf16 134 us,
+// not 122; with seven, of 4096 118, not 105.)
 template <typename V>
-__global__ void __launch_bounds__(32 * kCopyWarps) sort_copy_kernel(const SortParams p) {
+__global__ void __launch_bounds__(32 * kCopyWarps, 6) sort_copy_kernel(const SortParams p) {
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5);
     const char* row = static_cast<const char*>(p.x) + t * p.x_pitch;
