@@ -1,0 +1,53 @@
+"""Rules of the kernels' sources whose breach is a race, which no run has to show (host side, no GPU)."""
+from __future__ import annotations
+
+import glob
+import os
+import re
+
+import pytest
+
+from wna16_grouped_gemm_gb300 import build
+
+SOURCES = sorted(glob.glob(os.path.join(build.CSRC, "*.cu")))
+
+
+def code_of(path):
+    """The source without comments and strings' contents."""
+    with open(path) as f:
+        s = f.read()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", lambda m: "\n" * m.group().count("\n"), s, flags=re.S)
+
+
+def bodies(s):
+    """(name, body) of every __global__ function that is defined in s."""
+    for m in re.finditer(r"__global__\b", s):
+        name = re.search(r"\b(\w+_kernel)\s*\(", s[m.end():m.end() + 600])
+        at = s.find("{", m.end())
+        semicolon = s.find(";", m.end())
+        if at < 0 or (0 <= semicolon < at):
+            continue
+        depth, i = 0, at
+        while True:
+            depth += {"{": 1, "}": -1}.get(s[i], 0)
+            i += 1
+            if depth == 0:
+                break
+        yield name.group(1) if name else "?", s[at:i]
+
+
+def test_kernels_are_found():
+    assert sum(len(list(bodies(code_of(p)))) for p in SOURCES) >= 25
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_a_cluster_has_started_before_its_shared_memory_is_reached(path):
+    """A block of a cluster may reach another's shared memory once a barrier of the cluster shows that it has
+    started: cluster_sync(), or cluster_wait() behind a cluster_arrive()."""
+    for name, body in bodies(code_of(path)):
+        first = body.find("map_shared(")
+        if first < 0:
+            continue
+        before = body[:first]
+        split = before.find("cluster_arrive()")
+        assert "cluster_sync()" in before or 0 <= split < before.find("cluster_wait()"), name

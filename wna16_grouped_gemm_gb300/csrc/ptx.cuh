@@ -453,13 +453,16 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
-// All threads of all CTAs of the cluster.
+// All threads of all CTAs of the cluster: the barrier in one, and in two halves with work between them.  One of them stands
+// before the first access to another CTA's shared memory: a CTA that has not started has none.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile(
         "barrier.cluster.arrive.release.aligned;\n\t"
         "barrier.cluster.wait.acquire.aligned;" ::
             : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The shared-memory address `addr` of this CTA in the CTA of rank `rank`.
 __device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank) {

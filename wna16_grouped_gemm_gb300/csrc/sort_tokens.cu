@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortP
     const int rank = static_cast<int>(cluster_ctarank());
     const unsigned begin = static_cast<unsigned>(p.expert_begin);
     const unsigned* ids = reinterpret_cast<const unsigned*>(p.ids);
+    cluster_arrive();   // (the wait for it is behind the counting)
     pdl_wait();
     pdl_trigger();
     const int64_t R = p.T * p.topk;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortP
         count();
     }
     __syncthreads();
+    cluster_wait();     // every block has started: their shared memory is theirs
     if (tid < E) {
         int c = 0;
 #pragma unroll 8
