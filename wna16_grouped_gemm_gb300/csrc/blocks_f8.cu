@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) blocks_kerne
         if (VEC && count >= kV) {
 #pragma unroll
             for (int j = 0; j < static_cast<int>(sizeof(c[i]) / 16); ++j)
-                reinterpret_cast<uint4*>(c[i].w)[j] = __ldg(reinterpret_cast<const uint4*>(at) + j);
+                reinterpret_cast<uint4*>(c[i].w)[j] = reinterpret_cast<const uint4*>(at)[j];
         } else {
             c[i] = load_some(at, count);
         }

@@ -94,7 +94,7 @@ __device__ __forceinline__ bool warp_wait_inline(uint64_t* bar, uint32_t parity,
 // loaded into rows) held to [their predecessor, T]; returns whether one had to be.
 __device__ __forceinline__ void f8_load_offsets(const LinearF8Params& p, int* rows) {
     if (!p.offsets) return;
-    for (int i = threadIdx.x; i <= p.E; i += blockDim.x) rows[i] = __ldg(p.offsets + i);
+    for (int i = threadIdx.x; i <= p.E; i += blockDim.x) rows[i] = p.offsets[i];
     __syncthreads();
 }
 __device__ inline bool f8_tile_list(const LinearF8Params& p, int tile, int* rows, int* tiles) {

@@ -18,11 +18,17 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kChannels = 16;
 
+// (Not for the non-coherent path: the kernel before may write these.)
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_again(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 
@@ -80,10 +86,10 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) small_kernel(const Linear
             a[u][3] = some ? ld_stream(w1 + k + 64) : zero;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                c[u][j][0] = some ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : zero;
-                c[u][j][1] = some ? __ldg(reinterpret_cast<const uint4*>(x[j] + k + 64)) : zero;
+                c[u][j][0] = some ? ld_again(x[j] + k) : zero;
+                c[u][j][1] = some ? ld_again(x[j] + k + 64) : zero;
             }
-            s[u] = some ? __ldg(ws + b) : 0.0f;
+            s[u] = some ? ws[b] : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
@@ -103,7 +109,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) small_kernel(const Linear
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const float s0 = __ldg(xs[j][0] + b) * s[u], s1 = __ldg(xs[j][1] + b) * s[u];
+                const float s0 = xs[j][0][b] * s[u], s1 = xs[j][1][b] * s[u];
                 sum[j][0] = fmaf(acc[j][0], s0, sum[j][0]);
                 sum[j][1] = fmaf(acc[j][1], s1, sum[j][1]);
                 sum[j][2] = fmaf(acc[j][2], s0, sum[j][2]);
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) small_kernel(const Linear
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += part[w][r][tt];
-        if (p.bias) v += __ldg(p.bias + n);
+        if (p.bias) v += p.bias[n];
         const int64_t o = static_cast<int64_t>(t) * p.N + n;
         if (p.addend) v += elem_to_f(static_cast<const T*>(p.addend)[o]);
         static_cast<T*>(p.out)[o] = elem_from_f<T>(v);

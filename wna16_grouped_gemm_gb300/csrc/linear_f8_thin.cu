@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
         const int r = tile.r0 + col, n = tile.nt * kM + channel;
         if (r >= tile.r1 || n >= p.N) return;
         const int64_t at = static_cast<int64_t>(r) * p.N + n;
-        if (p.bias) sum += __ldg(p.bias + n);
+        if (p.bias) sum += p.bias[n];
         if (p.addend) sum += elem_to_f(static_cast<const T*>(p.addend)[at]);
         static_cast<T*>(p.out)[at] = elem_from_f<T>(done ? sum : NAN);
     };

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // scales, two blocks ahead (past the ends: the last ones; what they scale is not stored)
             const float* xs = p.xs + static_cast<int64_t>(min(tile.r0 + row, p.T - 1)) * blocks;
             const float* ws = p.ws + (static_cast<int64_t>(tile.e) * L.n_blocks + min(tile.nt * kHalves + half, L.n_blocks - 1)) * blocks;
-            float x0 = __ldg(xs), w0 = __ldg(ws), x1 = __ldg(xs + min(1, blocks - 1)), w1 = __ldg(ws + min(1, blocks - 1));
+            float x0 = *xs, w0 = *ws, x1 = xs[min(1, blocks - 1)], w1 = ws[min(1, blocks - 1)];
             float acc[kCols];
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (c == 1) {
                             x0 = x1;
                             w0 = w1;
-                            x1 = __ldg(xs + min(kb + 2, blocks - 1));
-                            w1 = __ldg(ws + min(kb + 2, blocks - 1));
+                            x1 = xs[min(kb + 2, blocks - 1)];
+                            w1 = ws[min(kb + 2, blocks - 1)];
                         }
                     } else {   // all of it has been read
                         tc_fence_before();
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (p.bias) {
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) acc[j] += __ldg(p.bias + min(n0 + j, p.N - 1));
+                for (int j = 0; j < kCols; ++j) acc[j] += p.bias[min(n0 + j, p.N - 1)];
             }
             if (p.addend && mine) {
                 const T* add = static_cast<const T*>(p.addend) + static_cast<int64_t>(r) * p.N + n0;

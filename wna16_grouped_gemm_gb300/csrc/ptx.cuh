@@ -94,6 +94,9 @@ __device__ __forceinline__ bool elect_one(int* status) {
 
 // Wait until the grids this one depends on (same stream, launched with
 // programmatic serialisation) have completed and their writes are visible.
+// What they may have written is loaded by plain loads behind this: __ldg and
+// the like are for data that does not change during the kernel's life, and the
+// kernel's life began before.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Allow the next grid in the stream to start launching (its CTAs still wait

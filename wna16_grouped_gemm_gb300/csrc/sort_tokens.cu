@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortPar
         for (int e = tid; e < 1024; e += kSmallThreads) pos[e] = 0;
         __syncthreads();
         for (int f = tid; f < R; f += kSmallThreads) {
-            const unsigned e = __ldg(ids + f) - begin;
+            const unsigned e = ids[f] - begin;
             if (e < E) atomicAdd(&pos[e], 1);
         }
         __syncthreads();
@@ -107,12 +107,12 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortPar
         int n[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            e[q] = j0 + q < p.topk ? __ldg(ids + f + q) - begin : ~0u;
+            e[q] = j0 + q < p.topk ? ids[f + q] - begin : ~0u;
             n[q] = 0;
         }
 #pragma unroll 4
         for (int i = tid; i < R; i += kSmallThreads) {
-            const unsigned o = __ldg(ids + i) - begin;
+            const unsigned o = ids[i] - begin;
 #pragma unroll
             for (int q = 0; q < 8; ++q) n[q] += o < e[q] || (o == e[q] && i < f + q);
         }
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortPar
             int row = 0;
 #pragma unroll
             for (int w = 0; w < kSmallThreads / 32; ++w) row += part[w][tid];
-            if (__ldg(ids + f + tid) - begin >= E) row = -1;
+            if (ids[f + tid] - begin >= E) row = -1;
             pos[j0 + tid] = row;
             p.inv[f + tid] = row;
         }
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortP
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
             const int64_t f = at + i * 32 + lane;
-            e[i] = f < f1 ? __ldg(ids + f) - begin : ~0u;
+            e[i] = f < f1 ? ids[f] - begin : ~0u;
         }
     };
     // every slot's rank among its expert's, and the counts of the warp
@@ -289,12 +289,12 @@ __global__ void __launch_bounds__(32 * kCopyWarps, 6) sort_copy_kernel(const Sor
     const int32_t* inv = p.inv + t * p.topk;
     for (int j0 = 0; j0 < p.topk; j0 += 32) {
         const int count = min(32, p.topk - j0);
-        const int mine = lane < count ? __ldg(inv + j0 + lane) : -1;
+        const int mine = lane < count ? inv[j0 + lane] : -1;
         for (int64_t v0 = lane; v0 - lane < n_vec; v0 += 4 * 32) {   // the same turns for every lane
             V a[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                if (v0 + c * 32 < n_vec) a[c] = __ldg(src + v0 + c * 32);
+                if (v0 + c * 32 < n_vec) a[c] = src[v0 + c * 32];
             for (int j = 0; j < count; ++j) {
                 const int r = __shfl_sync(kAll, mine, j);
                 if (r < 0) continue;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps, 6) sort_copy_kernel(const Sor
         }
         if (p.x_scales)
             for (int64_t v = lane; v - lane < p.groups; v += 32) {
-                const float a = v < p.groups ? __ldg(p.x_scales + t * p.groups + v) : 0.0f;
+                const float a = v < p.groups ? p.x_scales[t * p.groups + v] : 0.0f;
                 for (int j = 0; j < count; ++j) {
                     const int r = __shfl_sync(kAll, mine, j);
                     if (r >= 0 && v < p.groups) p.row_scales[r * p.groups + v] = a;
@@ -452,9 +452,9 @@ __device__ __forceinline__ Slots load_slots(const UnsortParams& p, int64_t t, in
     Slots s;
     if (t < p.T && j0 + lane < p.topk) {
         const int64_t f = t * p.topk + j0 + lane;
-        const int r = __ldg(p.inv + f);
+        const int r = p.inv[f];
         s.row = r >= 0 && r < p.R ? r : -1;
-        if (p.weights) s.w = __ldg(p.weights + f);
+        if (p.weights) s.w = p.weights[f];
     }
     return s;
 }
