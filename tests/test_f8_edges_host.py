@@ -1,0 +1,20 @@
+"""Argument checks of the routed experts in 8-bit floats that test_f8_host.py does not reach (no GPU)."""
+from __future__ import annotations
+
+import pytest
+
+from tests.test_f8_host import E4, FP, I32, _More, lib  # noqa: F401  (lib: the fixture)
+from wna16_grouped_gemm_gb300 import f8
+
+
+def test_sort_refuses_outputs_that_nothing_fills(lib):  # noqa: F811
+    """Rows without x, scales without x and rows' scales without scales: refused, as the C ABI does, and not returned unwritten."""
+    T, k, E, K = 4, 2, 8, 256
+    ids, off, inv = _More(I32, T, k), _More(I32, E + 1), _More(I32, T, k)
+    x, xs, rows, rs = _More(E4, T, K), _More(FP, T, 2), _More(E4, T * k, K), _More(FP, T * k, 2)
+    for args, kw, message in (((None, ids, E), dict(rows=rows), "rows without x"),
+                              ((None, ids, E), dict(scales=xs, row_scales=rs), "scales without x"),
+                              ((None, ids, E), dict(row_scales=rs), "row_scales without scales"),
+                              ((x, ids, E), dict(rows=rows, row_scales=rs), "row_scales without scales")):
+        with pytest.raises(ValueError, match=message):
+            f8.sort_tokens(*args, offsets=off, inv=inv, **kw)

@@ -336,6 +336,13 @@ static PyObject* sort_tokens(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         PyErr_Format(PyExc_ValueError, "topk_ids [%lld, %lld] is too large", (long long)ids.n0, (long long)ids.n1);
         return NULL;
     }
+    static const struct { int out, in; const char* message; } kPairs[] = {
+        {6, 1, "rows without x"}, {2, 1, "scales without x"}, {7, 2, "row_scales without scales"}};
+    for (int i = 0; i < 3; ++i)
+        if (MAYBE(a[kPairs[i].out]) && !MAYBE(a[kPairs[i].in])) {
+            PyErr_SetString(PyExc_ValueError, kPairs[i].message);
+            return NULL;
+        }
     const int64_t R = ids.n0 * ids.n1;
     if (MAYBE(a[1]) && (take(a[1], "x", dev, NULL, FLOATS | CODES, ROWS, &x) || want_rows(&x, "x", ids.n0, x.n1) ||
                         take(a[6], "rows", dev, NULL, 1u << x.type, WHOLE, &rows) || want_rows(&rows, "rows", R, x.n1)))
