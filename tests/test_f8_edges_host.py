@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import pytest
 
-from tests.test_f8_host import E4, FP, I32, _More, lib  # noqa: F401  (lib: the fixture)
+from tests.test_f8_host import E4, FP, I32, INV, _grad, _More, lib  # noqa: F401  (lib: the fixture)
 from wna16_grouped_gemm_gb300 import f8
 
 
@@ -18,3 +18,11 @@ def test_sort_refuses_outputs_that_nothing_fills(lib):  # noqa: F811
                               ((x, ids, E), dict(rows=rows, row_scales=rs), "row_scales without scales")):
         with pytest.raises(ValueError, match=message):
             f8.sort_tokens(*args, offsets=off, inv=inv, **kw)
+
+
+def test_gradient_of_no_rows(lib):  # noqa: F811
+    """Without rows (R = 0) there is no dy to write; with y or dweights the other one is still wanted where there are rows."""
+    assert _grad(lib, R=0, y=None, w=None, dy=None, dw=None) == 0
+    assert _grad(lib, R=0, y=None, dy=None, dw=None) == 0
+    assert _grad(lib, R=1, y=None, dy=None, dw=None) == INV
+    assert _grad(lib, R=1, dw=None) == INV

@@ -37,3 +37,14 @@ def test_lists_of_a_cluster_are_the_same_every_time(moe, T, topk, total):  # noq
     torch.cuda.synchronize()
     for o, i in zip(offs, invs):
         assert np.array_equal(o.cpu().numpy(), off_ref) and np.array_equal(i.cpu().numpy(), inv_ref)
+
+
+def test_gradient_of_no_rows(moe):  # noqa: F811
+    """A share of the experts that got no slot, with buffers of no rows."""
+    inv = torch.full((5, 3), -1, dtype=I32, device="cuda")
+    d, none = randn(5, 64, dtype=BF), torch.empty(0, 64, dtype=BF, device="cuda")
+    dy, dw = moe.unsort_tokens_grad(d, inv, dy=none)
+    assert dy is none and dw is None
+    dy, dw = moe.unsort_tokens_grad(d, inv, none, torch.rand(5, 3, device="cuda"), dy=torch.empty_like(none))
+    assert dy.shape == (0, 64) and torch.equal(dw, torch.zeros(5, 3, device="cuda"))
+    assert torch.equal(moe.unsort_tokens(none, inv), torch.zeros_like(d))

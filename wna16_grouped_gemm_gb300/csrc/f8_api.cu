@@ -145,6 +145,7 @@ int wna16_moe_unsort_tokens_grad(const void* dout, const int32_t* inv, const voi
     if (int rc = check_slots(T, K, topk)) return rc;
     if (R < 0 || R >= (int64_t(1) << 31)) return set_error(WNA16_ERR_INVALID_ARG, "R=%lld must be in [0, 2^31)", (ll)R);
     if (T == 0) return WNA16_OK;
+    if (R == 0 && !dweights) return WNA16_OK;   // dy has no rows
     if (!dy && !dweights) return set_error(WNA16_ERR_INVALID_ARG, "dy and dweights are both NULL");
     const size_t es = size_of(type), slots = static_cast<size_t>(T) * topk;
     if (R > 0 && !y != !dweights) return set_error(WNA16_ERR_INVALID_ARG, "y and dweights go together");
