@@ -53,13 +53,19 @@ def test_a_cluster_has_started_before_its_shared_memory_is_reached(path):
         assert "cluster_sync()" in before or 0 <= split < before.find("cluster_wait()"), name
 
 
-#: the sources of the routed experts in 8-bit floats
-F8 = ["blocks_f8.cu", "linear_f8.cuh", "linear_f8_small.cu", "linear_f8_thin.cu", "linear_f8_wide.cu", "sort_tokens.cu"]
+def signature_of(s, name):
+    at = s.index("(", s.index(name + "("))
+    return s[at:s.index("{", at)]
 
 
-@pytest.mark.parametrize("name", F8)
-def test_inputs_are_loaded_coherently(name):
+@pytest.mark.parametrize("path", SOURCES + sorted(glob.glob(os.path.join(build.CSRC, "*.cuh"))), ids=os.path.basename)
+def test_inputs_are_loaded_coherently(path):
     """A kernel that starts before the one ahead of it ends (pdl_wait) reads what that one writes: such data changes
-    during the kernel's life, which the non-coherent path does not allow, and a compiler may move its loads ahead of the wait."""
-    code = code_of(os.path.join(build.CSRC, name))
-    assert "__ldg" not in code and ".nc." not in code and not re.search(r"const[\w\s:]*\*\s*__restrict__", code)
+    during the kernel's life, which the non-coherent path does not allow (__ldg, .nc, or a compiler's choice of them for a const
+    __restrict__ argument), and a compiler may move its loads ahead of the wait."""
+    code = code_of(path)
+    kernels = [name for name, body in bodies(code) if "pdl_wait()" in body]
+    if kernels or path.endswith(".cuh"):
+        assert "__ldg" not in code and ".nc." not in code
+    for name in kernels:
+        assert not re.search(r"const[\w\s:]*\*\s*__restrict__", signature_of(code, name)), name

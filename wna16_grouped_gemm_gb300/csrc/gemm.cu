@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(Roles<DW>::kThreads, 1)
                     const int grow = r < kRowsPerTile ? r0 + r : r1 + (r - kRowsPerTile);
                     if (!in_bounds(grow >= 0 && grow < p.n_weight_rows, status)) continue;
                     const uint16_t* src = p.scales + static_cast<int64_t>(grow) * ng + g0;
-                    for (int g = 0; g < ng_item; ++g) d16[r * ng_item + g] = __ldg(src + g);
+                    for (int g = 0; g < ng_item; ++g) d16[r * ng_item + g] = ld_u16(src + g);
                 }
                 mbar_arrive(&sfull[sb.idx]);
             }
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(Roles<DW>::kThreads, 1)
                         for (int i = 0; i < 8; ++i)
                             cs[i] = goff && i < tile.z &&
                                             in_bounds(tile.y + i < R_rows && split * ng_item + g < p.ngroups, status)
-                                        ? __ldg(crow + static_cast<int64_t>(g) * R_rows + i)
+                                        ? crow[static_cast<int64_t>(g) * R_rows + i]
                                         : 0.0f;
                         if (!mbar_wait(&gfull[gs.idx], gs.phase, abort_flag, status)) {
                             ok = false;

@@ -100,14 +100,6 @@ constexpr int kSmallWarps = 8;
 constexpr int kSmallRows = 16;
 constexpr int kExactSteps = 16;   // 64-k steps whose sums stay below 2^24 (1024 * 2^14)
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
@@ -149,7 +141,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, BLOCKS) small_kernel(const L
             const int k = k0 + u * kStep + q * 16;
             a[u] = k < K ? ld_stream(w0 + k) : zero;
             b[u] = k < K ? ld_stream(w1 + k) : zero;
-            c[u] = k < K ? __ldg(reinterpret_cast<const uint4*>(x[0] + k)) : zero;
+            c[u] = k < K ? *reinterpret_cast<const uint4*>(x[0] + k) : zero;
         }
         if (held + U > kExactSteps) {
 #pragma unroll
@@ -174,7 +166,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, BLOCKS) small_kernel(const L
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const uint4 xc = j == 0 ? c[u] : k < K ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : zero;
+                const uint4 xc = j == 0 ? c[u] : k < K ? *reinterpret_cast<const uint4*>(x[j] + k) : zero;
                 const uint32_t xw[4] = {xc.x, xc.y, xc.z, xc.w};
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
@@ -201,8 +193,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps, BLOCKS) small_kernel(const L
         int total = 0;
 #pragma unroll
         for (int w = 0; w < kSmallWarps; ++w) total += part[w][r][tt];
-        float v = static_cast<float>(total) * __ldg(p.xs + t) * __ldg(p.ws + n);
-        if (p.bias) v += __ldg(p.bias + n);
+        float v = static_cast<float>(total) * p.xs[t] * p.ws[n];
+        if (p.bias) v += p.bias[n];
         const int64_t o = static_cast<int64_t>(t) * p.N + n;
         if (p.addend) v += to_f(static_cast<const T*>(p.addend)[o]);
         static_cast<T*>(p.out)[o] = from_f<T>(v);
@@ -506,7 +498,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (SMALL_B && first < items) {   // (one item: the scales are not in its way then)
                 const float* scale = TM ? p.ws : p.xs;
                 const int i = static_cast<int>(threadIdx.x) - 32 * kFirstEpilogue;
-                if (i < nt) sScale[i] = __ldg(scale + min(b_row(first) + i, (TM ? p.N : p.T) - 1));
+                if (i < nt) sScale[i] = scale[min(b_row(first) + i, (TM ? p.N : p.T) - 1)];
             }
             const bool live = row < static_cast<uint32_t>(brows);   // a tile of fewer rows leaves threads without one
             const uint32_t r = live ? row : 0;
@@ -555,7 +547,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (p.bias) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] += TM ? __ldg(p.bias + b + (i < count ? i : 0)) : a_bias;
+            for (int i = 0; i < 16; ++i) r[i] += TM ? p.bias[b + (i < count ? i : 0)] : a_bias;
         }
         const int64_t at = TM ? static_cast<int64_t>(a) * p.N + b : static_cast<int64_t>(b) * p.N + a;
         const int64_t step = TM ? 1 : p.N;
@@ -603,11 +595,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t it = 0;
         for (int v = first; v < items; v += stride, ++it) {
             const int b0 = b_row(v), a = a_row(v) + row;
-            const float as = a < a_len ? __ldg(a_scale + a) : 0.0f;
-            const float bias = !TM && a < a_len && p.bias ? __ldg(p.bias + a) : 0.0f;
+            const float as = a < a_len ? a_scale[a] : 0.0f;
+            const float bias = !TM && a < a_len && p.bias ? p.bias[a] : 0.0f;
             if (it > 0) named_barrier(1, 32 * kEpilogues);   // the last tile's scales have been read
             if (!SMALL_B)
-                for (int i = thread; i < nt; i += 32 * kEpilogues) sScale[i] = __ldg(b_scale + min(b0 + i, b_len - 1));
+                for (int i = thread; i < nt; i += 32 * kEpilogues) sScale[i] = b_scale[min(b0 + i, b_len - 1)];
             // one warp polls; the others wait in a barrier, which costs the converters no issue slots
             if (warp == kFirstEpilogue) {
                 done = done && mbar_wait_bounded(accfull, it & 1u, abort_flag, status, true);
@@ -654,8 +646,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         cluster_sync();
         if (warp >= kFirstEpilogue) {
             const int a = a_row(v) + row;
-            const float as = a < a_len ? __ldg(a_scale + a) : 0.0f;
-            const float bias = !TM && a < a_len && p.bias ? __ldg(p.bias + a) : 0.0f;
+            const float as = a < a_len ? a_scale[a] : 0.0f;
+            const float bias = !TM && a < a_len && p.bias ? p.bias[a] : 0.0f;
             const int mine = min(share, nt - split * share);
             for (int j = eset * 16; j < mine; j += 32) {
                 float x[16], s[16];

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
 #pragma unroll
             for (int i = 0; i < PL; i += 4) {
                 float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                if (L.has(i)) v = __ldg(reinterpret_cast<const float4*>(row + i * L.per_group));
+                if (L.has(i)) v = *reinterpret_cast<const float4*>(row + i * L.per_group);
                 z[i] = v.x;
                 z[i + 1] = v.y;
                 z[i + 2] = v.z;
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
 #pragma unroll
             for (int i = 0; i < PL; i += 4) {
                 uint2 v = make_uint2(none, none);
-                if (L.has(i)) v = __ldg(reinterpret_cast<const uint2*>(row + i * L.per_group));
+                if (L.has(i)) v = *reinterpret_cast<const uint2*>(row + i * L.per_group);
                 const uint32_t h[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
         for (int i = 0; i < PL; i += 4) {
             if (p.bias_vec) {
                 if (L.has(i)) {
-                    const float4 v = __ldg(reinterpret_cast<const float4*>(src + i * L.per_group));
+                    const float4 v = *reinterpret_cast<const float4*>(src + i * L.per_group);
                     bias[i] = v.x;
                     bias[i + 1] = v.y;
                     bias[i + 2] = v.z;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(32 * kWarps, PL <= 8 ? 8 : 1) route_scored_ker
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (L.has(i + j)) bias[i + j] = __ldg(src + i * L.per_group + j);
+                    if (L.has(i + j)) bias[i + j] = src[i * L.per_group + j];
             }
         }
     }

@@ -472,7 +472,7 @@ __device__ __forceinline__ void values8(uint32_t lo, uint32_t hi, float scale, i
 constexpr int kDequant = 16;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
-    dequantize_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scales, int K, int q_type, int group_log,
+    dequantize_kernel(const uint8_t* q, const float* scales, int K, int q_type, int group_log,
                       T* __restrict__ out) {
     pdl_wait();
     pdl_trigger();
@@ -480,11 +480,11 @@ __global__ void __launch_bounds__(256)
     const int k = (blockIdx.y * blockDim.x + threadIdx.x) * kDequant;
     if (k >= K) return;
     // (a group is a multiple of 16)
-    const float s = __ldg(scales + (group_log ? t * (K >> group_log) + (k >> group_log) : t));
+    const float s = scales[group_log ? t * (K >> group_log) + (k >> group_log) : t];
     const uint8_t* src = q + t * K + k;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if (VEC) {
-        const uint4 c = __ldg(reinterpret_cast<const uint4*>(src));
+        const uint4 c = *reinterpret_cast<const uint4*>(src);
         w[0] = c.x;
         w[1] = c.y;
         w[2] = c.z;
