@@ -69,3 +69,18 @@ def test_inputs_are_loaded_coherently(path):
         assert "__ldg" not in code and ".nc." not in code
     for name in kernels:
         assert not re.search(r"const[\w\s:]*\*\s*__restrict__", signature_of(code, name)), name
+
+
+@pytest.mark.parametrize("name,least", [("sort_tokens.cu", 6), ("linear_f8.cuh", 3), ("linear_f8_thin.cu", 1), ("linear_f8_wide.cu", 1),
+                                        ("gemm.cu", 10), ("kernels.cu", 6)])
+def test_indices_from_device_data_are_checked_in_the_bounds_checked_build(name, least):
+    code = code_of(os.path.join(build.CSRC, name))
+    assert len(re.findall(r"\b(?:row_)?in_bounds\(", code)) >= least
+
+
+def test_only_the_bounds_checked_build_has_the_checks_word():
+    from wna16_grouped_gemm_gb300 import binding
+    build.build()
+    build.build(debug=True)
+    assert hasattr(binding.load_debug_library(), "wna16_moe_debug_index_status")
+    assert not hasattr(binding.load_library(), "wna16_moe_debug_index_status")

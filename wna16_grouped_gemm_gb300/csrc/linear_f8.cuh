@@ -158,14 +158,18 @@ __device__ inline bool f8_tile_list(const LinearF8Params& p, int tile, int* rows
 struct F8Tile {
     int e = 0;
     int r0 = 0, r1 = 0, nt = 0;
-    // the tile of item v (items of a walk come in ascending order)
-    __device__ __forceinline__ void locate(int v, int n_tiles, int tile, const int* rows, const int* tiles) {
+    // the tile of item v (items of a walk come in ascending order); the bounds-checked build takes the first expert's first
+    // one where the lists lead outside the buffers
+    __device__ __forceinline__ void locate(int v, int n_tiles, int tile, const int* rows, const int* tiles,
+                                           const LinearF8Params& p, int* status) {
         const int q = v / n_tiles;
-        while (tiles[e + 1] <= q) ++e;
+        while (in_bounds(e < p.E, status) && tiles[e + 1] <= q) ++e;
+        if (!in_bounds(e < p.E, status)) e = 0;
         const int count = tiles[e + 1] - tiles[e], local = v - tiles[e] * n_tiles;
         nt = local / count;
         r0 = rows[e] + (local - nt * count) * tile;
         r1 = rows[e + 1];
+        if (!in_bounds(nt >= 0 && nt < n_tiles && r0 >= 0 && r0 < r1 && r1 <= p.T, status)) nt = r0 = r1 = 0;
     }
 };
 

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
     const int quarter = warp & 3, channel = quarter * 32 + lane, col0 = (warp - kFirstEpilogue) / 4 * kCols;
     auto store = [&](int col, float sum) {
         const int r = tile.r0 + col, n = tile.nt * kM + channel;
-        if (r >= tile.r1 || n >= p.N) return;
+        if (r >= tile.r1 || n >= p.N || !in_bounds(r >= 0 && r < p.T, status)) return;
         const int64_t at = static_cast<int64_t>(r) * p.N + n;
         if (p.bias) sum += p.bias[n];
         if (p.addend) sum += elem_to_f(static_cast<const T*>(p.addend)[at]);
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
             uint32_t issued = 0;
             bool ok = true, is_free = false;
             for (int v = first; v < items && ok; v += stride) {
-                tile.locate(v, L.n_tiles, NT, rows, tiles);
+                tile.locate(v, L.n_tiles, NT, rows, tiles, p, status);
                 // weights that no other tile reads need not stay in L2
                 const uint64_t pol = tiles[tile.e + 1] - tiles[tile.e] > 1 ? again : first_use;
                 for (int kb = kb0; kb < kb1; ++kb, ++issued) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
         RingSlot sl;
         bool ok = true;
         for (int v = first; v < items && ok; v += stride) {
-            tile.locate(v, L.n_tiles, NT, rows, tiles);
+            tile.locate(v, L.n_tiles, NT, rows, tiles, p, status);
             const float* ws = p.ws + (static_cast<int64_t>(tile.e) * L.n_blocks + tile.nt) * L.blocks;
             for (int kb = kb0; kb < kb1; ++kb, sl.next(kScaleSlots)) {
                 if (!warp_wait_all(&sempty[sl.i], sl.phase ^ 1u, abort_flag, status)) {
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Thin<NT>::kThreads, 1)
         uint32_t at = 0;
         int held = 0;
         for (int v = first; v < items; v += stride) {
-            tile.locate(v, L.n_tiles, NT, rows, tiles);
+            tile.locate(v, L.n_tiles, NT, rows, tiles, p, status);
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
             for (int kb = kb0; kb < kb1; kb += kBatch) {

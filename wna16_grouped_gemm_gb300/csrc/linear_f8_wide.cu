@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t issued = 0;
                 bool ok = true;
                 for (int v = first; v < items && ok; v += stride) {
-                    tile.locate(v, L.n_tiles, kRows, rows, tiles);
+                    tile.locate(v, L.n_tiles, kRows, rows, tiles, p, status);
                     // a tile of few rows has a lower box (what lies in the others' place goes to sums that are not stored)
                     const bool low = tile.r1 - tile.r0 <= kLowRows;
                     const uint32_t bytes = ((low ? kLowRows : kRows) + kTile) * kScaleBlock;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool done = true;   // false: a wait gave up; what is missing is written as NaN
         RingSlot buf;
         for (int v = first; v < items; v += stride) {
-            tile.locate(v, L.n_tiles, kRows, rows, tiles);
+            tile.locate(v, L.n_tiles, kRows, rows, tiles, p, status);
             // scales, two blocks ahead (past the ends: the last ones; what they scale is not stored)
             const float* xs = p.xs + static_cast<int64_t>(min(tile.r0 + row, p.T - 1)) * blocks;
             const float* ws = p.ws + (static_cast<int64_t>(tile.e) * L.n_blocks + min(tile.nt * kHalves + half, L.n_blocks - 1)) * blocks;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = tile.r0 + row, n0 = tile.nt * kTile + half * kCols;
             T* out = static_cast<T*>(p.out) + static_cast<int64_t>(r) * p.N + n0;
             const int box_r = r - lane, cols = p.N - n0;   // columns that exist
-            const bool mine = r < tile.r1;
+            const bool mine = r < tile.r1 && in_bounds(r >= 0 && r < p.T, status);
             // What is not always there stands apart: this code runs once per tile, and fetching it is what it costs
             // (with the tests beside every value a tile's end took 20000 cycles).
             if (!done) {

@@ -26,6 +26,18 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
+// The status word of the index checks here (the bounds-checked build; these operators have no workspace).
+#ifdef WNA16_DEBUG
+__device__ int g_index_status;
+__device__ __forceinline__ int* index_status() { return &g_index_status; }
+#else
+__device__ __forceinline__ constexpr int* index_status() { return nullptr; }
+#endif
+// A row of R, which the bounds-checked build leaves out if it is none.
+__device__ __forceinline__ int row_in_bounds(int row, int64_t R) {
+    return in_bounds(row >= 0 && row < R, index_status()) ? row : -1;
+}
+
 // ------------------------------------------------------------------ sort
 
 constexpr int kSmallThreads = 256;
@@ -123,7 +135,7 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortPar
             int row = 0;
 #pragma unroll
             for (int w = 0; w < kSmallThreads / 32; ++w) row += part[w][tid];
-            if (ids[f + tid] - begin >= E) row = -1;
+            row = ids[f + tid] - begin >= E ? -1 : row_in_bounds(row, R);
             pos[j0 + tid] = row;
             p.inv[f + tid] = row;
         }
@@ -250,7 +262,7 @@ __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortP
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
             const int64_t f = f0 + i * 32 + lane;
-            if (f < f1) p.inv[f] = e[i] != ~0u ? base[e[i]] + my[e[i]] + at_rank[i] : -1;
+            if (f < f1) p.inv[f] = e[i] != ~0u ? row_in_bounds(base[e[i]] + my[e[i]] + at_rank[i], R) : -1;
         }
         return;
     }
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kListThreads, 1) sort_lists_kernel(const SortP
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
             const int64_t f = at + i * 32 + lane;
-            if (f < f1) p.inv[f] = e[i] != ~0u ? base[e[i]] + at_rank[i] : -1;
+            if (f < f1) p.inv[f] = e[i] != ~0u ? row_in_bounds(base[e[i]] + at_rank[i], R) : -1;
         }
     }
 }
@@ -297,7 +309,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps, 6) sort_copy_kernel(const Sor
                 if (v0 + c * 32 < n_vec) a[c] = src[v0 + c * 32];
             for (int j = 0; j < count; ++j) {
                 const int r = __shfl_sync(kAll, mine, j);
-                if (r < 0) continue;
+                if (r < 0 || row_in_bounds(r, p.T * p.topk) < 0) continue;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     if (v0 + c * 32 < n_vec) dst[r * n_vec + v0 + c * 32] = a[c];
@@ -308,7 +320,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps, 6) sort_copy_kernel(const Sor
                 const float a = v < p.groups ? p.x_scales[t * p.groups + v] : 0.0f;
                 for (int j = 0; j < count; ++j) {
                     const int r = __shfl_sync(kAll, mine, j);
-                    if (r >= 0 && v < p.groups) p.row_scales[r * p.groups + v] = a;
+                    if (r >= 0 && v < p.groups && row_in_bounds(r, p.T * p.topk) >= 0) p.row_scales[r * p.groups + v] = a;
                 }
             }
     }
@@ -513,7 +525,7 @@ __global__ void __launch_bounds__(kBackThreads, RUNS == 4 ? kGradBlocks : kBackB
         }
 #pragma unroll
         for (int q = 0; q < RUNS; ++q) {
-            if (n <= q * width) break;
+            if (n <= q * width || !in_bounds(now < p.T, index_status())) break;
             const int64_t at = now * p.K + k + q * width;
             if (p.addend) {
                 float a[kV<T>];
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(kBackThreads, kGradBlocks) unsort_grad_kernel(
 #pragma unroll
                         for (int i = 0; i < kSlots; ++i) {
                             const float w = __shfl_sync(kAll, s.w, (j0 + i) & 31);
-                            if (mine && row[i] >= 0) {
+                            if (mine && row[i] >= 0 && in_bounds(row[i] < p.R, index_status())) {
                                 float o[kV<T>];
 #pragma unroll
                                 for (int e = 0; e < kV<T>; ++e) o[e] = w * d[e];
@@ -656,6 +668,18 @@ cudaError_t launch_back_grad(const UnsortParams& p, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+#ifdef WNA16_DEBUG
+// The bounds-checked build only: what the index checks of these operators have recorded (0, or WNA16_ERR_INDEX), after
+// all work on the device; cleared.  Returns a CUDA error code.
+extern "C" __attribute__((visibility("default"))) int wna16_moe_debug_index_status(int* status) {
+    cudaError_t e = cudaDeviceSynchronize();
+    const int clear = 0;
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(status, g_index_status, sizeof(int));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_index_status, &clear, sizeof(int));
+    return e;
+}
+#endif
 
 cudaError_t launch_sort_tokens(const SortParams& p, cudaStream_t s) {
     // the widest accesses that every row allows
