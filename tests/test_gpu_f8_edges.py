@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_f8 import BF, E4, FP, I32, check_sort, lists_ref, make_ids, moe, rows_f8  # noqa: F401  (moe: the fixture)
-from tests.test_gpu_block import randn
+from tests.test_gpu_f8 import (BF, E4, FP, I32, check_sort, lists_ref, make_ids, moe, product_ref,  # noqa: F401  (moe: the fixture)
+                               product_tol, rows_f8)
+from tests.test_gpu_block import U, check, half_step, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +123,78 @@ def test_bounds_checked_products(moe, checked, counts, K, N, dt):  # noqa: F811
         assert moe.read_status(work) == moe.OK
         outs.append(out)
     assert status() == 0 and torch.equal(*outs)
+
+
+@pytest.mark.parametrize("R,mine,before", [
+    (24, 11, (0, 1, 5, 8, 13)),                    # a mean of 4: tiles of 16 rows
+    (60, 37, (0, 3, 16, 21, 23)),                  # of 10: 32 rows
+    (200, 140, (0, 1, 31, 32, 47, 60)),            # of 33: 64 rows
+    (600, 300, (0, 1, 33, 64, 127, 129, 300)),     # of 100: 128 rows
+])
+@pytest.mark.parametrize("K,N", [(1024, 300), (640, 264)])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_a_row_does_not_depend_on_its_neighbours(moe, R, mine, before, K, N, dt):  # noqa: F811
+    """An expert's rows, moved to other places of the tiles among other experts' rows, some of them NaN in codes, scales and weights:
+    the same bits (the numbers of rows and experts, which choose the kernel, stay).  And they are those of one weight's product."""
+    E, e = 6, 3
+    xq, xs = rows_f8(mine, K, 5)
+    wq = rows_f8(E * N, K, 6)[0].view(E, N, K)
+    ws = torch.exp(randn(E * -(-N // 128), K // 128, seed=7)).view(E, -1, K // 128) * 0.001
+    bad_w = torch.full_like(wq.view(torch.uint8), 0x7f).view(E4)
+    bad_w[e] = wq[e]
+    first = None
+    for at in before:
+        for poison in (False, True):
+            q, s = rows_f8(R, K, at)
+            if poison:
+                q = torch.full_like(q.view(torch.uint8), 0x7f).view(E4)
+                s = torch.full_like(s, float("nan"))
+            q[at:at + mine], s[at:at + mine] = xq, xs
+            behind = R - at - mine
+            counts = [at // 2, 0, at - at // 2, mine, behind // 3, behind - behind // 3]
+            offsets = torch.tensor([0, *np.cumsum(counts)], dtype=I32, device="cuda")
+            out = moe.grouped_linear_f8(q, s, bad_w if poison else wq, ws, offsets, dtype=dt)
+            got = out[at:at + mine]
+            assert bool(got.isfinite().all())
+            others = torch.cat([out[:at], out[at + mine:]])
+            assert bool(others.isnan().all() if poison else others.isfinite().all())
+            first = got.clone() if first is None else first
+            assert torch.equal(got, first), (at, poison)
+    ref, S = product_ref(xq, xs, wq[e], ws[e])
+    check(first, ref, half_step(dt) + U, "experts", extra=product_tol(K, S))
+    h = half_step(dt) + U      # both are within h |ref| + tol of ref, and |ref| within (|other| + tol) / (1 - h)
+    check(first, moe.linear_f8(xq, xs, wq[e], ws[e], dtype=dt).double(), 2 * h * (1 + 2 * h), "one weight", extra=2 * (1 + 2 * h) * product_tol(K, S))
+
+
+def test_products_that_overlap_share_nothing(moe):  # noqa: F811
+    """Products of several kernels and plans (two of them with a K shared over clusters, none with a workspace), queued on four
+    streams from graphs, so that they run at the same time: each gives what it gives alone."""
+    calls = [(64, 4096, 2048), (100, 8192, 256), (4, 4096, 4096), (700, 2048, 1024), (30, 16384, 128), (300, 1024, 520)]
+    streams, graphs, inputs = [torch.cuda.Stream() for _ in range(4)], [], []
+    for i, s in enumerate(streams):
+        mine = []
+        for T, K, N in calls[i:] + calls[:i]:
+            xq, xs = rows_f8(T, K, T)
+            wq, ws = rows_f8(N, K, T + 1)[0], torch.exp(randn(-(-N // 128), K // 128, seed=T + 2)) * 0.001
+            mine.append((xq, xs, wq, ws, torch.zeros(T, N, device="cuda"), moe.linear_f8(xq, xs, wq, ws, dtype=FP)))
+        inputs.append(mine)
+    torch.cuda.synchronize()
+    for s, mine in zip(streams, inputs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(4):
+                for xq, xs, wq, ws, out, _ in mine:
+                    moe.linear_f8(xq, xs, wq, ws, out=out)
+        graphs.append(g)
+    for _ in range(8):
+        for mine in inputs:
+            for c in mine:
+                c[4].fill_(-1.0)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for mine in inputs:
+            for c in mine:
+                assert torch.equal(c[4], c[5]), tuple(c[0].shape)
