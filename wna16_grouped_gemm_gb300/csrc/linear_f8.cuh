@@ -89,14 +89,15 @@ __device__ __forceinline__ bool warp_wait_inline(uint64_t* bar, uint32_t parity,
     return __all_sync(0xffffffffu, wait_inline(smem_u32(bar), parity, abort, status));
 }
 
-// The list of tiles: rows[e] is the first row of expert e (rows[E] the end), tiles[e] the number
-// of tiles of `tile` rows before it.  Written by one warp, from the offsets (which the block has
-// loaded into rows) held to [their predecessor, T]; returns whether one had to be.
+// The offsets into rows [E + 1], by the whole block; a barrier of the block is behind them.
 __device__ __forceinline__ void f8_load_offsets(const LinearF8Params& p, int* rows) {
     if (!p.offsets) return;
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) rows[i] = p.offsets[i];
     __syncthreads();
 }
+// The list of tiles: rows[e] is the first row of expert e (rows[E] the end), tiles[e] the number
+// of tiles of `tile` rows before it.  Written by one warp, from the offsets (which the block has
+// loaded into rows) held to [their predecessor, T]; returns whether one had to be.
 __device__ inline bool f8_tile_list(const LinearF8Params& p, int tile, int* rows, int* tiles) {
     const int lane = threadIdx.x & 31;
     if (!p.offsets) {
