@@ -26,3 +26,9 @@ def test_gradient_of_no_rows(lib):  # noqa: F811
     assert _grad(lib, R=0, y=None, dy=None, dw=None) == 0
     assert _grad(lib, R=1, y=None, dy=None, dw=None) == INV
     assert _grad(lib, R=1, dw=None) == INV
+
+
+def test_gradient_of_nothing_is_refused(lib):  # noqa: F811
+    d, inv = _More(FP, 4, 256), _More(I32, 4, 2)
+    with pytest.raises(ValueError, match="neither dy nor y"):
+        f8.unsort_tokens_grad(d, inv, want_dy=False)

@@ -397,6 +397,10 @@ static PyObject* unsort_tokens_grad(PyObject* self, PyObject* const* a, Py_ssize
         take_slots(a[2], a[4], dev, d.n0, &inv, &w))
         return NULL;
     const unsigned same = 1u << d.type;
+    if (!MAYBE(a[5]) && !MAYBE(a[6]) && d.n0 > 0) {   /* (R is not known without them) */
+        PyErr_SetString(PyExc_ValueError, "neither dy nor y: no gradient is wanted");
+        return NULL;
+    }
     if (MAYBE(a[3]) && (take(a[3], "y", dev, NULL, same, WHOLE, &y) || want_rows(&y, "y", y.n0, d.n1))) return NULL;
     if (MAYBE(a[5]) && (take(a[5], "dy", dev, NULL, same, WHOLE, &dy) ||
                         want_rows(&dy, "dy", MAYBE(a[3]) ? y.n0 : dy.n0, d.n1)))
