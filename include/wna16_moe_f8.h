@@ -101,7 +101,8 @@ WNA16_API int wna16_moe_grouped_linear_f8(const void* xq, const float* x_scales,
  *   m = max |w|,  scale = m / 448,  code = e4m3(w * (448 / m)),  value = code * scale
  * with the rules of wna16_moe_block.h for m below 2^-100 and for values that are not finite.
  *   w of `type`; element (e, n, k) at e * stride_e + n * stride_n + k * stride_k, where
- *     stride_k is 1, or stride_n is 1 (a transposed weight)
+ *     stride_k is 1 and stride_n at least K, or stride_n is 1 (a transposed weight) and stride_k at least N;
+ *     stride_e at least a weight's extent, (N - 1) * stride_n + (K - 1) * stride_k + 1 (E > 1)
  *   q e4m3 [E, N, K], scales fp32 [E, ceil(N / 128), K / 128], contiguous
  * K a multiple of 128.  */
 WNA16_API int wna16_moe_quantize_blocks_f8(const void* w, int64_t E, int64_t N, int64_t K, int64_t stride_e,

@@ -4,8 +4,9 @@
 // Bound by the bytes of the weights, read once.  A thread block has one block of
 // the weight in registers from its reads to the codes (four of them per SM with 16-bit values, three with fp32; with three, 16 x
 // 4096 x 4096 bf16 126 us and transposed 134; with five fp16 135 and 150).
-// Measured (us), 16 x 4096 x 4096: fp32 183 (7.3 TB/s), transposed 186; bf16 120 (6.7), transposed 121; fp16 121, 126.  1000 x
-// 2048 bf16 2.6, transposed 2.9.
+// Measured (us), 16 x 4096 x 4096: fp32 184 (7.3 TB/s), transposed 188; bf16 120 (6.7), transposed 122; fp16 122, 127.  1000 x
+// 2048 bf16 2.5, transposed 2.8.  With four blocks per SM the fp16 kernels spill 48 to 96 bytes per thread, bf16 transposed off 16-byte
+// boundaries 60.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -71,10 +71,14 @@ Plan plan_one_weight(const LinearF8Params& p, int sms) {
 }
 
 // With a weight per expert the rows of each are known on the device only; the mean decides.  Measured (us, 256 experts of
-// 4096 x 4096, rows at random; thin with 16, 32, 64 rows per tile / wide; the weights alone take 632):
+// 4096 x 4096, rows at random; thin with 16, 32, 64 rows per tile / wide; the weights alone take 632 at the measured copy
+// bandwidth, and are read faster where nothing is written):
 //   mean 2   516 517 533 / 545      mean 16  715 623 623 / 702      mean 48  1640 1178 667 / 725
 //   mean 8   607 608 613 / 650      mean 32  1179 862 654 / 696     mean 64  2095 1325 942 / 722
-// (with skewed popularity, mean 8: 643 588 580 / 577, mean 16: 851 718 673 / 660, mean 32: 1250 935 784 / 705)
+// (with skewed popularity, mean 8: 643 588 580 / 577, mean 16: 851 718 673 / 660, mean 32: 1250 935 784 / 705: wide tiles lose
+// less there than thin ones gain in the first table, so they begin below its crossing.)  Other sizes and fewer experts, whose tiles
+// may not fill the SMs, follow the same rule and have not been measured for it; with `expert_begin` the mean counts the slots of
+// other experts too.
 Plan plan_experts(const LinearF8Params& p, int sms) {
     Plan best;
     const double mean = static_cast<double>(p.T) / p.E;

@@ -11,12 +11,15 @@
 // warps take registers from the others (setmaxnreg).
 //
 // Bound by what an SM gets from L2: a stage is 48 KB, at 64 bytes a cycle 770 cycles, of 835 that it takes (the tensor cores
-// need 512, the multiply-adds 256 issue slots).  Measured (us, 8192 x 4096 x 4096): 114 by itself (2.4 PFLOP/s), 125 among
-// other calls (with the issuers' waits and elections by whole warps 117; then 109 without the multiply-adds or with a quarter
+// need 512, the multiply-adds 256 issue slots).  Measured (us, 8192 x 4096 x 4096): 114 by itself (2.4 PFLOP/s, 0.64 of twice the
+// measured bf16 rate: an 8-bit product has twice the rate of a 16-bit one), 125 to 128 among other calls (with the issuers' waits and elections by whole warps 117; then 109 without the multiply-adds or with a quarter
 // of the products, 102 with neither).  8192 x 2048 x 4096 64, 1024 x 4096 x 4096 19 (one tile per SM).  256 experts of
-// 4096 x 4096, 65536 rows with skewed popularity: 1380 to 1500 (1.6 PFLOP/s: 640 tiles of 128 rows for 512 that would be full).
-// Tried and not kept: pairs of CTAs (cta_group::2; 32 KB per stage and CTA) 116, but tiles of 256 rows make that 1790 for the
-// experts; two blocks per SM with 128 x 128 tiles 147; 16 epilogue warps of 64 channels 128; packed multiply-adds
+// 4096 x 4096, 65536 rows with skewed popularity: 1330 to 1520 (640 tiles of 128 rows for 512 that would be full, 10240 with their
+// channels: at the time per tile of the line above 1100; the rest is boxes of rows that another expert follows, stored value by value,
+// and weights read again, and is not told apart).  Channels whose rows are not of 16 bytes are stored so throughout: 8192 x 4096 x 4097 384.
+// Lists of more than 356 experts leave room for three stages: 64 rows each of 2048 x 1024, per expert 0.597 us, 0.589 with four.
+// Tried and not kept: pairs of CTAs (cta_group::2; 32 KB per stage and CTA) 116, by what is not known, and tiles of 256 rows make that
+// 1790 for the experts; two blocks per SM with 128 x 128 tiles 147; 16 epilogue warps of 64 channels 128; packed multiply-adds
 // (fma.rn.f32x2) 140; stages of weights sent to L2 four to 32 blocks ahead 137, experts 1600 to 2170; three stages and twice
 // the room for results 124; results stored without TMA 147.  (All beside 118.)
 #include <algorithm>

@@ -7,9 +7,11 @@
 //
 // Bound by the bytes of the rows.  Sums are fp32, in an order that the sizes alone fix.
 // Measured (us; 8 slots per token on 256 experts, rows of 4096 bf16; of a measured copy's 6793 GB/s):
-//   8192 tokens   lists 8.8, lists and rows 106 (0.84 of it; the copies alone 0.91), back 99 (0.90), gradient 173 (0.97)
-//   4 tokens      3.0, 2.1, 3.9 (a launch); 1024 tokens: 17.5, 16, 25
-//   8192 tokens   fp32 202, 171, 335; e4m3 56; rows of 4100 bf16 (4-byte accesses) 122, 116, 212; of 4097 203, 244, 443
+//   8192 tokens   lists 8.9, lists and rows 106 (0.84 of it; the copies alone 0.91), back 90 (0.98), gradient 173 (0.97)
+//   4 tokens      3.2, 2.1, 4.1 (a launch); 1024 tokens: 17.7, 14.7, 25
+//   8192 tokens   fp32 202, 171, 338; e4m3 58; rows of 4100 bf16 (4-byte accesses) 122, 121, 212; of 4097 205, 232, 443
+// The gradient of a few thousand tokens is further from it, since a block's items are whole tokens: 2047 of them with about half of
+// their 8 slots in use 31 to 33 us, of 22 that the bytes take (608 blocks, 3.4 turns of unequal length).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

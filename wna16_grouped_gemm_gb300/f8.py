@@ -11,6 +11,10 @@
 As in ``block``: argument checks and marshalling only, CUDA tensors, the current stream (or
 ``stream``), outputs allocated unless they are passed in.  8-bit rows (q, scales) are those of
 ``quantize_q8``, ``add_rmsnorm_q8`` and ``swiglu_q8`` with float8_e4m3fn and groups of 128.
+
+Nothing here takes part in autograd: outputs carry no graph, whatever the inputs require.  A program that trains
+calls the gradients itself: unsort_tokens without weights for sort_tokens, unsort_tokens_grad for unsort_tokens, the
+products with transposed weights for theirs with respect to the rows.
 """
 from __future__ import annotations
 
@@ -156,7 +160,8 @@ def grouped_linear_f8(xq, x_scales, wq, w_scales, offsets, *, dtype=torch.bfloat
 
 def quantize_blocks_f8(w, *, q=None, scales=None, stream=None):
     """(q, scales) of a weight [N, K] or of weights [E, N, K] (bf16, fp16 or fp32; rows or columns contiguous)
-    in e4m3 with a scale per block of 128 x 128: q of w's shape, scales fp32 [(E,) ceil(N / 128), K / 128]."""
+    in e4m3 with a scale per block of 128 x 128: q of w's shape, scales fp32 [(E,) ceil(N / 128), K / 128].
+    Weights, and the rows or columns of one, lie behind one another, with or without gaps; interleaved ones are refused."""
     entry = (_entries or _load())["quantize_blocks_f8"]
     if q is None or scales is None:
         if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
@@ -177,7 +182,8 @@ def forward_f8(xq, x_scales, topk_ids, topk_weights, w13, w13_scales, w2, w2_sca
 
     xq float8_e4m3fn [T, K], x_scales fp32 [T, K / 128]; w13 [E, 2N, K] (gate rows, then up rows) and w2
     [E, K, N] as for grouped_linear_f8.  The experts of the weights are [expert_begin, expert_begin + E); slots of
-    others add nothing.  The products are rounded to `dtype`, the SwiGLU's rows to e4m3 in groups of 128."""
+    others add nothing.  The products are rounded to `dtype`, the SwiGLU's rows to e4m3 in groups of 128.
+    Buffers are of T * topk rows, and the SwiGLU works on all of them, also where most slots are of other experts."""
     if not isinstance(w13, torch.Tensor) or w13.dim() != 3:
         raise ValueError("w13 must be a [E, 2N, K] tensor")
     rows, row_scales, offsets, inv = sort_tokens(xq, topk_ids, w13.shape[0], scales=x_scales, expert_begin=expert_begin,
