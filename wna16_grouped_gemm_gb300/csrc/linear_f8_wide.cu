@@ -12,7 +12,8 @@
 //
 // Bound by what an SM gets from L2: a stage is 48 KB, at 64 bytes a cycle 770 cycles, of 835 that it takes (the tensor cores
 // need 512, the multiply-adds 256 issue slots).  Measured (us, 8192 x 4096 x 4096): 114 by itself (2.4 PFLOP/s, 0.64 of twice the
-// measured bf16 rate: an 8-bit product has twice the rate of a 16-bit one), 125 to 128 among other calls (with the issuers' waits and elections by whole warps 117; then 109 without the multiply-adds or with a quarter
+// measured bf16 rate: an 8-bit product has twice the rate of a 16-bit one), 125 to 128 among other calls (with the issuers'
+// waits and elections by whole warps 117; then 109 without the multiply-adds or with a quarter
 // of the products, 102 with neither).  8192 x 2048 x 4096 64, 1024 x 4096 x 4096 19 (one tile per SM).  256 experts of
 // 4096 x 4096, 65536 rows with skewed popularity: 1330 to 1520 (640 tiles of 128 rows for 512 that would be full, 10240 with their
 // channels: at the time per tile of the line above 1100; the rest is boxes of rows that another expert follows, stored value by value,
